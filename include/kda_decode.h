@@ -56,11 +56,11 @@ extern "C" {
 /* Rows (tokens) one request may chain in one launch: 1 + up to 7 drafts. */
 #define KDA_MAX_ROWS 8
 
-/* Element type of a state pool. */
+/* Element type of a state pool (or of the tensors of the kda_kv_* functions). */
 typedef enum kda_dtype {
   KDA_F32 = 0,
   KDA_F16 = 1,
-  KDA_BF16 = 2 /* named only to be refused */
+  KDA_BF16 = 2 /* refused for state pools; a type of the kda_kv_* functions' tensors */
 } kda_dtype;
 
 typedef enum kda_status {
@@ -68,7 +68,8 @@ typedef enum kda_status {
   KDA_ERR_NULL = 1,           /* a required pointer is NULL */
   KDA_ERR_DTYPE_REFUSED = 2,  /* bf16 or an unknown dtype */
   KDA_ERR_DTYPE_MISMATCH = 3, /* state_dtype differs from the pool's dtype */
-  KDA_ERR_SHAPE = 4,          /* K or V != 128, H outside [1, 65535], n_slots < 1 */
+  KDA_ERR_SHAPE = 4,          /* K or V != 128, H outside [1, 65535], n_slots < 1;
+                                 or a key/value cache's shape */
   KDA_ERR_ROWS = 5,           /* rows per request outside [1, KDA_MAX_ROWS] */
   KDA_ERR_SLOT = 6,           /* slot id out of range or repeated, or more
                                  rows than slots */
@@ -479,6 +480,162 @@ int kda_prefill(const kda_pool* pool, const int32_t* init_slot_ids,
 int kda_prefill_validate(const kda_pool* pool, const int32_t* init_slot_ids_host,
                          const int32_t* dst_slot_ids_host, const int32_t* cu_seqlens_host,
                          int32_t n_seq, int64_t n_tokens, kda_dtype state_dtype);
+
+/* ------------------------------------------------------------------------
+ * The paged 4-bit key/value cache: what the softmax-attention layers of a
+ * hybrid model keep beside the KDA layers' states.  Its memory is what a
+ * narrower state pool is traded for (ROCm/ATOM PR #2945, Performance: an
+ * fp16 state pool leaves room for 45% more cache blocks).
+ *
+ * Format: OCP microscaling MXFP4.  A value is an E2M1 number (0, 0.5, 1, 1.5,
+ * 2, 3, 4, 6 and their negatives; the code's high bit is the sign) times
+ * 2^(e - 127), with one exponent byte e for 32 channels.  For 32 numbers x,
+ *   e = clamp(floor(log2 max|x|) - 2 + 127, 2, 252)
+ *   code = x / 2^(e - 127) rounded to nearest, ties to even, at most 6.
+ * Exponents 2..252 make every value a normal (or zero) bf16.  4.25 bits a
+ * value: 136 bytes for a token's key and value of 128 channels.
+ */
+
+/*
+ * A cache: device memory holding [n_pages, H] blocks of page_tokens tokens.
+ * A block is P * (D + D / 16) bytes (P = page_tokens):
+ *   key codes       [P][D / 2]    channels 2i (low half) and 2i + 1 of a byte
+ *   value codes     [P][D / 2]
+ *   key exponents   [P][D / 32]
+ *   value exponents [D / 32][P]
+ * page_tokens: 16, 32, 64, 128 or 256; D: 64 or 128; H in [1, 4096]; base
+ * 16-byte aligned.  The caller allocates, owns and frees it; it need not be
+ * cleared.
+ */
+typedef struct kda_kv_pool {
+  void* base;
+  int32_t n_pages;
+  int32_t page_tokens;
+  int32_t H;
+  int32_t D;
+} kda_kv_pool;
+
+/* Bytes of a cache; 0 for a shape that is not supported. */
+size_t kda_kv_pool_bytes(int32_t n_pages, int32_t page_tokens, int32_t H, int32_t D);
+
+/*
+ * The tables every kda_kv_* launch takes (device memory):
+ *  page_table  int32 [n_seq, max_pages]: sequence s keeps position p on page
+ *              page_table[s][p / page_tokens], at token p % page_tokens.
+ *              Entries behind a sequence's last token are not read.
+ *              max_pages * page_tokens < 2^31.
+ *  cu_seqlens  int32 [n_seq + 1], non-decreasing: sequence s owns tokens
+ *              cu_seqlens[s] .. cu_seqlens[s + 1] - 1 of the launch (none, one,
+ *              chained rows or a prompt).  A sequence whose entries are
+ *              out of range is skipped.  Tokens before the first or behind
+ *              the last sequence are left as they were.
+ *  cache_lens  int32 [n_seq]: tokens sequence s had before this launch: its
+ *              i-th token of the launch is at position cache_lens[s] + i.  The
+ *              append and the attention of a step take the same tables.
+ *  n_tokens    rows of the token tensors (< 2^31).
+ * Token tensors are [n_tokens, heads, D] of `dtype` (KDA_F32, KDA_F16 or
+ * KDA_BF16) with D contiguous channels, heads next to each other, and
+ * `..._stride` elements from one token to the next (at least heads * D, a
+ * multiple of 16 bytes), so that slices of one joint projection can be passed
+ * as they lie.  All device pointers 16-byte aligned (the tables: 4-byte).
+ * Nothing is allocated or synchronised; launches are captured into graphs as
+ * they are.  Calls on different streams may overlap as long as they do not
+ * write the same pages, outputs or workspaces.
+ * Checks run in the order: pool NULL, SHAPE (pool), ARG (counts, max_pages),
+ * DTYPE_REFUSED, SHAPE (heads, rot_dim) and ARG (the other numbers), then, for
+ * n_seq and n_tokens > 0 (either 0 is a valid no-op), NULL, ARG (strides),
+ * ALIGN, the workspace.  KDA_ERR_LAUNCH as everywhere.
+ */
+
+/*
+ * kda_kv_append -- stores a step's new keys and values, turning keys (and
+ * queries) by their positions on the way.
+ *
+ *  k, v      [n_tokens, H, D]; q: NULL, or [n_tokens, q_heads, D].
+ *  q_out     the turned queries, [n_tokens, q_heads, D] without gaps, of
+ *            dtype; may be q itself where q has no gaps either.  Not
+ *            touched with q_heads == 0.
+ *  cos, sin  device fp32 [n_positions, rot_dim / 2], row p for position p; the
+ *            first rot_dim channels (a multiple of 16, 0 for no rotation) of
+ *            every key and query are turned: pair (a, b) of table column c
+ *            becomes (a cos - b sin, b cos + a sin), where (a, b) are channels
+ *            (c, c + rot_dim / 2), or with interleaved = 1 (2c, 2c + 1).
+ * Queries are turned in fp32 and rounded once; keys are turned and rounded
+ * in fp64, so a code next to a rounding border is the definition's.
+ * A key or value row (one token, one cached head) that holds a NaN or an
+ * infinity poisons that token for that head: its key exponents become 255 (its
+ * key reads back as NaN) and its value zeros; rows that see the token get NaN
+ * from the attention in that head's outputs, other rows are not changed.
+ * A token whose position has no valid page, or lies behind the tables, is not
+ * stored, and its q_out rows are NaN.  Two tokens of one launch must not have
+ * the same place (kda_kv_validate checks host copies).
+ */
+int kda_kv_append(const kda_kv_pool* kv, const int32_t* page_table, int32_t max_pages,
+                  const int32_t* cu_seqlens, const int32_t* cache_lens, const void* k, const void* v,
+                  int64_t k_stride, int64_t v_stride, const void* q, int64_t q_stride, void* q_out,
+                  const float* cos, const float* sin, int32_t n_positions, int32_t rot_dim,
+                  int32_t interleaved, int32_t n_seq, int64_t n_tokens, int32_t q_heads,
+                  kda_dtype dtype, void* stream);
+
+/*
+ * kda_kv_read -- the values the cache holds: token i of sequence s gets those
+ * of position first[s] + i (moving a prefix to another cache, inspection).
+ * k_out, v_out: [n_tokens, H, D] of dtype with strides as above; one of them
+ * may be NULL.  Exact in fp32 and bf16; fp16 rounds to nearest even (values
+ * from 65520 are infinite there, below 2^-24 zero or rounded).  Tokens without
+ * a valid page read as NaN.
+ */
+int kda_kv_read(const kda_kv_pool* kv, const int32_t* page_table, int32_t max_pages,
+                const int32_t* cu_seqlens, const int32_t* first, void* k_out, void* v_out,
+                int64_t k_stride, int64_t v_stride, int32_t n_seq, int64_t n_tokens, kda_dtype dtype,
+                void* stream);
+
+/*
+ * kda_kv_attend -- attention of a launch's rows over the cache, causal: the
+ * row at position p sees the sequence's positions 0..p (its own included: the
+ * step's tokens are appended first).  Query head i reads cached head
+ * i / (q_heads / H).
+ *   out = sum_t softmax_t(scale * q . k_t) v_t
+ *  q               [n_tokens, q_heads, D]; out: the same without gaps.
+ *  max_rows        the longest sequence's rows in this launch, max_kv_len its
+ *                  tokens including them (0: all that max_pages covers).  Both
+ *                  only lay out the launch: longer sequences are taken as
+ *                  well, more slowly.
+ *  q_heads         a multiple of H; n_tokens * q_heads / H < 2^30.
+ *  scale           finite.
+ *  workspace       kda_kv_attend_workspace() bytes for the same arguments (may
+ *                  be NULL for 0), 16-byte aligned, free for use again once
+ *                  the launch has run.  Calls that may overlap need their own.
+ * Products are exact: q enters the matrix cores as 3 (fp32), 2 (fp16) or 1
+ * bf16 numbers that add up to it; scores, weights, their sums and the output's
+ * sums are fp32.  The order of the sums depends on the launch's sizes, not on
+ * timing: equal calls give equal bits.
+ * A row that sees a poisoned token or a page that does not exist is NaN in
+ * that head; the rows of a sequence with a negative length or one that
+ * max_pages cannot hold are NaN.  Errors: KDA_ERR_NULL and KDA_ERR_ARG also for
+ * a workspace that is missing or too small.
+ */
+int kda_kv_attend(const kda_kv_pool* kv, const int32_t* page_table, int32_t max_pages,
+                  const int32_t* cu_seqlens, const int32_t* cache_lens, const void* q, int64_t q_stride,
+                  void* out, int32_t n_seq, int64_t n_tokens, int32_t max_rows, int64_t max_kv_len,
+                  int32_t q_heads, kda_dtype dtype, float scale, void* workspace, size_t workspace_bytes,
+                  void* stream);
+
+/* Bytes of workspace kda_kv_attend needs for these arguments (0: none, or
+ * arguments it refuses). */
+size_t kda_kv_attend_workspace(const kda_kv_pool* kv, int32_t max_pages, int32_t n_seq, int64_t n_tokens,
+                               int32_t max_rows, int64_t max_kv_len, int32_t q_heads, kda_dtype dtype);
+
+/*
+ * kda_kv_validate -- host-side check of a step's tables (host copies): ARG for
+ * cu_seqlens that descend or leave [0, n_tokens], a negative length or one
+ * that max_pages cannot hold; SLOT for a page that is out of range, or one that
+ * takes new tokens and appears twice among the pages in use (pages before a
+ * sequence's first new token may be shared).  CPU only.
+ */
+int kda_kv_validate(const kda_kv_pool* kv, const int32_t* page_table_host, int32_t max_pages,
+                    const int32_t* cu_seqlens_host, const int32_t* cache_lens_host, int32_t n_seq,
+                    int64_t n_tokens);
 
 /* Launch shape kda_decode_step uses for a given problem (host only). */
 typedef struct kda_launch_desc {

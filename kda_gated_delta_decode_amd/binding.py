@@ -58,6 +58,11 @@ class kda_conv_pool(ctypes.Structure):
     _fields_ = [("base", ctypes.c_void_p), ("n_slots", ctypes.c_int32), ("H", ctypes.c_int32)]
 
 
+class kda_kv_pool(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("n_pages", ctypes.c_int32), ("page_tokens", ctypes.c_int32),
+                ("H", ctypes.c_int32), ("D", ctypes.c_int32)]
+
+
 class kda_launch_opts(ctypes.Structure):
     _fields_ = [("waves_per_tile", ctypes.c_int32), ("bv", ctypes.c_int32),
                 ("block_rows", ctypes.c_int32), ("rows_layout", ctypes.c_int32),
@@ -84,6 +89,7 @@ class KdaError(RuntimeError):
 # The C symbols and their signatures, as include/kda_decode.h declares them.
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
+_I64 = ctypes.c_int64
 SIGNATURES = {
     "kda_decode_step": (ctypes.c_int, [ctypes.POINTER(kda_pool), _P, _P, _P, _P, _P, _P, _P,
                                        _I32, _I32, ctypes.c_int, ctypes.c_float, _P]),
@@ -119,6 +125,17 @@ SIGNATURES = {
     "kda_tile_probe": (ctypes.c_int, [ctypes.POINTER(kda_pool), _P, _I32, ctypes.c_int, _P]),
     "kda_rows_probe": (ctypes.c_int, [ctypes.POINTER(kda_pool), _P, _P, _I32, _I32, _I32, _I32, ctypes.c_int,
                                       _P]),
+    "kda_kv_pool_bytes": (ctypes.c_size_t, [_I32, _I32, _I32, _I32]),
+    "kda_kv_append": (ctypes.c_int, [ctypes.POINTER(kda_kv_pool), _P, _I32, _P, _P, _P, _P, _I64, _I64, _P,
+                                     _I64, _P, _P, _P, _I32, _I32, _I32, _I32, _I64, _I32, ctypes.c_int, _P]),
+    "kda_kv_read": (ctypes.c_int, [ctypes.POINTER(kda_kv_pool), _P, _I32, _P, _P, _P, _P, _I64, _I64, _I32,
+                                   _I64, ctypes.c_int, _P]),
+    "kda_kv_attend": (ctypes.c_int, [ctypes.POINTER(kda_kv_pool), _P, _I32, _P, _P, _P, _I64, _P, _I32, _I64,
+                                     _I32, _I64, _I32, ctypes.c_int, ctypes.c_float, _P, ctypes.c_size_t,
+                                     _P]),
+    "kda_kv_attend_workspace": (ctypes.c_size_t, [ctypes.POINTER(kda_kv_pool), _I32, _I32, _I64, _I32, _I64,
+                                                  _I32, ctypes.c_int]),
+    "kda_kv_validate": (ctypes.c_int, [ctypes.POINTER(kda_kv_pool), _P, _I32, _P, _P, _I32, _I64]),
     "kda_strerror": (ctypes.c_char_p, [ctypes.c_int]),
     "kda_abi_version": (ctypes.c_int, []),
 }
@@ -531,6 +548,203 @@ def kda_rows_probe(pool, slot_ids, n_rows: int, init_slot_ids=None, tile_cols: i
     _check(library().kda_rows_probe(ctypes.byref(P), _dev(slot_ids, "slot_ids", torch.int32, dv),
                                     _dev(init_slot_ids, "init_slot_ids", torch.int32, dv), n_req, n_rows,
                                     int(tile_cols), int(waves), P.dtype, _stream_ptr(stream)), "kda_rows_probe")
+
+
+# ---------------------------------------------------------------------------
+# the paged 4-bit key/value cache
+# ---------------------------------------------------------------------------
+
+def kv_pool_shape(n_pages: int, H: int, page_tokens: int, D: int):
+    """Shape of the uint8 tensor that holds a cache: [n_pages, H, page_tokens,
+    17 D / 16].  The last two axes together are one block's bytes (codes, then
+    exponents; see kda_kv_pool in include/kda_decode.h)."""
+    return (int(n_pages), int(H), int(page_tokens), int(D) * 17 // 16)
+
+
+def make_kv_pool(pool) -> kda_kv_pool:
+    """kda_kv_pool describing a contiguous uint8 GPU tensor of kv_pool_shape."""
+    import torch
+    _on_gpu(pool, "pool")
+    if pool.dtype != torch.uint8 or pool.dim() != 4 or not pool.is_contiguous():
+        raise ValueError("a cache must be a contiguous uint8 tensor [n_pages, H, page_tokens, 17 D / 16]")
+    n_pages, H, P, width = pool.shape
+    if width % 17:
+        raise ValueError("a cache's last axis must be 17 D / 16 bytes, got %d" % width)
+    return kda_kv_pool(pool.data_ptr(), n_pages, P, H, width // 17 * 16)
+
+
+def _rows(t, name, pool, heads, D, dtype, n_tokens):
+    """Address and token stride of a token tensor [n_tokens, heads, D] whose
+    heads and channels lie without gaps."""
+    _on_gpu(t, name)
+    if t.device != pool.device:
+        raise TypeError("%s is on %s, the pool on %s" % (name, t.device, pool.device))
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != (n_tokens, heads, D):
+        raise ValueError("%s must be [%d, %d, %d], got %s" % (name, n_tokens, heads, D, list(t.shape)))
+    stride = t.stride()
+    if n_tokens and (stride[2] != 1 or (heads > 1 and stride[1] != D)):
+        raise ValueError("%s must have contiguous heads and channels" % name)
+    return t.data_ptr(), stride[0] if n_tokens > 1 else heads * D
+
+
+def _kv_tables(pool, page_table, cu_seqlens, lens):
+    """The checked tables of a cache launch: their addresses, n_seq, max_pages."""
+    import torch
+    for t, name, dim in ((page_table, "page_table", 2), (cu_seqlens, "cu_seqlens", 1), (lens, "cache_lens", 1)):
+        _on_gpu(t, name)
+        if t.device != pool.device:
+            raise TypeError("%s is on %s, the pool on %s" % (name, t.device, pool.device))
+        if t.dtype != torch.int32 or t.dim() != dim or not t.is_contiguous():
+            raise TypeError("%s must be a contiguous int32 tensor of %d dimensions" % (name, dim))
+    n_seq, max_pages = page_table.shape
+    if lens.numel() != n_seq or cu_seqlens.numel() != n_seq + 1:
+        raise ValueError("page_table has %d rows: cu_seqlens needs one entry more, cache_lens as many" % n_seq)
+    return page_table.data_ptr(), max_pages, cu_seqlens.data_ptr(), lens.data_ptr(), n_seq
+
+
+def _kv_stream(pool, stream):
+    """The stream's address: by default the current one of the pool's device."""
+    import torch
+    if stream is None:
+        return torch.cuda.current_stream(pool.device).cuda_stream
+    if isinstance(stream, int):
+        return stream
+    if stream.device != pool.device:
+        raise ValueError("the stream is on %s, the pool on %s" % (stream.device, pool.device))
+    return stream.cuda_stream
+
+
+def _kv_call(name, pool, *args):
+    """Calls the library with the pool's device as the current one."""
+    import torch
+    fn = getattr(library(), name)
+    if torch.cuda.current_device() == pool.device.index:
+        rc = fn(*args)
+    else:
+        with torch.cuda.device(pool.device):
+            rc = fn(*args)
+    _check(rc, name)
+
+
+def kda_kv_append(pool, page_table, cu_seqlens, cache_lens, k, v, q=None, q_out=None, cos=None, sin=None,
+                  interleaved: bool = False, stream=None) -> None:
+    """Stores a step's keys and values in the cache, turned by their positions
+    (see kda_kv_append in include/kda_decode.h).
+
+    pool: uint8 tensor of kv_pool_shape; page_table: int32 [n_seq, max_pages];
+    cu_seqlens: int32 [n_seq + 1]; cache_lens: int32 [n_seq]; k, v: [T, H, D] of
+    float32, float16 or bfloat16, slices of a joint projection allowed; q: None
+    or [T, q_heads, D] of the same type, turned into q_out (contiguous); cos,
+    sin: None, or float32 [n_positions, rot_dim / 2]."""
+    import torch
+    P = make_kv_pool(pool)
+    tables = _kv_tables(pool, page_table, cu_seqlens, cache_lens)
+    T, dtype = k.shape[0], k.dtype
+    kp, ks = _rows(k, "k", pool, P.H, P.D, dtype, T)
+    vp, vs = _rows(v, "v", pool, P.H, P.D, dtype, T)
+    qp = qs = qo = heads = 0
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    if q is not None:
+        heads = q.shape[1] if q.dim() == 3 else -1
+        qp, qs = _rows(q, "q", pool, heads, P.D, dtype, T)
+        qo, _ = _rows(q_out, "q_out", pool, heads, P.D, dtype, T)
+        if not q_out.is_contiguous():
+            raise ValueError("q_out must be contiguous")
+    cp = sp = positions = half = 0
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin go together")
+    if cos is not None:
+        if cos.dim() != 2 or cos.shape != sin.shape:
+            raise ValueError("cos and sin must be [n_positions, rot_dim / 2], both")
+        positions, half = cos.shape
+        cp, sp = (_dev(t, n, torch.float32, pool.device) for t, n in ((cos, "cos"), (sin, "sin")))
+    _kv_call("kda_kv_append", pool, ctypes.byref(P), tables[0], tables[1], tables[2], tables[3], kp, vp, ks, vs, qp, qs,
+             qo, cp, sp, positions, 2 * half, int(interleaved), tables[4], T, heads, dtype_code(dtype),
+             _kv_stream(pool, stream))
+
+
+def kda_kv_read(pool, page_table, cu_seqlens, first, k_out=None, v_out=None, stream=None) -> None:
+    """Reads cached keys and values back (see kda_kv_read in
+    include/kda_decode.h): token i of sequence s gets position first[s] + i.
+    k_out, v_out: [T, H, D] of one floating type; either may be None."""
+    P = make_kv_pool(pool)
+    tables = _kv_tables(pool, page_table, cu_seqlens, first)
+    some = k_out if k_out is not None else v_out
+    if some is None:
+        raise ValueError("nothing to read into: k_out and v_out are both None")
+    T, dtype = some.shape[0], some.dtype
+    kp, ks = (0, 0) if k_out is None else _rows(k_out, "k_out", pool, P.H, P.D, dtype, T)
+    vp, vs = (0, 0) if v_out is None else _rows(v_out, "v_out", pool, P.H, P.D, dtype, T)
+    _kv_call("kda_kv_read", pool, ctypes.byref(P), tables[0], tables[1], tables[2], tables[3], kp, vp, ks, vs, tables[4],
+             T, dtype_code(dtype), _kv_stream(pool, stream))
+
+
+def kda_kv_attend_workspace(pool, page_table, n_tokens: int, q_heads: int, max_rows: int, max_kv_len: int = 0,
+                            dtype="f32") -> int:
+    """Bytes of workspace kda_kv_attend needs for a launch of these sizes."""
+    P = make_kv_pool(pool)
+    return int(library().kda_kv_attend_workspace(ctypes.byref(P), page_table.shape[1], page_table.shape[0],
+                                                 int(n_tokens), int(max_rows), int(max_kv_len), int(q_heads),
+                                                 _dtype_arg(dtype)))
+
+
+def kda_kv_attend(pool, page_table, cu_seqlens, cache_lens, q, out, max_rows: int | None = None,
+                  max_kv_len: int = 0, scale: float | None = None, workspace=None, stream=None) -> None:
+    """Causal attention of a step's rows over the cache (see kda_kv_attend in
+    include/kda_decode.h).
+
+    q: [T, q_heads, D] of float32, float16 or bfloat16 (token stride free);
+    out: the same, contiguous.  max_rows: the longest sequence's rows in this
+    launch (default T); max_kv_len: its tokens including them (default: what
+    page_table covers): they lay out the launch, results hold for any.
+    workspace: a contiguous uint8 tensor of kda_kv_attend_workspace bytes, or
+    None to take one from torch's allocator on the launch's stream."""
+    import torch
+    P = make_kv_pool(pool)
+    tables = _kv_tables(pool, page_table, cu_seqlens, cache_lens)
+    if q.dim() != 3:
+        raise ValueError("q must be [T, q_heads, D], got %s" % list(q.shape))
+    T, heads, dtype = q.shape[0], q.shape[1], q.dtype
+    qp, qs = _rows(q, "q", pool, heads, P.D, dtype, T)
+    op, _ = _rows(out, "out", pool, heads, P.D, dtype, T)
+    if not out.is_contiguous():
+        raise ValueError("out must be contiguous")
+    rows, code = T if max_rows is None else int(max_rows), dtype_code(dtype)
+    st = _kv_stream(pool, stream)
+    if workspace is None:
+        n = library().kda_kv_attend_workspace(ctypes.byref(P), tables[1], tables[4], T, rows, int(max_kv_len), heads,
+                                              code)
+        if n:
+            current = torch.cuda.current_stream(pool.device)
+            if st == current.cuda_stream:
+                workspace = torch.empty(n, dtype=torch.uint8, device=pool.device)
+            else:
+                # memory of that stream: the allocator hands it on in its order
+                on = torch.cuda.ExternalStream(st, device=pool.device) if st else torch.cuda.default_stream(pool.device)
+                with torch.cuda.stream(on):
+                    workspace = torch.empty(n, dtype=torch.uint8, device=pool.device)
+    wp, wn = (0, 0) if workspace is None else (_dev(workspace, "workspace", torch.uint8, pool.device),
+                                               workspace.numel())
+    _kv_call("kda_kv_attend", pool, ctypes.byref(P), tables[0], tables[1], tables[2], tables[3], qp, qs, op, tables[4], T,
+             rows, int(max_kv_len), heads, code, 1.0 / math.sqrt(P.D) if scale is None else float(scale), wp, wn, st)
+
+
+def kda_kv_validate(pool_desc: kda_kv_pool, page_table_host, cu_seqlens_host, cache_lens_host, n_tokens: int) -> int:
+    """Host-side check of a step's cache tables; returns the kda_status code."""
+    table = np.ascontiguousarray(page_table_host, dtype=np.int32)
+    cu = np.ascontiguousarray(cu_seqlens_host, dtype=np.int32)
+    lens = np.ascontiguousarray(cache_lens_host, dtype=np.int32)
+    if table.ndim != 2 or cu.size != table.shape[0] + 1 or lens.size != table.shape[0]:
+        raise ValueError("page_table [n_seq, max_pages], cu_seqlens [n_seq + 1], cache_lens [n_seq]")
+    return int(library().kda_kv_validate(ctypes.byref(pool_desc), table.ctypes.data, table.shape[1], cu.ctypes.data,
+                                         lens.ctypes.data, table.shape[0], int(n_tokens)))
+
+
+def kda_kv_pool_bytes(n_pages: int, page_tokens: int, H: int, D: int) -> int:
+    return int(library().kda_kv_pool_bytes(n_pages, page_tokens, H, D))
 
 
 def kda_strerror(code: int) -> str:

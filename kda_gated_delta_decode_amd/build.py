@@ -4,8 +4,9 @@
 
 Compiles csrc/kda_decode.hip (decode kernels and launch entry points),
 csrc/kda_prefill.hip (the chunked prefill), csrc/kda_probe.hip (bandwidth
-probes) and csrc/kda_host.cpp (validation, addressing, sizing) with hipcc into
-kda_gated_delta_decode_amd/libkda_decode.so.  Flags:
+probes), csrc/kda_kv.hip (the paged 4-bit key/value cache) and their host
+halves csrc/kda_host.cpp and csrc/kda_kv_host.cpp (validation, addressing,
+sizing) with hipcc into kda_gated_delta_decode_amd/libkda_decode.so.  Flags:
   --offload-arch=gfx950          MI355X only
   -ffp-contract=off              no implicit multiply-add fusion: every fused
                                  multiply-add in the kernels is an explicit
@@ -28,7 +29,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libkda_decode.so")
 SOURCES = [os.path.join(CSRC, "kda_decode.hip"), os.path.join(CSRC, "kda_prefill.hip"),
-           os.path.join(CSRC, "kda_probe.hip"), os.path.join(CSRC, "kda_host.cpp")]
+           os.path.join(CSRC, "kda_probe.hip"), os.path.join(CSRC, "kda_kv.hip"),
+           os.path.join(CSRC, "kda_host.cpp"), os.path.join(CSRC, "kda_kv_host.cpp")]
 ARCH = "gfx950"
 
 

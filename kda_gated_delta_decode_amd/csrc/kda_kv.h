@@ -1,0 +1,91 @@
+// kda_kv.h -- the paged 4-bit key/value cache: block layout, argument structs
+// and launch-shape rules shared by the host checks (kda_kv_host.cpp) and the
+// gfx950 kernels (kda_kv.hip).  Internal header.
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "kda_decode.h"
+#include "kda_launch.h"
+
+namespace kda {
+
+constexpr int kKvGroup = 32;      // channels that share one exponent byte
+constexpr int kKvMinExp = 2;      // exponent bytes stored: every value a normal bf16,
+constexpr int kKvMaxExp = 252;    //   and 6 * 2^(252 - 127) finite
+constexpr int kKvPoison = 255;    // key exponent of a token whose key or value was not finite
+constexpr int kKvMaxHeads = 4096;
+
+// Bytes of one (page, head) block of P tokens of D channels: key codes
+// [P][D/2], value codes [P][D/2], key exponents [P][D/32], value exponents
+// [D/32][P].
+KDA_HD constexpr int kv_block_bytes(int P, int D) { return P * D + P * D / 16; }
+KDA_HD constexpr int kv_value_codes(int P, int D) { return P * D / 2; }
+KDA_HD constexpr int kv_key_exps(int P, int D) { return P * D; }
+KDA_HD constexpr int kv_value_exps(int P, int D) { return P * D + P * D / kKvGroup; }
+
+// The cache and the tables that place a launch's tokens in it.
+struct KvTables {
+  uint8_t* base;
+  const int32_t* page_table;  // [n_seq][max_pages]
+  const int32_t* cu;          // [n_seq + 1]
+  const int32_t* past;        // [n_seq]: tokens before the launch's first one
+  int64_t page_bytes;         // all heads of one page
+  int64_t n_tokens;
+  int32_t n_pages, max_pages, n_seq;
+  int32_t H;                  // cached heads
+  int32_t log_p;              // log2 of tokens a page
+  int32_t P;
+};
+
+struct KvAppendArgs {
+  KvTables t;
+  const void* q;
+  const void* k;
+  const void* v;
+  void* q_out;
+  const float* cos;
+  const float* sin;
+  int64_t q_stride, k_stride, v_stride;  // elements between tokens
+  int32_t n_positions, half, interleaved, q_heads;
+  int32_t units, units_per_block, unit_blocks;  // units: cached heads, then query heads
+};
+
+struct KvReadArgs {
+  KvTables t;
+  void* k_out;
+  void* v_out;
+  int64_t k_stride, v_stride;
+  int32_t heads_per_block, head_blocks;
+};
+
+struct KvAttendArgs {
+  KvTables t;
+  const void* q;
+  void* out;
+  float* part;     // workspace: [n_splits][n_tokens * q_heads][D] sums, then
+  float* part_ml;  //   [n_splits][n_tokens * q_heads][2] maxima and sums of weights
+  int64_t q_stride;
+  int32_t q_heads, group;       // group: query heads of one cached head
+  int32_t chunk, n_splits;      // tokens a split covers
+  int32_t row_tiles;            // tiles of rows a sequence is given blocks for
+  float scale;                  // |scale| * log2(e)
+  int32_t negate;               // scale < 0
+};
+
+// How kda_kv_attend takes a launch.
+struct KvPlan {
+  int32_t tile_rows;  // rows (tokens x query heads of one cached head) a workgroup takes
+  int32_t row_tiles;
+  int32_t chunk;
+  int32_t n_splits;
+};
+
+KvPlan kv_plan(int32_t H, int32_t D, int32_t n_seq, int64_t n_tokens, int32_t max_rows,
+               int64_t max_kv_len, int32_t q_heads, kda_dtype dtype);
+
+// Checks shared by the entry points, in the documented order.
+int kv_check(const kda_kv_pool* kv, int32_t max_pages, int32_t n_seq, int64_t n_tokens);
+
+}  // namespace kda

@@ -1,0 +1,970 @@
+// kda_kv.hip -- the paged 4-bit key/value cache on gfx950: appending keys and
+// values with the position rotation, reading them back, and attention.
+//
+// The cache's format is OCP microscaling MXFP4: E2M1 codes with one E8M0
+// exponent for 32 channels, 4.25 bits a value.  Two properties carry the
+// kernels.  v_cvt_scalef32_pk_bf16_fp4 turns two codes and their exponent
+// into two bf16 in one instruction, and every such value is exact in bf16
+// (exponent bytes 2..252), so the matrix cores take the cache without a
+// rounding; queries and weights enter as 1..3 bf16 pieces whose sum is the
+// fp32, fp16 or bf16 number.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <type_traits>
+
+#include "kda_decode.h"
+#include "kda_device.h"
+#include "kda_kv.h"
+
+namespace kda {
+namespace {
+
+using bf2 = __bf16 __attribute__((ext_vector_type(2)));
+using bf8 = __bf16 __attribute__((ext_vector_type(8)));
+using u2 = uint32_t __attribute__((ext_vector_type(2)));
+using u4 = uint32_t __attribute__((ext_vector_type(4)));
+
+// Loads of uniform addresses through the scalar cache, apart from the vector
+// loads' counter: a page id can be waited for while cache rows are in flight.
+using const_i32 = const int32_t __attribute__((address_space(4)));
+
+template <int DT>
+constexpr int elem_bytes() { return DT == KDA_F32 ? 4 : 2; }
+
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ uint32_t bits(float x) { return __float_as_uint(x); }
+// the upper (lower) halves of a and b as one register, a's first
+__device__ __forceinline__ uint32_t pack_hi(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302); }
+__device__ __forceinline__ uint32_t pack_lo(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x05040100); }
+// two E2M1 codes (byte SEL of c) times 2^(e - 127), scale = e << 23, as two bf16
+template <int SEL>
+__device__ __forceinline__ uint32_t dequant2(uint32_t c, float scale) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, SEL));
+}
+__device__ __forceinline__ float exp_scale(uint32_t e) { return __uint_as_float(e << 23); }
+
+template <int DT>
+__device__ __forceinline__ void load8(const void* p, int64_t at, float (&x)[8]) {
+  if constexpr (DT == KDA_F32) {
+    const f4* s = reinterpret_cast<const f4*>(static_cast<const float*>(p) + at);
+    const f4 a = s[0], b = s[1];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = a[e], x[e + 4] = b[e];
+  } else if constexpr (DT == KDA_F16) {
+    const h8 a = *reinterpret_cast<const h8*>(static_cast<const _Float16*>(p) + at);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = static_cast<float>(a[e]);
+  } else {
+    const u4 a = *reinterpret_cast<const u4*>(static_cast<const uint16_t*>(p) + at);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[2 * e] = __uint_as_float(a[e] << 16);
+      x[2 * e + 1] = __uint_as_float(a[e] & 0xFFFF0000u);
+    }
+  }
+}
+
+// rounds to nearest even, once
+template <int DT>
+__device__ __forceinline__ void store8(void* p, int64_t at, const float (&x)[8]) {
+  if constexpr (DT == KDA_F32) {
+    f4* d = reinterpret_cast<f4*>(static_cast<float*>(p) + at);
+    d[0] = f4{x[0], x[1], x[2], x[3]};
+    d[1] = f4{x[4], x[5], x[6], x[7]};
+  } else if constexpr (DT == KDA_F16) {
+    h8 a;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) a[e] = static_cast<_Float16>(x[e]);
+    *reinterpret_cast<h8*>(static_cast<_Float16*>(p) + at) = a;
+  } else {
+    bf8 a;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) a[e] = static_cast<__bf16>(x[e]);
+    *reinterpret_cast<bf8*>(static_cast<__bf16*>(p) + at) = a;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Which sequence a token belongs to, and where the cache keeps it
+// ---------------------------------------------------------------------------
+
+enum Place { kOutside = 0, kBad = 1, kPlaced = 2 };
+
+struct TokenPlace {
+  int what;          // a Place
+  int32_t pos;       // position in its sequence
+  uint8_t* block;    // head 0's block of its page
+  int32_t row;       // its token row there
+};
+
+// W lanes (one token each group of W) search cu together: each round splits
+// the range in W and keeps the part that holds the token, so 16 lanes need
+// one round of loads for up to 16 sequences and two for 256.
+template <int W>
+__device__ __forceinline__ TokenPlace find_token(const KvTables& t, int64_t token, int n_positions) {
+  const int lane = threadIdx.x % 64, li = lane % W;
+  const uint64_t mask = ((1ull << W) - 1) << (lane - li);
+  TokenPlace r{kOutside, 0, t.base, 0};
+  int lo = 0, hi = t.n_seq;
+  if (token < t.n_tokens) {
+    while (hi - lo > 1) {
+      const int step = (hi - lo + W - 1) / W;
+      const int i = lo + step * (li + 1);
+      const bool before = i < hi && t.cu[i] <= token;
+      lo += step * __popcll(__ballot(before) & mask);
+      hi = lo + step < hi ? lo + step : hi;
+    }
+    const int64_t first = t.cu[lo], end = t.cu[lo + 1], past = t.past[lo];
+    if (first >= 0 && token >= first && token < end) {
+      const int64_t pos = past + (token - first);
+      r.what = kBad;
+      if (past >= 0 && pos < n_positions && (pos >> t.log_p) < t.max_pages) {
+        const int32_t page = t.page_table[static_cast<int64_t>(lo) * t.max_pages + (pos >> t.log_p)];
+        if (page >= 0 && page < t.n_pages) {
+          r.what = kPlaced;
+          r.pos = static_cast<int32_t>(pos);
+          r.block = t.base + page * t.page_bytes;
+          r.row = static_cast<int32_t>(pos) & (t.P - 1);
+        }
+      }
+    }
+  }
+  return r;
+}
+
+// ---------------------------------------------------------------------------
+// Append
+// ---------------------------------------------------------------------------
+
+// maximum over the 4 lanes that hold one exponent's 32 channels
+__device__ __forceinline__ int quad_max(int x) {
+  int y = __builtin_amdgcn_mov_dpp(x, kDppQuadXor1, 0xF, 0xF, true);
+  x = x > y ? x : y;
+  y = __builtin_amdgcn_mov_dpp(x, kDppQuadXor2, 0xF, 0xF, true);
+  return x > y ? x : y;
+}
+
+__device__ __forceinline__ int clamp_exp(int e) { return e < kKvMinExp ? kKvMinExp : e > kKvMaxExp ? kKvMaxExp : e; }
+
+// 8 values already divided by their power of two: rounded to E2M1 (nearest,
+// ties to even, saturating at 6)
+__device__ __forceinline__ uint32_t quant8(const float (&a)[8]) {
+  uint32_t c = 0;
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, a[0], a[1], 1.0f, 0);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, a[2], a[3], 1.0f, 1);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, a[4], a[5], 1.0f, 2);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, a[6], a[7], 1.0f, 3);
+  return c;
+}
+
+// A double as the fp32 of 20 mantissa bits whose lowest of 23 is set when any
+// later bit was: E2M1's rounding borders have at most two mantissa bits, so
+// rounding this number gives what rounding the double would.
+__device__ __forceinline__ float sticky_float(double d) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, d);
+  const uint32_t hi = static_cast<uint32_t>(b >> 32), lo = static_cast<uint32_t>(b);
+  const uint32_t mag = hi & 0x7FFFFFFFu;
+  const uint32_t f = ((mag - (896u << 20)) << 3) | (lo != 0 ? 1u : 0u);
+  return __uint_as_float((mag < (897u << 20) ? 0u : f) | (hi & 0x80000000u));
+}
+
+// One group of D / 8 lanes takes one token and walks over its units (cached
+// heads, then query heads), 8 channels a lane: the token's place and its
+// angles are looked up once.  Neighbouring groups take neighbouring tokens of
+// the same unit, so a wave writes 256 contiguous bytes of codes.
+template <int DT, int D>
+__global__ __launch_bounds__(256) void kda_kv_append_kernel(KvAppendArgs a) {
+  constexpr int W = D / 8;
+  const int li = threadIdx.x % W;
+  const int64_t tile = blockIdx.x / a.unit_blocks;
+  const int ub = blockIdx.x % a.unit_blocks;
+  const int64_t token = tile * (256 / W) + threadIdx.x / W;
+  const int u0 = ub * a.units_per_block;
+  const int u1 = u0 + a.units_per_block < a.units ? u0 + a.units_per_block : a.units;
+  const TokenPlace at = find_token<W>(a.t, token, a.n_positions);
+  if (at.what == kOutside) return;
+
+  // out[e] = x[e] * cs[e] + partner[e] * sn[e]
+  const int c0 = 8 * li;
+  const bool turned = c0 < 2 * a.half;
+  float cs[8], sn[8];
+  int partner = 0;  // channels to the partner's eight
+  if (turned && at.what == kPlaced) {
+    if (a.interleaved) {
+      const f4 c = *reinterpret_cast<const f4*>(a.cos + static_cast<int64_t>(at.pos) * a.half + c0 / 2);
+      const f4 s = *reinterpret_cast<const f4*>(a.sin + static_cast<int64_t>(at.pos) * a.half + c0 / 2);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) cs[e] = c[e / 2], sn[e] = e % 2 ? s[e / 2] : -s[e / 2];
+    } else {
+      const bool first = c0 < a.half;
+      const int64_t row = static_cast<int64_t>(at.pos) * a.half + (first ? c0 : c0 - a.half);
+      load8<KDA_F32>(a.cos, row, cs);
+      load8<KDA_F32>(a.sin, row, sn);
+      partner = first ? a.half : -a.half;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sn[e] = first ? -sn[e] : sn[e];
+    }
+  }
+  const int block_bytes = kv_block_bytes(a.t.P, D);
+  const int lane = threadIdx.x % 64;
+  const uint64_t mine = ((1ull << W) - 1) << (lane - li);
+
+  for (int u = u0; u < u1; ++u) {
+    if (u < a.t.H) {
+      if (at.what != kPlaced) continue;
+      float x[8], v[8];
+      const int64_t kat = token * a.k_stride + u * D + c0;
+      load8<DT>(a.k, kat, x);
+      load8<DT>(a.v, token * a.v_stride + u * D + c0, v);
+      // the keys' rotation and scaling in 64 bits: a code next to a rounding
+      // border comes out as the definition has it
+      double y[8];
+      if (turned) {
+        float p[8];
+        if (a.interleaved) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) p[e] = x[e ^ 1];
+        } else {
+          load8<DT>(a.k, kat + partner, p);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          y[e] = static_cast<double>(x[e]) * static_cast<double>(cs[e]) +
+                 static_cast<double>(p[e]) * static_cast<double>(sn[e]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = static_cast<double>(x[e]);
+      }
+      int ek = 0, ev = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int k = static_cast<int>(__builtin_bit_cast(uint64_t, y[e]) >> 52) & 0x7FF;
+        const int w = static_cast<int>(bits(v[e]) >> 23) & 0xFF;
+        ek = ek > k ? ek : k;
+        ev = ev > w ? ev : w;
+      }
+      ek = quad_max(ek);
+      ev = quad_max(ev);
+      const bool poison = (__ballot(ek == 0x7FF || ev == 0xFF) & mine) != 0;
+      const int kb = clamp_exp(ek - 1023 - 2 + 127), vb = clamp_exp(ev - 2);
+      const double km = __builtin_bit_cast(double, static_cast<uint64_t>(1023 + 127 - kb) << 52);
+      const float vm = exp_scale(254 - vb);
+      float ka[8], va[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        ka[e] = sticky_float(y[e] * km);
+        va[e] = v[e] * vm;
+      }
+      uint8_t* block = at.block + static_cast<int64_t>(u) * block_bytes;
+      const int code = at.row * (D / 2) + 4 * li;
+      *reinterpret_cast<uint32_t*>(block + code) = poison ? 0 : quant8(ka);
+      *reinterpret_cast<uint32_t*>(block + kv_value_codes(a.t.P, D) + code) = poison ? 0 : quant8(va);
+      if (li % 4 == 0) {
+        block[kv_key_exps(a.t.P, D) + at.row * (D / kKvGroup) + li / 4] =
+            static_cast<uint8_t>(poison ? kKvPoison : kb);
+        block[kv_value_exps(a.t.P, D) + (li / 4) * a.t.P + at.row] = static_cast<uint8_t>(poison ? kKvMinExp : vb);
+      }
+    } else {
+      const int h = u - a.t.H;
+      float x[8], o[8];
+      const int64_t qat = token * a.q_stride + h * D + c0;
+      load8<DT>(a.q, qat, x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = x[e];
+      if (turned && at.what == kPlaced) {
+        float p[8];
+        if (a.interleaved) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) p[e] = x[e ^ 1];
+        } else {
+          load8<DT>(a.q, qat + partner, p);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = x[e] * cs[e] + p[e] * sn[e];
+      }
+      if (at.what == kBad) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = __builtin_nanf("");
+      }
+      store8<DT>(a.q_out, (token * a.q_heads + h) * D + c0, o);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Read back
+// ---------------------------------------------------------------------------
+
+template <int DT>
+__device__ __forceinline__ void store_codes(void* p, int64_t at, uint32_t c, uint32_t e, bool nan) {
+  const float s = exp_scale(e);
+  if constexpr (DT == KDA_BF16) {
+    u4 o = {dequant2<0>(c, s), dequant2<1>(c, s), dequant2<2>(c, s), dequant2<3>(c, s)};
+    if (nan) o = u4{0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};
+    *reinterpret_cast<u4*>(static_cast<uint16_t*>(p) + at) = o;
+  } else {
+    const f2 y0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 0);
+    const f2 y1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 1);
+    const f2 y2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 2);
+    const f2 y3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 3);
+    float x[8] = {y0[0], y0[1], y1[0], y1[1], y2[0], y2[1], y3[0], y3[1]};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = nan ? __builtin_nanf("") : x[i];
+    store8<DT>(p, at, x);
+  }
+}
+
+// Groups of lanes as in the append: one token each, 8 channels a lane.
+template <int DT, int D>
+__global__ __launch_bounds__(256) void kda_kv_read_kernel(KvReadArgs a) {
+  constexpr int W = D / 8;
+  const int li = threadIdx.x % W;
+  const int64_t tile = blockIdx.x / a.head_blocks;
+  const int hb = blockIdx.x % a.head_blocks;
+  const int64_t token = tile * (256 / W) + threadIdx.x / W;
+  const int h0 = hb * a.heads_per_block;
+  const int h1 = h0 + a.heads_per_block < a.t.H ? h0 + a.heads_per_block : a.t.H;
+  const TokenPlace at = find_token<W>(a.t, token, INT32_MAX);
+  if (at.what == kOutside) return;
+  const int block_bytes = kv_block_bytes(a.t.P, D);
+  const bool bad = at.what == kBad;
+  const int code = at.row * (D / 2) + 4 * li;
+  for (int h = h0; h < h1; ++h) {
+    const uint8_t* block = at.block + static_cast<int64_t>(h) * block_bytes;
+    uint32_t kc = 0, vc = 0, ke = kKvPoison, ve = kKvPoison;
+    if (!bad) {
+      kc = *reinterpret_cast<const uint32_t*>(block + code);
+      vc = *reinterpret_cast<const uint32_t*>(block + kv_value_codes(a.t.P, D) + code);
+      ke = block[kv_key_exps(a.t.P, D) + at.row * (D / kKvGroup) + li / 4];
+      ve = block[kv_value_exps(a.t.P, D) + (li / 4) * a.t.P + at.row];
+    }
+    if (a.k_out != nullptr)
+      store_codes<DT>(a.k_out, token * a.k_stride + h * D + 8 * li, kc, ke, ke == kKvPoison);
+    if (a.v_out != nullptr)
+      store_codes<DT>(a.v_out, token * a.v_stride + h * D + 8 * li, vc, ve, ve == kKvPoison);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Attention: one sequence's rows
+// ---------------------------------------------------------------------------
+
+// A sequence as the attention kernels see it.
+struct Seq {
+  int64_t n0;    // its first token's index
+  int rows;      // its tokens in this launch
+  int past;      // tokens cached before them
+  bool skip;     // nothing is written for it
+  bool bad;      // its rows are set to NaN
+};
+
+__device__ __forceinline__ Seq seq_of(const KvTables& t, int s) {
+  const_i32* cu = (const_i32*)t.cu;
+  const_i32* len = (const_i32*)t.past;
+  const int64_t n0 = cu[s], n1 = cu[s + 1];
+  Seq q;
+  q.past = len[s];
+  q.n0 = n0;
+  q.skip = n0 < 0 || n1 <= n0 || n1 > t.n_tokens;
+  q.rows = q.skip ? 0 : static_cast<int>(n1 - n0);
+  q.bad = q.past < 0 || static_cast<int64_t>(q.past) + q.rows > (static_cast<int64_t>(t.max_pages) << t.log_p);
+  return q;
+}
+
+// Splits of a tile whose last row sees `vis` tokens; the last split takes what
+// the launch had no blocks for.
+__device__ __forceinline__ int kv_splits(int vis, const KvAttendArgs& a) {
+  const int n = static_cast<int>((static_cast<int64_t>(vis) + a.chunk - 1) / a.chunk);
+  return n < a.n_splits ? n : a.n_splits;
+}
+
+// bf16 pieces that represent a type's numbers exactly: 24, 11 or 8
+// significant bits, 8 a piece.
+template <int DT>
+constexpr int q_pieces() { return DT == KDA_F32 ? 3 : DT == KDA_F16 ? 2 : 1; }
+// Softmax weights are fp32.  fp32 outputs take all 24 bits of them; for 16-bit
+// outputs two pieces leave 2^-16, a sixteenth of fp16's step.
+template <int DT>
+constexpr int w_pieces() { return DT == KDA_F32 ? 3 : 2; }
+
+// Splits pairs of numbers into N packed bf16 pieces by truncation: what is
+// left after each piece is exact, and 3 pieces hold all of an fp32.
+template <int N>
+__device__ __forceinline__ void split_pair(float x, float y, uint32_t (&out)[N]) {
+#pragma unroll
+  for (int p = 0; p < N; ++p) {
+    out[p] = pack_hi(bits(x), bits(y));
+    x -= __uint_as_float(bits(x) & 0xFFFF0000u);
+    y -= __uint_as_float(bits(y) & 0xFFFF0000u);
+  }
+}
+
+__device__ __forceinline__ f4 mfma16(u4 a, u4 b, f4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, a), __builtin_bit_cast(bf8, b), c, 0, 0, 0);
+}
+
+__device__ __forceinline__ float max_xor16(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(bits(x), bits(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float max_xor32(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(bits(x), bits(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+// Few rows: 16 * NT rows of one sequence and cached head against one split of
+// its tokens, over NW waves.
+//
+// S^T = K Q^T and O^T = V^T P^T in 16x16x32 products, so that the weights go
+// from the first product's result registers straight into the second's right
+// operand: lane l holds query row l % 16, and its tokens 4j + r (j = l / 16)
+// of two 16-token tiles are the 8 contraction slots of the second product.
+// Which channel (or token) sits in which contraction slot is free as long as
+// both operands agree, and it is chosen so that every lane reads whole
+// contiguous pieces of the cache as it lies: a quarter of a key row (16 bytes
+// and one exponent at D = 128), and D / 16 channels of 8 value rows.
+// The waves take the split's 32-token steps in turn, each with its own
+// maximum and sum, and join in LDS.  Bound by HBM: the next step's keys are
+// loaded as soon as the scores have used this step's, its values likewise, so
+// one set of registers keeps loads in flight all the time.
+template <int DT, int D, int NT, int NW>
+__global__ __launch_bounds__(64 * NW) void kda_kv_rows_kernel(KvAttendArgs a) {
+  constexpr int NQ = q_pieces<DT>(), NP = w_pieces<DT>();
+  constexpr int M = D / 32;   // products over the channels
+  constexpr int C = D / 16;   // channels of a lane in the second product, and its row tiles
+  constexpr int R = 16 * NT;
+  constexpr int LD = D + 4;
+  __shared__ float o_sh[NW][R][LD];
+  __shared__ float ml_sh[NW][R][2];
+
+  const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int i16 = lane % 16, j = lane / 16;
+  // block -> (sequence, cached head, split, row tile): row tiles that read
+  // the same tokens are neighbours on one XCD
+  const int id = tile_of_block(blockIdx.x, gridDim.x);
+  const int rt0 = id % a.row_tiles;
+  const int sp = (id / a.row_tiles) % a.n_splits;
+  const int h = (id / a.row_tiles / a.n_splits) % a.t.H;
+  const int s = id / a.row_tiles / a.n_splits / a.t.H;
+  const Seq q = seq_of(a.t, s);
+  if (q.skip) return;
+  const int64_t all_rows = static_cast<int64_t>(q.rows) * a.group;
+
+  const int block_bytes = kv_block_bytes(a.t.P, D);
+  const uint8_t* head0 = a.t.base + static_cast<int64_t>(h) * block_bytes;
+  const_i32* table = (const_i32*)(a.t.page_table + static_cast<int64_t>(s) * a.t.max_pages);
+
+  // Tiles beyond those the launch has blocks for are walked by the same blocks.
+  for (int64_t rt = rt0; rt * R < all_rows; rt += a.row_tiles) {
+    const int row0 = static_cast<int>(rt * R);
+    const int last_row = static_cast<int>(row0 + R < all_rows ? row0 + R : all_rows) - 1;
+    const int vis = q.past + last_row / a.group + 1;  // tokens the last row sees
+    const int splits = q.bad ? 1 : kv_splits(vis, a);
+    if (sp >= splits) continue;
+    const int t0 = q.bad ? 0 : sp * a.chunk;
+    const int t1 = q.bad ? 0 : sp == splits - 1 ? vis : t0 + a.chunk;
+    const int first_limit = q.past + row0 / a.group;  // the last token every row sees
+
+    // this lane's query row of each tile, and the last token it sees
+    u4 qf[NT][NQ][M];
+    int limit[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int row = row0 + 16 * n + i16;
+      const int r = row <= last_row ? row : last_row;
+      const int tok = r / a.group, g = r - tok * a.group;
+      limit[n] = row <= last_row ? q.past + tok : -1;
+      const int64_t at = (q.n0 + tok) * a.q_stride + (static_cast<int64_t>(h) * a.group + g) * D + j * (D / 4);
+#pragma unroll
+      for (int m = 0; m < M; ++m) {
+        float x[8];
+        load8<DT>(a.q, at + 8 * m, x);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t w[NQ];
+          split_pair<NQ>(a.negate ? -x[2 * e] : x[2 * e], a.negate ? -x[2 * e + 1] : x[2 * e + 1], w);
+#pragma unroll
+          for (int p = 0; p < NQ; ++p) qf[n][p][m][e] = w[p];
+        }
+      }
+    }
+
+    f4 o[NT][C];
+    float mx[NT], sum[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      mx[n] = -INFINITY;
+      sum[n] = 0.0f;
+#pragma unroll
+      for (int m = 0; m < C; ++m) o[n][m] = f4{0, 0, 0, 0};
+    }
+
+    uint32_t kc[2][M], ke[2];  // keys: token i16 of two 16-token tiles, D / 4 channels of it
+    uint32_t vc[8], ve[2];     // values: D / 16 channels of tokens 4j + r of both tiles
+    // The page of a tile; -1 if it does not exist or no token is left.
+    auto page_of = [&](int t) __attribute__((always_inline)) {
+      const int page = t < t1 ? table[t >> a.t.log_p] : -1;
+      return page < a.t.n_pages ? page : -1;
+    };
+    // without a page: keys that score NaN (seen only where the mask lets
+    // them), values of zero
+    auto load_keys = [&](int tb) __attribute__((always_inline)) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int page = page_of(tb + 16 * b);
+        if (page >= 0) {
+          const uint8_t* blk = head0 + page * a.t.page_bytes;
+          const int row = ((tb + 16 * b) & (a.t.P - 1)) + i16;
+          const uint8_t* kp = blk + row * (D / 2) + j * (D / 8);
+          if constexpr (D == 128) {
+            const u4 x = *reinterpret_cast<const u4*>(kp);
+#pragma unroll
+            for (int m = 0; m < M; ++m) kc[b][m] = x[m];
+          } else {
+            const u2 x = *reinterpret_cast<const u2*>(kp);
+#pragma unroll
+            for (int m = 0; m < M; ++m) kc[b][m] = x[m];
+          }
+          ke[b] = blk[kv_key_exps(a.t.P, D) + row * (D / kKvGroup) + j * (D / 4) / kKvGroup];
+        } else {
+          ke[b] = kKvPoison;
+#pragma unroll
+          for (int m = 0; m < M; ++m) kc[b][m] = 0;
+        }
+      }
+    };
+    auto load_values = [&](int tb) __attribute__((always_inline)) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int page = page_of(tb + 16 * b);
+        if (page >= 0) {
+          const uint8_t* blk = head0 + page * a.t.page_bytes;
+          const int row = ((tb + 16 * b) & (a.t.P - 1)) + 4 * j;
+          const uint8_t* vp = blk + kv_value_codes(a.t.P, D) + row * (D / 2) + i16 * (D / 32);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            if constexpr (D == 128)
+              vc[4 * b + r] = *reinterpret_cast<const uint32_t*>(vp + r * (D / 2));
+            else
+              vc[4 * b + r] = *reinterpret_cast<const uint16_t*>(vp + r * (D / 2));
+          }
+          ve[b] = *reinterpret_cast<const uint32_t*>(blk + kv_value_exps(a.t.P, D) + (i16 * C / kKvGroup) * a.t.P + row);
+        } else {
+          ve[b] = 0x7F7F7F7Fu;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) vc[4 * b + r] = 0;
+        }
+      }
+    };
+
+    int tb = t0 + 32 * wave;
+    if (tb < t1) {
+      load_keys(tb);
+      load_values(tb);
+    }
+    for (; tb < t1; tb += 32 * NW) {
+      // -- scores of 32 tokens
+      f4 sc[NT][2];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) sc[n][b] = f4{0, 0, 0, 0};
+        const float ks = exp_scale(ke[b]);
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+          u4 kf = {dequant2<0>(kc[b][m], ks), dequant2<1>(kc[b][m], ks), dequant2<2>(kc[b][m], ks),
+                   dequant2<3>(kc[b][m], ks)};
+          if (m == 0) kf[0] = ke[b] == kKvPoison ? 0x7FC07FC0u : kf[0];
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int p = 0; p < NQ; ++p) sc[n][b] = mfma16(kf, qf[n][p][m], sc[n][b]);
+        }
+      }
+      if (tb + 32 * NW < t1) load_keys(tb + 32 * NW);
+      // -- tokens behind a row's own; values there may be anything, and
+      // become zeros
+      const bool tail = tb + 31 > first_limit;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) sc[n][b] *= a.scale;
+      if (tail) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int t = tb + 16 * b + 4 * j + r;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) sc[n][b][r] = t > limit[n] ? -INFINITY : sc[n][b][r];
+            vc[4 * b + r] = t >= t1 ? 0 : vc[4 * b + r];
+            ve[b] = t >= t1 ? (ve[b] & ~(0xFFu << (8 * r))) | (127u << (8 * r)) : ve[b];
+          }
+      }
+      // -- weights: the running maximum is moved only when a score passes it
+      // by 8 (weights then stay below 2^8, and the sums keep their 24 bits)
+      u4 pf[NT][NP];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float best = fmaxf(fmaxf(fmaxf(sc[n][0][0], sc[n][0][1]), fmaxf(sc[n][0][2], sc[n][0][3])),
+                           fmaxf(fmaxf(sc[n][1][0], sc[n][1][1]), fmaxf(sc[n][1][2], sc[n][1][3])));
+        if (__ballot(best > mx[n] + 8.0f) != 0) {
+          best = fmaxf(max_xor32(max_xor16(best)), mx[n]);
+          const float keep = mx[n] == best ? 1.0f : exp2_hw(mx[n] - best);
+          mx[n] = best;
+          sum[n] *= keep;
+#pragma unroll
+          for (int m = 0; m < C; ++m) o[n][m] *= keep;
+        }
+        const float base = mx[n] == -INFINITY ? 0.0f : mx[n];
+        float w[8];
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) w[4 * b + r] = exp2_hw(sc[n][b][r] - base);
+        sum[n] += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t t[NP];
+          split_pair<NP>(w[2 * e], w[2 * e + 1], t);
+#pragma unroll
+          for (int p = 0; p < NP; ++p) pf[n][p][e] = t[p];
+        }
+      }
+      // -- values: two channels of the 8 tokens at a time
+      auto channels = [&](auto pick) __attribute__((always_inline)) {
+        constexpr int c = decltype(pick)::value;
+        uint32_t x[8];
+#pragma unroll
+        for (int t = 0; t < 8; ++t) x[t] = dequant2<c>(vc[t], exp_scale((ve[t / 4] >> (8 * (t % 4))) & 0xFF));
+        const u4 even = {pack_lo(x[0], x[1]), pack_lo(x[2], x[3]), pack_lo(x[4], x[5]), pack_lo(x[6], x[7])};
+        const u4 odd = {pack_hi(x[0], x[1]), pack_hi(x[2], x[3]), pack_hi(x[4], x[5]), pack_hi(x[6], x[7])};
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int p = 0; p < NP; ++p) {
+            o[n][2 * c] = mfma16(even, pf[n][p], o[n][2 * c]);
+            o[n][2 * c + 1] = mfma16(odd, pf[n][p], o[n][2 * c + 1]);
+          }
+      };
+      channels(std::integral_constant<int, 0>{});
+      channels(std::integral_constant<int, 1>{});
+      if constexpr (C == 8) {
+        channels(std::integral_constant<int, 2>{});
+        channels(std::integral_constant<int, 3>{});
+      }
+      if (tb + 32 * NW < t1) load_values(tb + 32 * NW);
+    }
+
+    // -- join the waves: row n of a tile, channels C (4j + r) + m
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const float total = sum_xor32(sum_xor16(sum[n]));
+      if (j == 0) {
+        ml_sh[wave][16 * n + i16][0] = mx[n];
+        ml_sh[wave][16 * n + i16][1] = total;
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int m = 0; m < C; m += 4)
+          *reinterpret_cast<f4*>(&o_sh[wave][16 * n + i16][C * (4 * j + r) + m]) =
+              f4{o[n][m][r], o[n][m + 1][r], o[n][m + 2][r], o[n][m + 3][r]};
+    }
+    __syncthreads();
+    constexpr int PER = D / 8;  // threads of a row, 8 channels each
+    for (int it = threadIdx.x; it < R * PER; it += 64 * NW) {
+      const int r = it / PER, c = 8 * (it % PER), row = row0 + r;
+      if (row > last_row) continue;
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) top = fmaxf(top, ml_sh[w][r][0]);
+      float acc[8] = {}, total = 0.0f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        const float m = ml_sh[w][r][0];
+        const float f = m == -INFINITY ? (top == -INFINITY ? 1.0f : 0.0f) : exp2_hw(m - top);
+        // a wave without a finite maximum holds zeros, or NaN from a page
+        // that does not exist or a poisoned key
+        total += m == -INFINITY ? ml_sh[w][r][1] : ml_sh[w][r][1] * f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] = fmaf(o_sh[w][r][c + e], f, acc[e]);
+      }
+      const int tok = row / a.group, g = row - tok * a.group;
+      const int64_t at = (q.n0 + tok) * a.q_heads + static_cast<int64_t>(h) * a.group + g;
+      if (splits == 1) {
+        // a row that sees nothing is zero; a bad sequence's rows are NaN
+        const float inv = q.bad ? __builtin_nanf("") : total == 0.0f ? 0.0f : 1.0f / total;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] *= inv;
+        store8<DT>(a.out, at * D + c, acc);
+      } else {
+        const int64_t slot = static_cast<int64_t>(sp) * a.t.n_tokens * a.q_heads + at;
+        store8<KDA_F32>(a.part, slot * D + c, acc);
+        if (c == 0) {
+          a.part_ml[2 * slot] = top;
+          a.part_ml[2 * slot + 1] = total;
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// Joins the splits of a row: one wave a row, D / 8 lanes across its channels
+// and the rest across its splits, so that 128 splits take 32 loads of a lane
+// (8 in flight) instead of 128 one after the other.
+template <int DT, int D>
+__global__ __launch_bounds__(256) void kda_kv_join_kernel(KvAttendArgs a, int tile_rows) {
+  constexpr int PER = D / 8, G = 64 / PER;
+  const int lane = threadIdx.x % 64, c = 8 * (lane % PER), grp = lane / PER;
+  const int slices = tile_rows / 4;
+  const int id = blockIdx.x;
+  const int r = (id % slices) * 4 + threadIdx.x / 64;
+  const int rt0 = (id / slices) % a.row_tiles;
+  const int h = (id / slices / a.row_tiles) % a.t.H;
+  const int s = id / slices / a.row_tiles / a.t.H;
+  const Seq q = seq_of(a.t, s);
+  if (q.skip || q.bad) return;
+  const int64_t all_rows = static_cast<int64_t>(q.rows) * a.group;
+  const int64_t stride = a.t.n_tokens * a.q_heads;
+  for (int64_t rt = rt0; rt * tile_rows + r < all_rows; rt += a.row_tiles) {
+    const int64_t row = rt * tile_rows + r;
+    const int64_t last = (rt + 1) * tile_rows < all_rows ? (rt + 1) * tile_rows - 1 : all_rows - 1;
+    const int splits = kv_splits(q.past + static_cast<int>(last / a.group) + 1, a);
+    if (splits <= 1) continue;  // written already
+    const int tok = static_cast<int>(row / a.group), g = static_cast<int>(row - static_cast<int64_t>(tok) * a.group);
+    const int64_t at = (q.n0 + tok) * a.q_heads + static_cast<int64_t>(h) * a.group + g;
+    float top = -INFINITY;
+    for (int i = lane; i < splits; i += 64) top = fmaxf(top, a.part_ml[2 * (i * stride + at)]);
+#pragma unroll
+    for (int m = 1; m < 64; m *= 2) top = fmaxf(top, __shfl_xor(top, m));
+    float acc[8] = {}, total = 0.0f;
+#pragma unroll 4
+    for (int i = grp; i < splits; i += G) {
+      const int64_t slot = i * stride + at;
+      const float m = a.part_ml[2 * slot], l = a.part_ml[2 * slot + 1];
+      float x[8];
+      load8<KDA_F32>(a.part, slot * D + c, x);
+      const float f = m == -INFINITY ? (top == -INFINITY ? 1.0f : 0.0f) : exp2_hw(m - top);
+      total += m == -INFINITY ? l : l * f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] = fmaf(x[e], f, acc[e]);
+    }
+#pragma unroll
+    for (int m = PER; m < 64; m *= 2) {
+      total += __shfl_xor(total, m);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] += __shfl_xor(acc[e], m);
+    }
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] *= inv;
+    if (grp == 0) store8<DT>(a.out, at * D + c, acc);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Launches
+// ---------------------------------------------------------------------------
+
+bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+int type_bytes(kda_dtype d) { return d == KDA_F32 ? 4 : d == KDA_F16 || d == KDA_BF16 ? 2 : 0; }
+
+KvTables make_tables(const kda_kv_pool* kv, const int32_t* page_table, int32_t max_pages, const int32_t* cu,
+                     const int32_t* past, int32_t n_seq, int64_t n_tokens) {
+  KvTables t;
+  t.base = static_cast<uint8_t*>(kv->base);
+  t.page_table = page_table;
+  t.cu = cu;
+  t.past = past;
+  t.page_bytes = static_cast<int64_t>(kv->H) * kv_block_bytes(kv->page_tokens, kv->D);
+  t.n_tokens = n_tokens;
+  t.n_pages = kv->n_pages;
+  t.max_pages = max_pages;
+  t.n_seq = n_seq;
+  t.H = kv->H;
+  t.P = kv->page_tokens;
+  t.log_p = 31 - __builtin_clz(static_cast<unsigned>(kv->page_tokens));
+  return t;
+}
+
+int status(hipError_t e) { return e == hipSuccess ? KDA_OK : KDA_ERR_LAUNCH; }
+
+// f(integral_constant<dtype>, integral_constant<D>)
+template <typename F>
+hipError_t by_type(kda_dtype dt, int D, F f) {
+  auto with_d = [&](auto t) {
+    return D == 128 ? f(t, std::integral_constant<int, 128>{}) : f(t, std::integral_constant<int, 64>{});
+  };
+  switch (dt) {
+    case KDA_F32: return with_d(std::integral_constant<int, KDA_F32>{});
+    case KDA_F16: return with_d(std::integral_constant<int, KDA_F16>{});
+    default: return with_d(std::integral_constant<int, KDA_BF16>{});
+  }
+}
+
+// A block takes 256 / (D / 8) tokens; with few of them the heads are dealt to
+// more blocks, down to one head each.
+int heads_a_block(int64_t token_tiles, int heads) {
+  const int64_t most = (4096 + token_tiles - 1) / token_tiles;  // blocks wanted a token tile
+  int64_t n = (heads + most - 1) / most;
+  return static_cast<int>(n < 1 ? 1 : n);
+}
+
+}  // namespace
+}  // namespace kda
+
+using namespace kda;
+
+extern "C" int kda_kv_append(const kda_kv_pool* kv, const int32_t* page_table, int32_t max_pages,
+                             const int32_t* cu_seqlens, const int32_t* cache_lens, const void* k, const void* v,
+                             int64_t k_stride, int64_t v_stride, const void* q, int64_t q_stride, void* q_out,
+                             const float* cos, const float* sin, int32_t n_positions, int32_t rot_dim,
+                             int32_t interleaved, int32_t n_seq, int64_t n_tokens, int32_t q_heads,
+                             kda_dtype dtype, void* stream) {
+  const int rc = kv_check(kv, max_pages, n_seq, n_tokens);
+  if (rc != KDA_OK) return rc;
+  const int size = type_bytes(dtype);
+  if (size == 0) return KDA_ERR_DTYPE_REFUSED;
+  if (q_heads < 0 || q_heads > 65535 || n_positions < 0 || (interleaved != 0 && interleaved != 1)) return KDA_ERR_ARG;
+  if (rot_dim < 0 || rot_dim > kv->D || rot_dim % 16 != 0) return KDA_ERR_SHAPE;
+  if (n_seq == 0 || n_tokens == 0) return KDA_OK;
+  if (page_table == nullptr || cu_seqlens == nullptr || cache_lens == nullptr || k == nullptr || v == nullptr)
+    return KDA_ERR_NULL;
+  if (q_heads > 0 && (q == nullptr || q_out == nullptr)) return KDA_ERR_NULL;
+  if (rot_dim > 0 && (cos == nullptr || sin == nullptr)) return KDA_ERR_NULL;
+  const int64_t kv_row = static_cast<int64_t>(kv->H) * kv->D, q_row = static_cast<int64_t>(q_heads) * kv->D;
+  if (k_stride < kv_row || v_stride < kv_row || (q_heads > 0 && q_stride < q_row)) return KDA_ERR_ARG;
+  if (!aligned(kv->base, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q, 16) || !aligned(q_out, 16) ||
+      !aligned(cos, 16) || !aligned(sin, 16) || !aligned(page_table, 4) || !aligned(cu_seqlens, 4) ||
+      !aligned(cache_lens, 4) || k_stride * size % 16 != 0 || v_stride * size % 16 != 0 ||
+      (q_heads > 0 && q_stride * size % 16 != 0))
+    return KDA_ERR_ALIGN;
+  KvAppendArgs a;
+  a.t = make_tables(kv, page_table, max_pages, cu_seqlens, cache_lens, n_seq, n_tokens);
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_out = q_out;
+  a.cos = cos;
+  a.sin = sin;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.n_positions = rot_dim > 0 ? n_positions : INT32_MAX;
+  a.half = rot_dim / 2;
+  a.interleaved = interleaved;
+  a.q_heads = q_heads;
+  a.units = kv->H + q_heads;
+  const int64_t tiles = (n_tokens + 256 / (kv->D / 8) - 1) / (256 / (kv->D / 8));
+  a.units_per_block = heads_a_block(tiles, a.units);
+  a.unit_blocks = (a.units + a.units_per_block - 1) / a.units_per_block;
+  if (tiles * a.unit_blocks > INT32_MAX) return KDA_ERR_ARG;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  return status(by_type(dtype, kv->D, [&](auto t, auto d) {
+    hipLaunchKernelGGL((kda_kv_append_kernel<decltype(t)::value, decltype(d)::value>),
+                       dim3(static_cast<uint32_t>(tiles * a.unit_blocks)), dim3(256), 0, st, a);
+    return hipGetLastError();
+  }));
+}
+
+extern "C" int kda_kv_read(const kda_kv_pool* kv, const int32_t* page_table, int32_t max_pages,
+                           const int32_t* cu_seqlens, const int32_t* first, void* k_out, void* v_out,
+                           int64_t k_stride, int64_t v_stride, int32_t n_seq, int64_t n_tokens, kda_dtype dtype,
+                           void* stream) {
+  const int rc = kv_check(kv, max_pages, n_seq, n_tokens);
+  if (rc != KDA_OK) return rc;
+  const int size = type_bytes(dtype);
+  if (size == 0) return KDA_ERR_DTYPE_REFUSED;
+  if (n_seq == 0 || n_tokens == 0) return KDA_OK;
+  if (page_table == nullptr || cu_seqlens == nullptr || first == nullptr || (k_out == nullptr && v_out == nullptr))
+    return KDA_ERR_NULL;
+  const int64_t row = static_cast<int64_t>(kv->H) * kv->D;
+  if ((k_out != nullptr && k_stride < row) || (v_out != nullptr && v_stride < row)) return KDA_ERR_ARG;
+  if (!aligned(kv->base, 16) || !aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(page_table, 4) ||
+      !aligned(cu_seqlens, 4) || !aligned(first, 4) || (k_out != nullptr && k_stride * size % 16 != 0) ||
+      (v_out != nullptr && v_stride * size % 16 != 0))
+    return KDA_ERR_ALIGN;
+  KvReadArgs a;
+  a.t = make_tables(kv, page_table, max_pages, cu_seqlens, first, n_seq, n_tokens);
+  a.k_out = k_out;
+  a.v_out = v_out;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  const int64_t tiles = (n_tokens + 256 / (kv->D / 8) - 1) / (256 / (kv->D / 8));
+  a.heads_per_block = heads_a_block(tiles, kv->H);
+  a.head_blocks = (kv->H + a.heads_per_block - 1) / a.heads_per_block;
+  if (tiles * a.head_blocks > INT32_MAX) return KDA_ERR_ARG;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  return status(by_type(dtype, kv->D, [&](auto t, auto d) {
+    hipLaunchKernelGGL((kda_kv_read_kernel<decltype(t)::value, decltype(d)::value>),
+                       dim3(static_cast<uint32_t>(tiles * a.head_blocks)), dim3(256), 0, st, a);
+    return hipGetLastError();
+  }));
+}
+
+extern "C" int kda_kv_attend(const kda_kv_pool* kv, const int32_t* page_table, int32_t max_pages,
+                             const int32_t* cu_seqlens, const int32_t* cache_lens, const void* q,
+                             int64_t q_stride, void* out, int32_t n_seq, int64_t n_tokens, int32_t max_rows,
+                             int64_t max_kv_len, int32_t q_heads, kda_dtype dtype, float scale, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  const int rc = kv_check(kv, max_pages, n_seq, n_tokens);
+  if (rc != KDA_OK) return rc;
+  const int size = type_bytes(dtype);
+  if (size == 0) return KDA_ERR_DTYPE_REFUSED;
+  if (q_heads < 1 || q_heads > 65535 || q_heads % kv->H != 0) return KDA_ERR_SHAPE;
+  if (max_rows < 0 || max_kv_len < 0 || !std::isfinite(scale)) return KDA_ERR_ARG;
+  // a row index is token * group + head within the group
+  if (n_tokens * (q_heads / kv->H) > INT32_MAX / 2) return KDA_ERR_ARG;
+  if (n_seq == 0 || n_tokens == 0) return KDA_OK;
+  if (page_table == nullptr || cu_seqlens == nullptr || cache_lens == nullptr || q == nullptr || out == nullptr)
+    return KDA_ERR_NULL;
+  if (q_stride < static_cast<int64_t>(q_heads) * kv->D) return KDA_ERR_ARG;
+  if (!aligned(kv->base, 16) || !aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 16) ||
+      !aligned(page_table, 4) || !aligned(cu_seqlens, 4) || !aligned(cache_lens, 4) || q_stride * size % 16 != 0)
+    return KDA_ERR_ALIGN;
+  const size_t need = kda_kv_attend_workspace(kv, max_pages, n_seq, n_tokens, max_rows, max_kv_len, q_heads, dtype);
+  if (need > 0 && workspace == nullptr) return KDA_ERR_NULL;
+  if (need > workspace_bytes) return KDA_ERR_ARG;
+  const int64_t cover = static_cast<int64_t>(max_pages) * kv->page_tokens;
+  const KvPlan p = kv_plan(kv->H, kv->D, n_seq, n_tokens, max_rows,
+                           max_kv_len > 0 && max_kv_len < cover ? max_kv_len : cover, q_heads, dtype);
+  KvAttendArgs a;
+  a.t = make_tables(kv, page_table, max_pages, cu_seqlens, cache_lens, n_seq, n_tokens);
+  a.q = q;
+  a.out = out;
+  a.q_stride = q_stride;
+  a.q_heads = q_heads;
+  a.group = q_heads / kv->H;
+  a.chunk = p.chunk;
+  a.n_splits = p.n_splits;
+  a.row_tiles = p.row_tiles;
+  a.scale = std::fabs(scale) * 1.44269504088896340736f;
+  a.negate = scale < 0.0f;
+  a.part = static_cast<float*>(workspace);
+  a.part_ml = a.part == nullptr ? nullptr : a.part + static_cast<int64_t>(p.n_splits) * n_tokens * q_heads * kv->D;
+  const int64_t blocks = static_cast<int64_t>(n_seq) * kv->H * p.row_tiles * p.n_splits;
+  if (blocks > INT32_MAX) return KDA_ERR_ARG;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  return status(by_type(dtype, kv->D, [&](auto t, auto d) {
+    constexpr int DT = decltype(t)::value, D = decltype(d)::value;
+    const dim3 grid(static_cast<uint32_t>(blocks));
+    if (p.tile_rows == 16)
+      hipLaunchKernelGGL((kda_kv_rows_kernel<DT, D, 1, 4>), grid, dim3(256), 0, st, a);
+    else
+      hipLaunchKernelGGL((kda_kv_rows_kernel<DT, D, 2, 4>), grid, dim3(256), 0, st, a);
+    hipError_t e = hipGetLastError();
+    if (e == hipSuccess && p.n_splits > 1) {
+      const int slices = p.tile_rows / 4;
+      hipLaunchKernelGGL((kda_kv_join_kernel<DT, D>),
+                         dim3(static_cast<uint32_t>(n_seq) * kv->H * p.row_tiles * slices), dim3(256), 0, st, a,
+                         p.tile_rows);
+      e = hipGetLastError();
+    }
+    return e;
+  }));
+}

@@ -1,0 +1,110 @@
+// kda_kv_host.cpp -- host half of the paged 4-bit key/value cache: argument
+// checks, sizes, table validation and the split of an attention launch.
+// Makes no HIP call, so every refusal can be exercised without a GPU.
+#include <cstdint>
+#include <unordered_map>
+
+#include "kda_kv.h"
+
+namespace kda {
+
+static bool page_tokens_ok(int32_t p) { return p == 16 || p == 32 || p == 64 || p == 128 || p == 256; }
+
+int kv_check(const kda_kv_pool* kv, int32_t max_pages, int32_t n_seq, int64_t n_tokens) {
+  if (kv == nullptr || kv->base == nullptr) return KDA_ERR_NULL;
+  if ((kv->D != 64 && kv->D != 128) || !page_tokens_ok(kv->page_tokens) || kv->H < 1 ||
+      kv->H > kKvMaxHeads || kv->n_pages < 1)
+    return KDA_ERR_SHAPE;
+  if (n_seq < 0 || n_tokens < 0 || n_tokens > INT32_MAX || max_pages < 1) return KDA_ERR_ARG;
+  // positions stay below 2^31
+  if (static_cast<int64_t>(max_pages) * kv->page_tokens > INT32_MAX) return KDA_ERR_ARG;
+  return KDA_OK;
+}
+
+KvPlan kv_plan(int32_t H, int32_t D, int32_t n_seq, int64_t n_tokens, int32_t max_rows,
+               int64_t max_kv_len, int32_t q_heads, kda_dtype dtype) {
+  (void)D;
+  (void)dtype;
+  KvPlan p;
+  const int64_t rows = static_cast<int64_t>(max_rows < n_tokens ? max_rows : n_tokens) * (q_heads / H);
+  p.tile_rows = rows <= 16 ? 16 : 32;
+  p.row_tiles = static_cast<int32_t>((rows + p.tile_rows - 1) / p.tile_rows);
+  if (p.row_tiles < 1) p.row_tiles = 1;
+  // Splits: enough workgroups for every compute unit to hold several, and no
+  // split shorter than 128 tokens (one step of each of its four waves).
+  const int64_t units = static_cast<int64_t>(n_seq) * H * p.row_tiles;
+  int64_t want = (4 * 256 + units - 1) / (units < 1 ? 1 : units);
+  const int64_t most = (max_kv_len + 127) / 128;
+  if (want > most) want = most;
+  if (want < 1) want = 1;
+  int64_t chunk = (max_kv_len + want - 1) / want;
+  chunk = (chunk + 127) / 128 * 128;
+  if (chunk < 128) chunk = 128;
+  p.chunk = static_cast<int32_t>(chunk);
+  p.n_splits = static_cast<int32_t>((max_kv_len + chunk - 1) / chunk);
+  if (p.n_splits < 1) p.n_splits = 1;
+  return p;
+}
+
+}  // namespace kda
+
+using namespace kda;
+
+extern "C" {
+
+size_t kda_kv_pool_bytes(int32_t n_pages, int32_t page_tokens, int32_t H, int32_t D) {
+  if ((D != 64 && D != 128) || !page_tokens_ok(page_tokens) || n_pages < 0 || H < 0) return 0;
+  return static_cast<size_t>(n_pages) * H * kv_block_bytes(page_tokens, D);
+}
+
+size_t kda_kv_attend_workspace(const kda_kv_pool* kv, int32_t max_pages, int32_t n_seq, int64_t n_tokens,
+                               int32_t max_rows, int64_t max_kv_len, int32_t q_heads, kda_dtype dtype) {
+  if (kv_check(kv, max_pages, n_seq, n_tokens) != KDA_OK) return 0;
+  if (q_heads < 1 || q_heads % kv->H != 0 || max_rows < 0 || max_kv_len < 0) return 0;
+  const int64_t cover = static_cast<int64_t>(max_pages) * kv->page_tokens;
+  const KvPlan p = kv_plan(kv->H, kv->D, n_seq, n_tokens, max_rows,
+                           max_kv_len > 0 && max_kv_len < cover ? max_kv_len : cover, q_heads, dtype);
+  if (p.n_splits == 1) return 0;
+  return static_cast<size_t>(p.n_splits) * n_tokens * q_heads * (kv->D + 2) * sizeof(float);
+}
+
+int kda_kv_validate(const kda_kv_pool* kv, const int32_t* page_table_host, int32_t max_pages,
+                    const int32_t* cu_seqlens_host, const int32_t* cache_lens_host, int32_t n_seq,
+                    int64_t n_tokens) {
+  const int rc = kv_check(kv, max_pages, n_seq, n_tokens);
+  if (rc != KDA_OK) return rc;
+  if (n_seq == 0) return KDA_OK;
+  if (page_table_host == nullptr || cu_seqlens_host == nullptr || cache_lens_host == nullptr)
+    return KDA_ERR_NULL;
+  if (cu_seqlens_host[0] < 0) return KDA_ERR_ARG;
+  const int64_t cover = static_cast<int64_t>(max_pages) * kv->page_tokens;
+  for (int32_t s = 0; s < n_seq; ++s) {
+    if (cu_seqlens_host[s + 1] < cu_seqlens_host[s] || cu_seqlens_host[s + 1] > n_tokens) return KDA_ERR_ARG;
+    if (cache_lens_host[s] < 0) return KDA_ERR_ARG;
+    if (static_cast<int64_t>(cache_lens_host[s]) + cu_seqlens_host[s + 1] - cu_seqlens_host[s] > cover)
+      return KDA_ERR_ARG;
+  }
+  // pages that hold a sequence's tokens exist; a page that takes new tokens
+  // belongs to that sequence alone (pages before it may be shared)
+  std::unordered_map<int32_t, int64_t> writer;  // page -> s * max_pages + index
+  for (int pass = 0; pass < 2; ++pass)
+    for (int32_t s = 0; s < n_seq; ++s) {
+      const int32_t n = cu_seqlens_host[s + 1] - cu_seqlens_host[s];
+      const int64_t used = (static_cast<int64_t>(cache_lens_host[s]) + n + kv->page_tokens - 1) / kv->page_tokens;
+      const int64_t first_new = cache_lens_host[s] / kv->page_tokens;
+      for (int64_t i = 0; i < used; ++i) {
+        const int64_t at = static_cast<int64_t>(s) * max_pages + i;
+        const int32_t page = page_table_host[at];
+        if (page < 0 || page >= kv->n_pages) return KDA_ERR_SLOT;
+        const bool written = n > 0 && i >= first_new;
+        if (pass == 0 && written && !writer.emplace(page, at).second) return KDA_ERR_SLOT;
+        if (pass == 1) {
+          const auto it = writer.find(page);
+          if (it != writer.end() && it->second != at) return KDA_ERR_SLOT;
+        }
+      }
+    }
+  return KDA_OK;
+}
+
+}  // extern "C"
