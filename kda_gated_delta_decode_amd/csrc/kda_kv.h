@@ -71,7 +71,7 @@ struct KvAttendArgs {
   int32_t chunk, n_splits;      // tokens a split covers
   int32_t row_tiles;            // tiles of rows a sequence is given blocks for
   float scale;                  // |scale| * log2(e)
-  int32_t negate;               // scale < 0
+  float sign;                   // of scale: queries are multiplied by it
 };
 
 // How kda_kv_attend takes a launch.

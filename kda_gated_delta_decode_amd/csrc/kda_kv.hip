@@ -13,6 +13,7 @@
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
+#include <utility>
 
 #include "kda_decode.h"
 #include "kda_device.h"
@@ -23,6 +24,7 @@ namespace {
 
 using bf2 = __bf16 __attribute__((ext_vector_type(2)));
 using bf8 = __bf16 __attribute__((ext_vector_type(8)));
+using f16v = float __attribute__((ext_vector_type(16)));
 using u2 = uint32_t __attribute__((ext_vector_type(2)));
 using u4 = uint32_t __attribute__((ext_vector_type(4)));
 
@@ -34,6 +36,8 @@ template <int DT>
 constexpr int elem_bytes() { return DT == KDA_F32 ? 4 : 2; }
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+// NaN if either is (one instruction, without fmaxf's quieting of its operands)
+__device__ __forceinline__ float max_nan(float x, float y) { return __builtin_elementwise_maximum(x, y); }
 __device__ __forceinline__ uint32_t bits(float x) { return __float_as_uint(x); }
 // the upper (lower) halves of a and b as one register, a's first
 __device__ __forceinline__ uint32_t pack_hi(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302); }
@@ -84,6 +88,27 @@ __device__ __forceinline__ void store8(void* p, int64_t at, const float (&x)[8])
     for (int e = 0; e < 8; ++e) a[e] = static_cast<__bf16>(x[e]);
     *reinterpret_cast<bf8*>(static_cast<__bf16*>(p) + at) = a;
   }
+}
+
+template <int DT>
+__device__ __forceinline__ void store4(void* p, int64_t at, f4 x) {
+  if constexpr (DT == KDA_F32) {
+    *reinterpret_cast<f4*>(static_cast<float*>(p) + at) = x;
+  } else if constexpr (DT == KDA_F16) {
+    *reinterpret_cast<h4*>(static_cast<_Float16*>(p) + at) =
+        h4{static_cast<_Float16>(x[0]), static_cast<_Float16>(x[1]), static_cast<_Float16>(x[2]), static_cast<_Float16>(x[3])};
+  } else {
+    using bf4 = __bf16 __attribute__((ext_vector_type(4)));
+    *reinterpret_cast<bf4*>(static_cast<__bf16*>(p) + at) =
+        bf4{static_cast<__bf16>(x[0]), static_cast<__bf16>(x[1]), static_cast<__bf16>(x[2]), static_cast<__bf16>(x[3])};
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ void store_channels(void* p, int64_t at, const float (&x)[8]) { store8<DT>(p, at, x); }
+template <int DT>
+__device__ __forceinline__ void store_channels(void* p, int64_t at, const float (&x)[4]) {
+  store4<DT>(p, at, f4{x[0], x[1], x[2], x[3]});
 }
 
 // ---------------------------------------------------------------------------
@@ -385,9 +410,13 @@ __device__ __forceinline__ int kv_splits(int vis, const KvAttendArgs& a) {
 template <int DT>
 constexpr int q_pieces() { return DT == KDA_F32 ? 3 : DT == KDA_F16 ? 2 : 1; }
 // Softmax weights are fp32.  fp32 outputs take all 24 bits of them; for 16-bit
-// outputs two pieces leave 2^-16, a sixteenth of fp16's step.
+// outputs two pieces leave less than 2^-15 of one, a sixteenth of fp16's half
+// step.  Prompts in bf16 take one, rounded to nearest: each weight is off by
+// at most the output's own half step, at random, and the product runs once.
 template <int DT>
 constexpr int w_pieces() { return DT == KDA_F32 ? 3 : 2; }
+template <int DT>
+constexpr int w_pieces_tiles() { return DT == KDA_BF16 ? 1 : w_pieces<DT>(); }
 
 // Splits pairs of numbers into N packed bf16 pieces by truncation: what is
 // left after each piece is exact, and 3 pieces hold all of an fp32.
@@ -398,6 +427,27 @@ __device__ __forceinline__ void split_pair(float x, float y, uint32_t (&out)[N])
     out[p] = pack_hi(bits(x), bits(y));
     x -= __uint_as_float(bits(x) & 0xFFFF0000u);
     y -= __uint_as_float(bits(y) & 0xFFFF0000u);
+  }
+}
+
+// 8 channels of a query as its bf16 pieces; sign is 1 or -1
+template <int DT>
+__device__ __forceinline__ void load_query(const void* q, int64_t at, float sign, u4 (&out)[q_pieces<DT>()]) {
+  if constexpr (DT == KDA_BF16) {
+    out[0] = *reinterpret_cast<const u4*>(static_cast<const uint16_t*>(q) + at);
+    const uint32_t flip = sign < 0.0f ? 0x80008000u : 0u;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) out[0][e] ^= flip;
+  } else {
+    float x[8];
+    load8<DT>(q, at, x);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      uint32_t w[q_pieces<DT>()];
+      split_pair<q_pieces<DT>()>(x[2 * e] * sign, x[2 * e + 1] * sign, w);
+#pragma unroll
+      for (int p = 0; p < q_pieces<DT>(); ++p) out[p][e] = w[p];
+    }
   }
 }
 
@@ -479,15 +529,10 @@ __global__ __launch_bounds__(64 * NW) void kda_kv_rows_kernel(KvAttendArgs a) {
       const int64_t at = (q.n0 + tok) * a.q_stride + (static_cast<int64_t>(h) * a.group + g) * D + j * (D / 4);
 #pragma unroll
       for (int m = 0; m < M; ++m) {
-        float x[8];
-        load8<DT>(a.q, at + 8 * m, x);
+        u4 x[NQ];
+        load_query<DT>(a.q, at + 8 * m, a.sign, x);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t w[NQ];
-          split_pair<NQ>(a.negate ? -x[2 * e] : x[2 * e], a.negate ? -x[2 * e + 1] : x[2 * e + 1], w);
-#pragma unroll
-          for (int p = 0; p < NQ; ++p) qf[n][p][m][e] = w[p];
-        }
+        for (int p = 0; p < NQ; ++p) qf[n][p][m] = x[p];
       }
     }
 
@@ -710,6 +755,326 @@ __global__ __launch_bounds__(64 * NW) void kda_kv_rows_kernel(KvAttendArgs a) {
       }
     }
     __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Attention: prompts
+// ---------------------------------------------------------------------------
+
+// f(0), f(1), .. with constants
+template <typename F, int... I>
+__device__ __forceinline__ void each_of(F f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+
+// Waves a SIMD for the registers: two where they fit in 256, else one.
+template <int DT, int D>
+constexpr int kv_tiles_waves() { return DT == KDA_BF16 || (DT == KDA_F16 && D == 64) ? 2 : 1; }
+
+__device__ __forceinline__ f16v mfma32(u4 a, u4 b, f16v c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8, a), __builtin_bit_cast(bf8, b), c, 0, 0, 0);
+}
+
+// Many rows: 128 rows of one sequence and cached head (32 a wave) against one
+// split of its tokens, 64 of them at a time.
+//
+// The products are the rows kernel's, S^T = K Q^T and O^T = V^T P^T, here as
+// 32x32x16: weights go from the first result's registers into the second
+// product without leaving the lane.  The tile's codes are turned into bf16
+// once for the four waves: each thread takes D / 4 channels of a key and
+// D / 16 channels of 4 values, and writes keys as rows of tokens and values as
+// rows of channels, so every operand is one 16-byte LDS read.  Rows are 16
+// bytes longer than their data: 16 rows in turn then start on different
+// 16-byte pieces of the 256 bytes that LDS serves at once.
+// A wave's matrix and vector work overlap: the scores of the next tile are
+// multiplied while this one's weights are formed, and the codes of later
+// tiles are turned while the values are multiplied.  Keys are therefore
+// staged one tile further ahead than values; one barrier a tile.
+template <int DT, int D>
+__global__ __launch_bounds__(256, (kv_tiles_waves<DT, D>())) void kda_kv_tiles_kernel(KvAttendArgs a) {
+  constexpr int NQ = q_pieces<DT>(), NP = w_pieces_tiles<DT>();
+  constexpr int KT = 64;            // tokens of a tile
+  constexpr int KS = D / 16;        // products over the channels
+  constexpr int CB = D / 32;        // 32-channel blocks
+  constexpr int VC = D / 16;        // channels of a thread's values
+  constexpr int R = 128;
+  constexpr int KROW = 2 * D + 16, VROW = 2 * KT + 16;  // LDS bytes of a token's key, of a channel's values
+  constexpr int KBUF = KT * KROW, VBUF = D * VROW;
+  __shared__ __attribute__((aligned(16))) char k_sh[2 * KBUF];
+  __shared__ __attribute__((aligned(16))) char v_sh[2 * VBUF];
+
+  const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
+  const int i32 = lane % 32, half = lane / 32;
+  // The last row tiles see the most tokens and go first.  One sequence: a
+  // cached head's tiles stay on one XCD and its L2.  Several: lengths differ,
+  // and every XCD gets some of each.
+  const int units = a.t.n_seq * a.t.H;
+  const int turn = blockIdx.x / units;
+  const int unit = (blockIdx.x + (a.t.n_seq > 1 ? turn : 0)) % units;
+  const int sp = turn % a.n_splits, rt0 = a.row_tiles - 1 - turn / a.n_splits;
+  const int h = unit % a.t.H, s = unit / a.t.H;
+  const Seq q = seq_of(a.t, s);
+  if (q.skip) return;
+  const int64_t all_rows = static_cast<int64_t>(q.rows) * a.group;
+  const int block_bytes = kv_block_bytes(a.t.P, D);
+  const uint8_t* head0 = a.t.base + static_cast<int64_t>(h) * block_bytes;
+  const_i32* table = (const_i32*)(a.t.page_table + static_cast<int64_t>(s) * a.t.max_pages);
+
+  // -- a thread's share of a tile's codes: key kt, channels D / 4 kj..; values
+  // 4 vt .. 4 vt + 3, channels VC vo..  A wave's 16 tokens lie on one page.
+  const int kt = tid / 4, kj = tid % 4, vt = 4 * wave + lane % 4, vo = lane / 4;
+  // Values' row 16 n + vo holds channel VC vo + n: the channels that a lane
+  // ends up with are then neighbours.  4 tokens are half a 16-byte piece: a
+  // lane's 8 tokens in the product are 4 half .. + 3 and 8 + 4 half .. + 3 of 16.
+  const int k_to = kt * KROW + 16 * kj * (D / 32);
+  const int v_to = vo * VROW + 16 * (2 * (vt / 4) + vt % 2) + 8 * ((vt / 2) % 2);
+  const int k_at = i32 * KROW + 16 * half, v_at = i32 * VROW + 16 * half;
+
+  for (int64_t rt = rt0; rt * R < all_rows; rt += a.row_tiles) {
+    const int row0 = static_cast<int>(rt * R);
+    const int last_row = static_cast<int>(row0 + R < all_rows ? row0 + R : all_rows) - 1;
+    const int vis = q.past + last_row / a.group + 1;
+    const int splits = q.bad ? 1 : kv_splits(vis, a);
+    if (sp >= splits) continue;
+    const int t0 = q.bad ? 0 : sp * a.chunk;
+    const int t1 = q.bad ? 0 : sp == splits - 1 ? vis : t0 + a.chunk;
+    const int w_first = q.past + (row0 + 32 * wave) / a.group;  // the last token all of the wave's rows see
+
+    const int row = row0 + 32 * wave + i32;
+    const int r_in = row <= last_row ? row : last_row;
+    const int tok = r_in / a.group, g = r_in - tok * a.group;
+    const int limit = row <= last_row ? q.past + tok : -1;
+    u4 qf[NQ][KS];
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      u4 x[NQ];
+      load_query<DT>(a.q, (q.n0 + tok) * a.q_stride + (static_cast<int64_t>(h) * a.group + g) * D + 16 * ks + 8 * half,
+                     a.sign, x);
+#pragma unroll
+      for (int p = 0; p < NQ; ++p) qf[p][ks] = x[p];
+    }
+
+    uint32_t kc[D / 32], ke, vc[4], ve;
+    auto page_of = [&](int tb) __attribute__((always_inline)) {
+      const int t = tb + 16 * wave;
+      const int page = t < t1 ? table[t >> a.t.log_p] : -1;
+      return page < a.t.n_pages ? page : -1;
+    };
+    auto load_keys = [&](int tb) __attribute__((always_inline)) {
+      const int page = page_of(tb);
+      if (page >= 0) {
+        const uint8_t* blk = head0 + page * a.t.page_bytes;
+        const int r = (tb + kt) & (a.t.P - 1);
+        if constexpr (D == 128) {
+          const u4 x = *reinterpret_cast<const u4*>(blk + r * (D / 2) + 16 * kj);
+#pragma unroll
+          for (int m = 0; m < 4; ++m) kc[m] = x[m];
+        } else {
+          const u2 x = *reinterpret_cast<const u2*>(blk + r * (D / 2) + 8 * kj);
+          kc[0] = x[0], kc[1] = x[1];
+        }
+        ke = blk[kv_key_exps(a.t.P, D) + r * (D / kKvGroup) + kj * (D / 4) / kKvGroup];
+      } else {
+        ke = kKvPoison;  // scores NaN, seen only where the mask lets them
+#pragma unroll
+        for (int m = 0; m < D / 32; ++m) kc[m] = 0;
+      }
+    };
+    auto load_values = [&](int tb) __attribute__((always_inline)) {
+      const int page = page_of(tb);
+      if (page >= 0) {
+        const uint8_t* blk = head0 + page * a.t.page_bytes;
+        const int r = (tb + 4 * vt) & (a.t.P - 1);
+        const uint8_t* vp = blk + kv_value_codes(a.t.P, D) + r * (D / 2) + vo * (VC / 2);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (D == 128)
+            vc[e] = *reinterpret_cast<const uint32_t*>(vp + e * (D / 2));
+          else
+            vc[e] = *reinterpret_cast<const uint16_t*>(vp + e * (D / 2));
+        }
+        ve = *reinterpret_cast<const uint32_t*>(blk + kv_value_exps(a.t.P, D) + (vo * VC / kKvGroup) * a.t.P + r);
+      } else {
+        ve = 0x7F7F7F7Fu;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) vc[e] = 0;
+      }
+    };
+    // dword m of the key's codes
+    auto stage_key = [&](int buf, int m) __attribute__((always_inline)) {
+      const float ks = exp_scale(ke);
+      u4 x = {dequant2<0>(kc[m], ks), dequant2<1>(kc[m], ks), dequant2<2>(kc[m], ks), dequant2<3>(kc[m], ks)};
+      if (m == 0) x[0] = ke == kKvPoison ? 0x7FC07FC0u : x[0];
+      *reinterpret_cast<u4*>(k_sh + buf * KBUF + k_to + 16 * m) = x;
+    };
+    // values behind the last token may be anything: zeros
+    auto end_values = [&](int tb) __attribute__((always_inline)) {
+      if (tb + KT > t1) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (tb + 4 * vt + e >= t1) {
+            vc[e] = 0;
+            ve = (ve & ~(0xFFu << (8 * e))) | (127u << (8 * e));
+          }
+      }
+    };
+    // channels 2 c2 and 2 c2 + 1 of the 4 values
+    auto stage_value = [&](int buf, auto pick) __attribute__((always_inline)) {
+      constexpr int c2 = decltype(pick)::value;
+      uint32_t x[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = dequant2<c2>(vc[e], exp_scale((ve >> (8 * e)) & 0xFF));
+      *reinterpret_cast<u2*>(v_sh + buf * VBUF + 32 * c2 * VROW + v_to) = u2{pack_lo(x[0], x[1]), pack_lo(x[2], x[3])};
+      *reinterpret_cast<u2*>(v_sh + buf * VBUF + (32 * c2 + 16) * VROW + v_to) =
+          u2{pack_hi(x[0], x[1]), pack_hi(x[2], x[3])};
+    };
+    f16v zero;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) zero[e] = 0.0f;
+    // product i of a tile's scores: channels 16 (i / 2).., tokens 32 (i % 2)..
+    auto key_piece = [&](int buf, int i) __attribute__((always_inline)) {
+      const int ks = i / 2, b = i % 2;
+      return *reinterpret_cast<const u4*>(k_sh + buf * KBUF + k_at + 32 * ks + 32 * b * KROW);
+    };
+    auto score = [&](int i, u4 kf, f16v (&out)[2]) __attribute__((always_inline)) {
+#pragma unroll
+      for (int p = 0; p < NQ; ++p) out[i % 2] = mfma32(kf, qf[p][i / 2], i / 2 == 0 && p == 0 ? zero : out[i % 2]);
+    };
+    // product i of the outputs: tokens 16 (i / CB).., rows 32 (i % CB)..
+    auto value_piece = [&](int buf, int i) __attribute__((always_inline)) {
+      return *reinterpret_cast<const u4*>(v_sh + buf * VBUF + v_at + 32 * (i / CB) + 32 * (i % CB) * VROW);
+    };
+    f16v sc0[2], sc1[2];  // scores of tiles in turn
+
+    f16v o[CB];
+#pragma unroll
+    for (int c = 0; c < CB; ++c) o[c] = zero;
+    float mx = -INFINITY, sum = 0.0f;
+    load_keys(t0);
+    load_values(t0);
+#pragma unroll
+    for (int m = 0; m < D / 32; ++m) stage_key(0, m);
+    load_keys(t0 + KT);
+    end_values(t0);
+    stage_value(0, std::integral_constant<int, 0>{});
+    stage_value(0, std::integral_constant<int, 1>{});
+    if constexpr (D == 128) {
+      stage_value(0, std::integral_constant<int, 2>{});
+      stage_value(0, std::integral_constant<int, 3>{});
+    }
+    load_values(t0 + KT);
+#pragma unroll
+    for (int m = 0; m < D / 32; ++m) stage_key(1, m);
+    load_keys(t0 + 2 * KT);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2 * KS; ++i) score(i, key_piece(0, i), sc0);
+    auto top_score = [&](const f16v (&x)[2]) __attribute__((always_inline)) {
+      float y = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) y = max_nan(y, max_nan(x[0][e], x[1][e]));
+      return y;
+    };
+    float best = top_score(sc0);
+    auto step = [&](int tb, auto which, f16v (&sc)[2], f16v (&next)[2]) __attribute__((always_inline)) {
+      constexpr int buf = decltype(which)::value;
+      if (tb + KT - 1 > w_first) {
+        const int left = limit - tb - 4 * half;  // the last of the lane's tokens its row sees
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) sc[b][e] = 32 * b + 8 * (e / 4) + e % 4 > left ? -INFINITY : sc[b][e];
+        best = top_score(sc);
+      }
+      // the running maximum moves only when a score passes it by 8
+      if (__ballot(best * a.scale > mx + 8.0f) != 0) {
+        const float to = fmaxf(max_xor32(best * a.scale), mx);
+        const float keep = mx == to ? 1.0f : exp2_hw(mx - to);
+        mx = to;
+        sum *= keep;
+#pragma unroll
+        for (int c = 0; c < CB; ++c) o[c] *= keep;
+      }
+      end_values(tb + KT);
+      const float base = mx == -INFINITY ? 0.0f : -mx;
+      // -- this tile's weights, the next one's scores: after each product the
+      // vector work that fits beside it, operands read AHEAD products early
+      constexpr int AHEAD = 2;
+      u4 pf[4][NP], ring[AHEAD + 1];
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) ring[i] = key_piece(buf ^ 1, i);
+#pragma unroll
+      for (int i = 0; i < 2 * KS; ++i) {
+        if (i + AHEAD < 2 * KS) ring[(i + AHEAD) % (AHEAD + 1)] = key_piece(buf ^ 1, i + AHEAD);
+        score(i, ring[i % (AHEAD + 1)], next);
+        constexpr int EACH = 16 / KS;  // weights beside a product
+#pragma unroll
+        for (int k = EACH * i; k < EACH * (i + 1); k += 2) {
+          const int b = k / 16, e = k % 16;
+          const float w0 = exp2_hw(fmaf(sc[b][e], a.scale, base)), w1 = exp2_hw(fmaf(sc[b][e + 1], a.scale, base));
+          sum += w0 + w1;
+          uint32_t x[NP];
+          if constexpr (NP == 1) {
+            const bf2 y = {static_cast<__bf16>(w0), static_cast<__bf16>(w1)};
+            x[0] = __builtin_bit_cast(uint32_t, y);
+          } else {
+            split_pair<NP>(w0, w1, x);
+          }
+#pragma unroll
+          for (int p = 0; p < NP; ++p) pf[2 * b + e / 8][p][(e % 8) / 2] = x[p];
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      // -- this tile's values; later tiles' codes; the next scores' maximum
+      best = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) ring[i] = value_piece(buf, i);
+      auto output = [&](auto at) __attribute__((always_inline)) {
+        constexpr int i = decltype(at)::value, G = 4 * CB, E = 32 / G;
+        if (i + AHEAD < G) ring[(i + AHEAD) % (AHEAD + 1)] = value_piece(buf, i + AHEAD);
+#pragma unroll
+        for (int p = 0; p < NP; ++p) o[i % CB] = mfma32(ring[i % (AHEAD + 1)], pf[i / CB][p], o[i % CB]);
+        if constexpr (i % 4 == 0) stage_key(buf, i / 4);
+        if constexpr (i % 4 == 2) stage_value(buf ^ 1, std::integral_constant<int, i / 4>{});
+#pragma unroll
+        for (int k = E * i; k < E * (i + 1); ++k) best = max_nan(best, next[k % 2][k / 2]);
+        __builtin_amdgcn_sched_barrier(0);
+      };
+      each_of(output, std::make_integer_sequence<int, 4 * CB>{});
+      load_keys(tb + 3 * KT);
+      load_values(tb + 2 * KT);
+      __syncthreads();
+    };
+    for (int tb = t0; tb < t1; tb += 2 * KT) {
+      step(tb, std::integral_constant<int, 0>{}, sc0, sc1);
+      if (tb + KT >= t1) break;
+      step(tb + KT, std::integral_constant<int, 1>{}, sc1, sc0);
+    }
+
+    // -- rows out: element e of block c is row 8 (e / 4) + 4 half + e % 4 of
+    // 32 c.., channel 2 c + e / 8 of the VC at VC (row % 16)
+    sum = sum_xor32(sum);
+    if (row <= last_row) {
+      const int64_t at = (q.n0 + tok) * a.q_heads + static_cast<int64_t>(h) * a.group + g;
+      const int64_t slot = static_cast<int64_t>(sp) * a.t.n_tokens * a.q_heads + at;
+      const float inv = splits > 1 ? 1.0f : q.bad ? __builtin_nanf("") : sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int64_t c0 = VC * (8 * (e / 4) + 4 * half + e % 4);
+        float x[VC];
+#pragma unroll
+        for (int n = 0; n < VC; ++n) x[n] = o[n / 2][8 * (n % 2) + e] * inv;
+        if (splits == 1)
+          store_channels<DT>(a.out, at * D + c0, x);
+        else
+          store_channels<KDA_F32>(a.part, slot * D + c0, x);
+      }
+      if (splits > 1 && half == 0) {
+        a.part_ml[2 * slot] = mx;
+        a.part_ml[2 * slot + 1] = sum;
+      }
+    }
   }
 }
 
@@ -943,8 +1308,10 @@ extern "C" int kda_kv_attend(const kda_kv_pool* kv, const int32_t* page_table, i
   a.chunk = p.chunk;
   a.n_splits = p.n_splits;
   a.row_tiles = p.row_tiles;
-  a.scale = std::fabs(scale) * 1.44269504088896340736f;
-  a.negate = scale < 0.0f;
+  // a zero scale stays above zero, so that a masked score (-infinity) times it
+  // is what it was; 2^-126 times any score leaves its weight 1
+  a.scale = std::fmax(std::fabs(scale) * 1.44269504088896340736f, 0x1p-126f);
+  a.sign = scale < 0.0f ? -1.0f : 1.0f;
   a.part = static_cast<float*>(workspace);
   a.part_ml = a.part == nullptr ? nullptr : a.part + static_cast<int64_t>(p.n_splits) * n_tokens * q_heads * kv->D;
   const int64_t blocks = static_cast<int64_t>(n_seq) * kv->H * p.row_tiles * p.n_splits;
@@ -953,7 +1320,9 @@ extern "C" int kda_kv_attend(const kda_kv_pool* kv, const int32_t* page_table, i
   return status(by_type(dtype, kv->D, [&](auto t, auto d) {
     constexpr int DT = decltype(t)::value, D = decltype(d)::value;
     const dim3 grid(static_cast<uint32_t>(blocks));
-    if (p.tile_rows == 16)
+    if (p.tile_rows == 128)
+      hipLaunchKernelGGL((kda_kv_tiles_kernel<DT, D>), grid, dim3(256), 0, st, a);
+    else if (p.tile_rows == 16)
       hipLaunchKernelGGL((kda_kv_rows_kernel<DT, D, 1, 4>), grid, dim3(256), 0, st, a);
     else
       hipLaunchKernelGGL((kda_kv_rows_kernel<DT, D, 2, 4>), grid, dim3(256), 0, st, a);

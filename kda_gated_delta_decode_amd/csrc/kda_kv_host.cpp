@@ -27,7 +27,7 @@ KvPlan kv_plan(int32_t H, int32_t D, int32_t n_seq, int64_t n_tokens, int32_t ma
   (void)dtype;
   KvPlan p;
   const int64_t rows = static_cast<int64_t>(max_rows < n_tokens ? max_rows : n_tokens) * (q_heads / H);
-  p.tile_rows = rows <= 16 ? 16 : 32;
+  p.tile_rows = rows <= 16 ? 16 : rows <= 64 ? 32 : 128;
   p.row_tiles = static_cast<int32_t>((rows + p.tile_rows - 1) / p.tile_rows);
   if (p.row_tiles < 1) p.row_tiles = 1;
   // Splits: enough workgroups for every compute unit to hold several, and no
