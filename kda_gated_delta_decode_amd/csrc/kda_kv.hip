@@ -464,6 +464,11 @@ __device__ __forceinline__ float max_xor32(float x) {
   return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
+// Waves a SIMD: three in 168 registers hide more of a step's latency than two
+// (64 ragged requests at up to 8192 tokens: 85 -> 81 us; four would spill).
+template <int DT, int D, int NT>
+constexpr int kv_rows_waves() { return NT == 1 && (DT != KDA_F32 || D == 64) ? 3 : NT == 1 ? 2 : 1; }
+
 // Few rows: 16 * NT rows of one sequence and cached head against one split of
 // its tokens, over NW waves.
 //
@@ -480,7 +485,7 @@ __device__ __forceinline__ float max_xor32(float x) {
 // loaded as soon as the scores have used this step's, its values likewise, so
 // one set of registers keeps loads in flight all the time.
 template <int DT, int D, int NT, int NW>
-__global__ __launch_bounds__(64 * NW) void kda_kv_rows_kernel(KvAttendArgs a) {
+__global__ __launch_bounds__(64 * NW, (kv_rows_waves<DT, D, NT>())) void kda_kv_rows_kernel(KvAttendArgs a) {
   constexpr int NQ = q_pieces<DT>(), NP = w_pieces<DT>();
   constexpr int M = D / 32;   // products over the channels
   constexpr int C = D / 16;   // channels of a lane in the second product, and its row tiles
@@ -491,20 +496,34 @@ __global__ __launch_bounds__(64 * NW) void kda_kv_rows_kernel(KvAttendArgs a) {
 
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int i16 = lane % 16, j = lane / 16;
-  // block -> (sequence, cached head, split, row tile): row tiles that read
-  // the same tokens are neighbours on one XCD
-  const int id = tile_of_block(blockIdx.x, gridDim.x);
-  const int rt0 = id % a.row_tiles;
-  const int sp = (id / a.row_tiles) % a.n_splits;
-  const int h = (id / a.row_tiles / a.n_splits) % a.t.H;
-  const int s = id / a.row_tiles / a.n_splits / a.t.H;
+  // block -> (split, sequence, cached head, row tile).  Row tiles, which read
+  // the same tokens, are neighbours on one XCD; with one of them the heads go
+  // round the XCDs, so each has a like share of every sequence.
+  const int id = a.row_tiles > 1 ? tile_of_block(blockIdx.x, gridDim.x) : blockIdx.x;
+  const int rt0 = id % a.row_tiles, unit = (id / a.row_tiles) % (a.t.n_seq * a.t.H);
+  const int sp = id / a.row_tiles / (a.t.n_seq * a.t.H);
+  const int h = unit % a.t.H, s = unit / a.t.H;
+  const int t0 = sp * a.chunk;
+  // Page ids of this wave's next 32 steps, two tiles each, loaded at once: a
+  // lookup is then a register read, with no load in front of the rows'.  They
+  // are asked for before the sequence's length is known.
+  const int32_t* table = a.t.page_table + static_cast<int64_t>(s) * a.t.max_pages;
+  auto load_pages = [&](int from) __attribute__((always_inline)) {
+    const int64_t at = (static_cast<int64_t>(from) + 32 * NW * (lane / 2) + 16 * (lane % 2)) >> a.t.log_p;
+    return at < a.t.max_pages ? table[at] : -1;
+  };
+  const int pages0 = load_pages(t0 + 32 * wave);
   const Seq q = seq_of(a.t, s);
   if (q.skip) return;
   const int64_t all_rows = static_cast<int64_t>(q.rows) * a.group;
 
   const int block_bytes = kv_block_bytes(a.t.P, D);
   const uint8_t* head0 = a.t.base + static_cast<int64_t>(h) * block_bytes;
-  const_i32* table = (const_i32*)(a.t.page_table + static_cast<int64_t>(s) * a.t.max_pages);
+  // the lane's places in a block, from a tile's first token row
+  const uint32_t k_off = i16 * (D / 2) + j * (D / 8);
+  const uint32_t ke_off = kv_key_exps(a.t.P, D) + i16 * (D / kKvGroup) + j * (D / 4) / kKvGroup;
+  const uint32_t v_off = kv_value_codes(a.t.P, D) + 4 * j * (D / 2) + i16 * (D / 32);
+  const uint32_t ve_off = kv_value_exps(a.t.P, D) + (i16 * C / kKvGroup) * a.t.P + 4 * j;
 
   // Tiles beyond those the launch has blocks for are walked by the same blocks.
   for (int64_t rt = rt0; rt * R < all_rows; rt += a.row_tiles) {
@@ -513,7 +532,6 @@ __global__ __launch_bounds__(64 * NW) void kda_kv_rows_kernel(KvAttendArgs a) {
     const int vis = q.past + last_row / a.group + 1;  // tokens the last row sees
     const int splits = q.bad ? 1 : kv_splits(vis, a);
     if (sp >= splits) continue;
-    const int t0 = q.bad ? 0 : sp * a.chunk;
     const int t1 = q.bad ? 0 : sp == splits - 1 ? vis : t0 + a.chunk;
     const int first_limit = q.past + row0 / a.group;  // the last token every row sees
 
@@ -548,63 +566,47 @@ __global__ __launch_bounds__(64 * NW) void kda_kv_rows_kernel(KvAttendArgs a) {
 
     uint32_t kc[2][M], ke[2];  // keys: token i16 of two 16-token tiles, D / 4 channels of it
     uint32_t vc[8], ve[2];     // values: D / 16 channels of tokens 4j + r of both tiles
-    // The page of a tile; -1 if it does not exist or no token is left.
-    auto page_of = [&](int t) __attribute__((always_inline)) {
-      const int page = t < t1 ? table[t >> a.t.log_p] : -1;
-      return page < a.t.n_pages ? page : -1;
-    };
-    // without a page: keys that score NaN (seen only where the mask lets
-    // them), values of zero
-    auto load_keys = [&](int tb) __attribute__((always_inline)) {
+    int tb = t0 + 32 * wave, step = 0;
+    int pages = pages0;
+    int kp[2], vp[2];  // pages of the keys and values in flight; -1: no such page, or no token left
+    auto load_keys = [&](int t) __attribute__((always_inline)) {
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        const int page = page_of(tb + 16 * b);
-        if (page >= 0) {
-          const uint8_t* blk = head0 + page * a.t.page_bytes;
-          const int row = ((tb + 16 * b) & (a.t.P - 1)) + i16;
-          const uint8_t* kp = blk + row * (D / 2) + j * (D / 8);
-          if constexpr (D == 128) {
-            const u4 x = *reinterpret_cast<const u4*>(kp);
+        const int page = __builtin_amdgcn_readlane(pages, 2 * (step % 32) + b);
+        kp[b] = t + 16 * b < t1 && page < a.t.n_pages ? page : -1;
+        const uint8_t* blk = head0 + (kp[b] < 0 ? 0 : kp[b]) * a.t.page_bytes;
+        const uint32_t row = (t + 16 * b) & (a.t.P - 1);
+        const uint8_t* at = blk + row * (D / 2);
+        if constexpr (D == 128) {
+          const u4 x = *reinterpret_cast<const u4*>(at + k_off);
 #pragma unroll
-            for (int m = 0; m < M; ++m) kc[b][m] = x[m];
-          } else {
-            const u2 x = *reinterpret_cast<const u2*>(kp);
-#pragma unroll
-            for (int m = 0; m < M; ++m) kc[b][m] = x[m];
-          }
-          ke[b] = blk[kv_key_exps(a.t.P, D) + row * (D / kKvGroup) + j * (D / 4) / kKvGroup];
+          for (int m = 0; m < M; ++m) kc[b][m] = x[m];
         } else {
-          ke[b] = kKvPoison;
+          const u2 x = *reinterpret_cast<const u2*>(at + k_off);
 #pragma unroll
-          for (int m = 0; m < M; ++m) kc[b][m] = 0;
+          for (int m = 0; m < M; ++m) kc[b][m] = x[m];
         }
+        ke[b] = (blk + row * (D / kKvGroup))[ke_off];
       }
     };
-    auto load_values = [&](int tb) __attribute__((always_inline)) {
+    auto load_values = [&](int t) __attribute__((always_inline)) {
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        const int page = page_of(tb + 16 * b);
-        if (page >= 0) {
-          const uint8_t* blk = head0 + page * a.t.page_bytes;
-          const int row = ((tb + 16 * b) & (a.t.P - 1)) + 4 * j;
-          const uint8_t* vp = blk + kv_value_codes(a.t.P, D) + row * (D / 2) + i16 * (D / 32);
+        vp[b] = kp[b];
+        const uint8_t* blk = head0 + (vp[b] < 0 ? 0 : vp[b]) * a.t.page_bytes;
+        const uint32_t row = (t + 16 * b) & (a.t.P - 1);
+        const uint8_t* at = blk + row * (D / 2);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            if constexpr (D == 128)
-              vc[4 * b + r] = *reinterpret_cast<const uint32_t*>(vp + r * (D / 2));
-            else
-              vc[4 * b + r] = *reinterpret_cast<const uint16_t*>(vp + r * (D / 2));
-          }
-          ve[b] = *reinterpret_cast<const uint32_t*>(blk + kv_value_exps(a.t.P, D) + (i16 * C / kKvGroup) * a.t.P + row);
-        } else {
-          ve[b] = 0x7F7F7F7Fu;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) vc[4 * b + r] = 0;
+        for (int r = 0; r < 4; ++r) {
+          if constexpr (D == 128)
+            vc[4 * b + r] = *reinterpret_cast<const uint32_t*>(at + v_off + r * (D / 2));
+          else
+            vc[4 * b + r] = *reinterpret_cast<const uint16_t*>(at + v_off + r * (D / 2));
         }
+        ve[b] = *reinterpret_cast<const uint32_t*>(blk + row + ve_off);
       }
     };
 
-    int tb = t0 + 32 * wave;
     if (tb < t1) {
       load_keys(tb);
       load_values(tb);
@@ -621,17 +623,22 @@ __global__ __launch_bounds__(64 * NW) void kda_kv_rows_kernel(KvAttendArgs a) {
         for (int m = 0; m < M; ++m) {
           u4 kf = {dequant2<0>(kc[b][m], ks), dequant2<1>(kc[b][m], ks), dequant2<2>(kc[b][m], ks),
                    dequant2<3>(kc[b][m], ks)};
-          if (m == 0) kf[0] = ke[b] == kKvPoison ? 0x7FC07FC0u : kf[0];
+          // a poisoned key, or no page: scores NaN, seen where the mask lets them
+          if (m == 0) kf[0] = ke[b] == kKvPoison || kp[b] < 0 ? 0x7FC07FC0u : kf[0];
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int p = 0; p < NQ; ++p) sc[n][b] = mfma16(kf, qf[n][p][m], sc[n][b]);
         }
       }
-      if (tb + 32 * NW < t1) load_keys(tb + 32 * NW);
-      // -- tokens behind a row's own; values there may be anything, and
-      // become zeros
-      const bool tail = tb + 31 > first_limit;
+      if (tb + 32 * NW < t1) {
+        if (++step % 32 == 0) pages = load_pages(tb + 32 * NW);
+        load_keys(tb + 32 * NW);
+      }
+      __builtin_amdgcn_sched_barrier(0);  // here and below: fewer registers alive
+      // -- tokens behind a row's own; values there, or of no page, may be
+      // anything, and become zeros
+      const bool tail = tb + 31 > first_limit || vp[0] < 0 || vp[1] < 0;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -644,8 +651,9 @@ __global__ __launch_bounds__(64 * NW) void kda_kv_rows_kernel(KvAttendArgs a) {
             const int t = tb + 16 * b + 4 * j + r;
 #pragma unroll
             for (int n = 0; n < NT; ++n) sc[n][b][r] = t > limit[n] ? -INFINITY : sc[n][b][r];
-            vc[4 * b + r] = t >= t1 ? 0 : vc[4 * b + r];
-            ve[b] = t >= t1 ? (ve[b] & ~(0xFFu << (8 * r))) | (127u << (8 * r)) : ve[b];
+            const bool none = t >= t1 || vp[b] < 0;
+            vc[4 * b + r] = none ? 0 : vc[4 * b + r];
+            ve[b] = none ? (ve[b] & ~(0xFFu << (8 * r))) | (127u << (8 * r)) : ve[b];
           }
       }
       // -- weights: the running maximum is moved only when a score passes it
@@ -678,6 +686,7 @@ __global__ __launch_bounds__(64 * NW) void kda_kv_rows_kernel(KvAttendArgs a) {
           for (int p = 0; p < NP; ++p) pf[n][p][e] = t[p];
         }
       }
+      __builtin_amdgcn_sched_barrier(0);
       // -- values: two channels of the 8 tokens at a time
       auto channels = [&](auto pick) __attribute__((always_inline)) {
         constexpr int c = decltype(pick)::value;
@@ -693,6 +702,7 @@ __global__ __launch_bounds__(64 * NW) void kda_kv_rows_kernel(KvAttendArgs a) {
             o[n][2 * c] = mfma16(even, pf[n][p], o[n][2 * c]);
             o[n][2 * c + 1] = mfma16(odd, pf[n][p], o[n][2 * c + 1]);
           }
+        __builtin_amdgcn_sched_barrier(0);
       };
       channels(std::integral_constant<int, 0>{});
       channels(std::integral_constant<int, 1>{});
@@ -1078,16 +1088,20 @@ __global__ __launch_bounds__(256, (kv_tiles_waves<DT, D>())) void kda_kv_tiles_k
   }
 }
 
-// Joins the splits of a row: one wave a row, D / 8 lanes across its channels
-// and the rest across its splits, so that 128 splits take 32 loads of a lane
-// (8 in flight) instead of 128 one after the other.
-template <int DT, int D>
+// Joins the splits of a row, ROWS rows a block of four waves: with few splits a
+// wave a row, with many all four on one.  D / 8 lanes lie across the channels,
+// the others (and the waves) across the splits, each with a maximum and sum of
+// its own, so that no load waits for another split's.
+template <int DT, int D, int ROWS>
 __global__ __launch_bounds__(256) void kda_kv_join_kernel(KvAttendArgs a, int tile_rows) {
-  constexpr int PER = D / 8, G = 64 / PER;
-  const int lane = threadIdx.x % 64, c = 8 * (lane % PER), grp = lane / PER;
-  const int slices = tile_rows / 4;
+  constexpr int PER = D / 8, W = 4 / ROWS;  // lanes of a row's channels, waves of a row
+  constexpr int G = 64 / PER * W;           // splits taken at once
+  __shared__ float part_sh[W][PER][10];
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  const int c = 8 * (lane % PER), grp = lane / PER + (W > 1 ? 64 / PER * wave : 0);
+  const int slices = tile_rows / ROWS;
   const int id = blockIdx.x;
-  const int r = (id % slices) * 4 + threadIdx.x / 64;
+  const int r = (id % slices) * ROWS + (W > 1 ? 0 : wave);
   const int rt0 = (id / slices) % a.row_tiles;
   const int h = (id / slices / a.row_tiles) % a.t.H;
   const int s = id / slices / a.row_tiles / a.t.H;
@@ -1102,32 +1116,55 @@ __global__ __launch_bounds__(256) void kda_kv_join_kernel(KvAttendArgs a, int ti
     if (splits <= 1) continue;  // written already
     const int tok = static_cast<int>(row / a.group), g = static_cast<int>(row - static_cast<int64_t>(tok) * a.group);
     const int64_t at = (q.n0 + tok) * a.q_heads + static_cast<int64_t>(h) * a.group + g;
-    float top = -INFINITY;
-    for (int i = lane; i < splits; i += 64) top = fmaxf(top, a.part_ml[2 * (i * stride + at)]);
+    float acc[8] = {}, total = 0.0f, top = -INFINITY;
+    // (m, l, x) joins this lane's; a side without a finite maximum holds
+    // zeros, or NaN from a page that does not exist or a poisoned key
+    auto join = [&](float m, float l, const float (&x)[8]) __attribute__((always_inline)) {
+      const float to = fmaxf(top, m);
+      const float f = top == to ? 1.0f : exp2_hw(top - to), y = m == to ? 1.0f : exp2_hw(m - to);
+      top = to;
+      total = fmaf(total, f, l * y);
 #pragma unroll
-    for (int m = 1; m < 64; m *= 2) top = fmaxf(top, __shfl_xor(top, m));
-    float acc[8] = {}, total = 0.0f;
+      for (int e = 0; e < 8; ++e) acc[e] = fmaf(acc[e], f, x[e] * y);
+    };
 #pragma unroll 4
     for (int i = grp; i < splits; i += G) {
       const int64_t slot = i * stride + at;
-      const float m = a.part_ml[2 * slot], l = a.part_ml[2 * slot + 1];
       float x[8];
       load8<KDA_F32>(a.part, slot * D + c, x);
-      const float f = m == -INFINITY ? (top == -INFINITY ? 1.0f : 0.0f) : exp2_hw(m - top);
-      total += m == -INFINITY ? l : l * f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] = fmaf(x[e], f, acc[e]);
+      join(a.part_ml[2 * slot], a.part_ml[2 * slot + 1], x);
     }
 #pragma unroll
     for (int m = PER; m < 64; m *= 2) {
-      total += __shfl_xor(total, m);
+      float x[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] += __shfl_xor(acc[e], m);
+      for (int e = 0; e < 8; ++e) x[e] = __shfl_xor(acc[e], m);
+      const float om = __shfl_xor(top, m), ol = __shfl_xor(total, m);
+      join(om, ol, x);
+    }
+    if constexpr (W > 1) {
+      if (lane < PER) {
+        part_sh[wave][lane][8] = top;
+        part_sh[wave][lane][9] = total;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) part_sh[wave][lane][e] = acc[e];
+      }
+      __syncthreads();
+      if (threadIdx.x < PER) {
+#pragma unroll
+        for (int w = 1; w < W; ++w) {
+          float x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = part_sh[w][lane][e];
+          join(part_sh[w][lane][8], part_sh[w][lane][9], x);
+        }
+      }
+      __syncthreads();
     }
     const float inv = total == 0.0f ? 0.0f : 1.0f / total;
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] *= inv;
-    if (grp == 0) store8<DT>(a.out, at * D + c, acc);
+    if (lane < PER && (W == 1 || wave == 0)) store8<DT>(a.out, at * D + c, acc);
   }
 }
 
@@ -1328,10 +1365,13 @@ extern "C" int kda_kv_attend(const kda_kv_pool* kv, const int32_t* page_table, i
       hipLaunchKernelGGL((kda_kv_rows_kernel<DT, D, 2, 4>), grid, dim3(256), 0, st, a);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && p.n_splits > 1) {
-      const int slices = p.tile_rows / 4;
-      hipLaunchKernelGGL((kda_kv_join_kernel<DT, D>),
-                         dim3(static_cast<uint32_t>(n_seq) * kv->H * p.row_tiles * slices), dim3(256), 0, st, a,
-                         p.tile_rows);
+      // one wave up to 8 splits a row (2 rounds of loads), else a block
+      const uint32_t tiles = static_cast<uint32_t>(n_seq) * kv->H * p.row_tiles;
+      if (p.n_splits <= 8)
+        hipLaunchKernelGGL((kda_kv_join_kernel<DT, D, 4>), dim3(tiles * (p.tile_rows / 4)), dim3(256), 0, st, a,
+                           p.tile_rows);
+      else
+        hipLaunchKernelGGL((kda_kv_join_kernel<DT, D, 1>), dim3(tiles * p.tile_rows), dim3(256), 0, st, a, p.tile_rows);
       e = hipGetLastError();
     }
     return e;

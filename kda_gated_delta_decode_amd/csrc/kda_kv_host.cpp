@@ -30,15 +30,33 @@ KvPlan kv_plan(int32_t H, int32_t D, int32_t n_seq, int64_t n_tokens, int32_t ma
   p.tile_rows = rows <= 16 ? 16 : rows <= 64 ? 32 : 128;
   p.row_tiles = static_cast<int32_t>((rows + p.tile_rows - 1) / p.tile_rows);
   if (p.row_tiles < 1) p.row_tiles = 1;
-  // Splits: enough workgroups for every compute unit to hold several, and no
-  // split shorter than 128 tokens (one step of each of its four waves).
-  const int64_t units = static_cast<int64_t>(n_seq) * H * p.row_tiles;
-  int64_t want = (4 * 256 + units - 1) / (units < 1 ? 1 : units);
-  const int64_t most = (max_kv_len + 127) / 128;
-  if (want > most) want = most;
-  if (want < 1) want = 1;
-  int64_t chunk = (max_kv_len + want - 1) / want;
-  chunk = (chunk + 127) / 128 * 128;
+  const int64_t units = static_cast<int64_t>(n_seq < 1 ? 1 : n_seq) * H * p.row_tiles;
+  const auto per = [](int64_t x, int64_t n) { return (x + n - 1) / n; };
+  // n splits of a cache, none shorter than `least`
+  const auto chunk_of = [&](int64_t blocks, int64_t least) {
+    const int64_t n = blocks / units;
+    const int64_t c = per(max_kv_len, n < 1 ? 1 : n);
+    return c < least ? least : c;
+  };
+  int64_t chunk;
+  if (p.tile_rows < 128) {
+    // Few rows.  768 workgroups are resident at once (three a compute unit).
+    // One sequence: its splits are all alike, and one round of them is best
+    // (131072 tokens, 8 cached heads: 38 us; 39.5 with 1024, 43 with 1536).
+    // Several: their lengths differ, and twice as many leave less of the chip
+    // idle at the end (64 ragged requests: 75 us; 81 with 768, 77 with 2048).
+    // A split costs as much as some 200 tokens, so none is shorter than 512
+    // (8 requests of 4097: 27 us; 31 with 384) unless the chip would stay empty.
+    chunk = chunk_of(n_seq > 1 ? 1536 : 768, 512);
+    if (per(max_kv_len, chunk) * units < 256) chunk = chunk_of(256, 128);
+  } else {
+    // Many rows, two workgroups a compute unit: one round of them for one
+    // sequence, two for several, whose rows and lengths differ (4 chunks of up
+    // to 700 rows on up to 16000 tokens: 305 us with 3 splits; 450, 380 and 335
+    // with 1, 2 and 4).
+    chunk = n_seq > 1 ? chunk_of(per(1024, units) * units, 1024) : chunk_of(512, 1024);
+  }
+  chunk = per(chunk, 128) * 128;
   if (chunk < 128) chunk = 128;
   p.chunk = static_cast<int32_t>(chunk);
   p.n_splits = static_cast<int32_t>((max_kv_len + chunk - 1) / chunk);
