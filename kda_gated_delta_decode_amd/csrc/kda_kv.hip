@@ -401,7 +401,7 @@ __device__ __forceinline__ Seq seq_of(const KvTables& t, int s) {
 // Splits of a tile whose last row sees `vis` tokens; the last split takes what
 // the launch had no blocks for.
 __device__ __forceinline__ int kv_splits(int vis, const KvAttendArgs& a) {
-  const int n = static_cast<int>((static_cast<int64_t>(vis) + a.chunk - 1) / a.chunk);
+  const int n = static_cast<int>((static_cast<uint32_t>(vis) + a.chunk - 1) / static_cast<uint32_t>(a.chunk));
   return n < a.n_splits ? n : a.n_splits;
 }
 
@@ -465,9 +465,10 @@ __device__ __forceinline__ float max_xor32(float x) {
 }
 
 // Waves a SIMD: three in 168 registers hide more of a step's latency than two
-// (64 ragged requests at up to 8192 tokens: 85 -> 81 us; four would spill).
-template <int DT, int D, int NT>
-constexpr int kv_rows_waves() { return NT == 1 && (DT != KDA_F32 || D == 64) ? 3 : NT == 1 ? 2 : 1; }
+// (64 ragged requests at up to 8192 tokens: 85 -> 81 us; four would spill); with
+// two row tiles two (32 rows of 8 requests at 4097 tokens: 28 -> 26 us).
+template <int NT>
+constexpr int kv_rows_waves() { return NT == 1 ? 3 : 2; }
 
 // Few rows: 16 * NT rows of one sequence and cached head against one split of
 // its tokens, over NW waves.
@@ -485,7 +486,7 @@ constexpr int kv_rows_waves() { return NT == 1 && (DT != KDA_F32 || D == 64) ? 3
 // loaded as soon as the scores have used this step's, its values likewise, so
 // one set of registers keeps loads in flight all the time.
 template <int DT, int D, int NT, int NW>
-__global__ __launch_bounds__(64 * NW, (kv_rows_waves<DT, D, NT>())) void kda_kv_rows_kernel(KvAttendArgs a) {
+__global__ __launch_bounds__(64 * NW, kv_rows_waves<NT>()) void kda_kv_rows_kernel(KvAttendArgs a) {
   constexpr int NQ = q_pieces<DT>(), NP = w_pieces<DT>();
   constexpr int M = D / 32;   // products over the channels
   constexpr int C = D / 16;   // channels of a lane in the second product, and its row tiles
@@ -521,9 +522,8 @@ __global__ __launch_bounds__(64 * NW, (kv_rows_waves<DT, D, NT>())) void kda_kv_
   const uint8_t* head0 = a.t.base + static_cast<int64_t>(h) * block_bytes;
   // the lane's places in a block, from a tile's first token row
   const uint32_t k_off = i16 * (D / 2) + j * (D / 8);
-  const uint32_t ke_off = kv_key_exps(a.t.P, D) + i16 * (D / kKvGroup) + j * (D / 4) / kKvGroup;
-  const uint32_t v_off = kv_value_codes(a.t.P, D) + 4 * j * (D / 2) + i16 * (D / 32);
-  const uint32_t ve_off = kv_value_exps(a.t.P, D) + (i16 * C / kKvGroup) * a.t.P + 4 * j;
+  const uint32_t v_off = 4 * j * (D / 2) + i16 * (D / 32);
+  const uint32_t ve_off = (i16 * C / kKvGroup) * a.t.P + 4 * j;
 
   // Tiles beyond those the launch has blocks for are walked by the same blocks.
   for (int64_t rt = rt0; rt * R < all_rows; rt += a.row_tiles) {
@@ -586,7 +586,7 @@ __global__ __launch_bounds__(64 * NW, (kv_rows_waves<DT, D, NT>())) void kda_kv_
 #pragma unroll
           for (int m = 0; m < M; ++m) kc[b][m] = x[m];
         }
-        ke[b] = (blk + row * (D / kKvGroup))[ke_off];
+        ke[b] = (blk + kv_key_exps(a.t.P, D) + row * (D / kKvGroup))[k_off / 16];  // 16 bytes of codes an exponent
       }
     };
     auto load_values = [&](int t) __attribute__((always_inline)) {
@@ -595,7 +595,7 @@ __global__ __launch_bounds__(64 * NW, (kv_rows_waves<DT, D, NT>())) void kda_kv_
         vp[b] = kp[b];
         const uint8_t* blk = head0 + (vp[b] < 0 ? 0 : vp[b]) * a.t.page_bytes;
         const uint32_t row = (t + 16 * b) & (a.t.P - 1);
-        const uint8_t* at = blk + row * (D / 2);
+        const uint8_t* at = blk + kv_value_codes(a.t.P, D) + row * (D / 2);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           if constexpr (D == 128)
@@ -603,7 +603,7 @@ __global__ __launch_bounds__(64 * NW, (kv_rows_waves<DT, D, NT>())) void kda_kv_
           else
             vc[4 * b + r] = *reinterpret_cast<const uint16_t*>(at + v_off + r * (D / 2));
         }
-        ve[b] = *reinterpret_cast<const uint32_t*>(blk + row + ve_off);
+        ve[b] = *reinterpret_cast<const uint32_t*>(blk + kv_value_exps(a.t.P, D) + row + ve_off);
       }
     };
 
@@ -624,11 +624,12 @@ __global__ __launch_bounds__(64 * NW, (kv_rows_waves<DT, D, NT>())) void kda_kv_
           u4 kf = {dequant2<0>(kc[b][m], ks), dequant2<1>(kc[b][m], ks), dequant2<2>(kc[b][m], ks),
                    dequant2<3>(kc[b][m], ks)};
           // a poisoned key, or no page: scores NaN, seen where the mask lets them
-          if (m == 0) kf[0] = ke[b] == kKvPoison || kp[b] < 0 ? 0x7FC07FC0u : kf[0];
+          if (m == 0) kf[0] |= ke[b] == kKvPoison || kp[b] < 0 ? ~0u : 0u;
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int p = 0; p < NQ; ++p) sc[n][b] = mfma16(kf, qf[n][p][m], sc[n][b]);
+          if constexpr (NQ == 3) __builtin_amdgcn_sched_barrier(0);
         }
       }
       if (tb + 32 * NW < t1) {
@@ -713,24 +714,29 @@ __global__ __launch_bounds__(64 * NW, (kv_rows_waves<DT, D, NT>())) void kda_kv_
       if (tb + 32 * NW < t1) load_values(tb + 32 * NW);
     }
 
-    // -- join the waves: row n of a tile, channels C (4j + r) + m
+    // -- join the waves: row n of a tile, channels C (4j + r) + m.  The lane's
+    // place is derived from an opaque thread id: hoisted out of the loop over
+    // tiles, these addresses would be spilled over the steps.
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));
+    const int e16 = tid % 16, ej = tid % 64 / 16;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const float total = sum_xor32(sum_xor16(sum[n]));
-      if (j == 0) {
-        ml_sh[wave][16 * n + i16][0] = mx[n];
-        ml_sh[wave][16 * n + i16][1] = total;
+      if (ej == 0) {
+        ml_sh[wave][16 * n + e16][0] = mx[n];
+        ml_sh[wave][16 * n + e16][1] = total;
       }
 #pragma unroll
       for (int r = 0; r < 4; ++r)
 #pragma unroll
         for (int m = 0; m < C; m += 4)
-          *reinterpret_cast<f4*>(&o_sh[wave][16 * n + i16][C * (4 * j + r) + m]) =
+          *reinterpret_cast<f4*>(&o_sh[wave][16 * n + e16][C * (4 * ej + r) + m]) =
               f4{o[n][m][r], o[n][m + 1][r], o[n][m + 2][r], o[n][m + 3][r]};
     }
     __syncthreads();
     constexpr int PER = D / 8;  // threads of a row, 8 channels each
-    for (int it = threadIdx.x; it < R * PER; it += 64 * NW) {
+    for (int it = tid; it < R * PER; it += 64 * NW) {
       const int r = it / PER, c = 8 * (it % PER), row = row0 + r;
       if (row > last_row) continue;
       float top = -INFINITY;
@@ -915,7 +921,7 @@ __global__ __launch_bounds__(256, (kv_tiles_waves<DT, D>())) void kda_kv_tiles_k
     auto stage_key = [&](int buf, int m) __attribute__((always_inline)) {
       const float ks = exp_scale(ke);
       u4 x = {dequant2<0>(kc[m], ks), dequant2<1>(kc[m], ks), dequant2<2>(kc[m], ks), dequant2<3>(kc[m], ks)};
-      if (m == 0) x[0] = ke == kKvPoison ? 0x7FC07FC0u : x[0];
+      if (m == 0) x[0] |= ke == kKvPoison ? ~0u : 0u;
       *reinterpret_cast<u4*>(k_sh + buf * KBUF + k_to + 16 * m) = x;
     };
     // values behind the last token may be anything: zeros
@@ -1359,9 +1365,9 @@ extern "C" int kda_kv_attend(const kda_kv_pool* kv, const int32_t* page_table, i
     const dim3 grid(static_cast<uint32_t>(blocks));
     if (p.tile_rows == 128)
       hipLaunchKernelGGL((kda_kv_tiles_kernel<DT, D>), grid, dim3(256), 0, st, a);
-    else if (p.tile_rows == 16)
+    else if (DT == KDA_F32 || p.tile_rows == 16)
       hipLaunchKernelGGL((kda_kv_rows_kernel<DT, D, 1, 4>), grid, dim3(256), 0, st, a);
-    else
+    else if constexpr (DT != KDA_F32)
       hipLaunchKernelGGL((kda_kv_rows_kernel<DT, D, 2, 4>), grid, dim3(256), 0, st, a);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && p.n_splits > 1) {
