@@ -565,7 +565,7 @@ def make_kv_pool(pool) -> kda_kv_pool:
     """kda_kv_pool describing a contiguous uint8 GPU tensor of kv_pool_shape."""
     import torch
     _on_gpu(pool, "pool")
-    if pool.dtype != torch.uint8 or pool.dim() != 4 or not pool.is_contiguous():
+    if pool.dtype is not torch.uint8 or pool.dim() != 4 or not pool.is_contiguous():
         raise ValueError("a cache must be a contiguous uint8 tensor [n_pages, H, page_tokens, 17 D / 16]")
     n_pages, H, P, width = pool.shape
     if width % 17:
@@ -573,59 +573,74 @@ def make_kv_pool(pool) -> kda_kv_pool:
     return kda_kv_pool(pool.data_ptr(), n_pages, P, H, width // 17 * 16)
 
 
-def _rows(t, name, pool, heads, D, dtype, n_tokens):
-    """Address and token stride of a token tensor [n_tokens, heads, D] whose
-    heads and channels lie without gaps."""
-    _on_gpu(t, name)
-    if t.device != pool.device:
-        raise TypeError("%s is on %s, the pool on %s" % (name, t.device, pool.device))
-    if t.dtype != dtype:
+def _kv_tensor(t, name, device, dtype):
+    """Refuses what is not a tensor of this type on this GPU (its index).  A
+    decode step's launches take a few microseconds each: these checks are kept
+    to one attribute read apiece."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch tensor" % name)
+    if t.get_device() != device:
+        raise TypeError("%s is on %s, the pool on GPU %d" % (name, t.device, device))
+    if t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+
+
+def _kv_rows(t, name, device, dtype, n_tokens, heads, D, gaps=True):
+    """Address and token stride of a token tensor [n_tokens, heads, D] whose
+    heads and channels lie without gaps (nor its tokens, unless gaps)."""
+    _kv_tensor(t, name, device, dtype)
     if t.shape != (n_tokens, heads, D):
         raise ValueError("%s must be [%d, %d, %d], got %s" % (name, n_tokens, heads, D, list(t.shape)))
-    stride = t.stride()
-    if n_tokens and (stride[2] != 1 or (heads > 1 and stride[1] != D)):
-        raise ValueError("%s must have contiguous heads and channels" % name)
-    return t.data_ptr(), stride[0] if n_tokens > 1 else heads * D
+    row, head, channel = t.stride()
+    if n_tokens < 2:
+        row = heads * D
+    if n_tokens and (channel != 1 or (heads > 1 and head != D) or not (gaps or row == heads * D)):
+        raise ValueError("%s must be contiguous%s" % (name, " within its tokens" if gaps else ""))
+    return t.data_ptr(), row
 
 
-def _kv_tables(pool, page_table, cu_seqlens, lens):
-    """The checked tables of a cache launch: their addresses, n_seq, max_pages."""
+def _kv_tables(device, page_table, cu_seqlens, lens):
+    """The checked tables of a cache launch: addresses of the page table,
+    max_pages, addresses of cu_seqlens and lengths; n_seq."""
     import torch
-    for t, name, dim in ((page_table, "page_table", 2), (cu_seqlens, "cu_seqlens", 1), (lens, "cache_lens", 1)):
-        _on_gpu(t, name)
-        if t.device != pool.device:
-            raise TypeError("%s is on %s, the pool on %s" % (name, t.device, pool.device))
-        if t.dtype != torch.int32 or t.dim() != dim or not t.is_contiguous():
-            raise TypeError("%s must be a contiguous int32 tensor of %d dimensions" % (name, dim))
+    i32 = torch.int32
+    _kv_tensor(page_table, "page_table", device, i32)
+    _kv_tensor(cu_seqlens, "cu_seqlens", device, i32)
+    _kv_tensor(lens, "cache_lens", device, i32)
+    if not (page_table.is_contiguous() and cu_seqlens.is_contiguous() and lens.is_contiguous()):
+        raise ValueError("page_table, cu_seqlens and cache_lens must be contiguous")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [n_seq, max_pages], got %s" % list(page_table.shape))
     n_seq, max_pages = page_table.shape
-    if lens.numel() != n_seq or cu_seqlens.numel() != n_seq + 1:
+    if lens.shape != (n_seq,) or cu_seqlens.shape != (n_seq + 1,):
         raise ValueError("page_table has %d rows: cu_seqlens needs one entry more, cache_lens as many" % n_seq)
-    return page_table.data_ptr(), max_pages, cu_seqlens.data_ptr(), lens.data_ptr(), n_seq
+    return (page_table.data_ptr(), max_pages, cu_seqlens.data_ptr(), lens.data_ptr()), n_seq
 
 
-def _kv_stream(pool, stream):
+def _kv_stream(device, stream):
     """The stream's address: by default the current one of the pool's device."""
     import torch
     if stream is None:
-        return torch.cuda.current_stream(pool.device).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(device)
     if isinstance(stream, int):
         return stream
-    if stream.device != pool.device:
-        raise ValueError("the stream is on %s, the pool on %s" % (stream.device, pool.device))
+    if stream.device.index != device:
+        raise ValueError("the stream is on %s, the pool on GPU %d" % (stream.device, device))
     return stream.cuda_stream
 
 
-def _kv_call(name, pool, *args):
+def _kv_call(name, device, *args):
     """Calls the library with the pool's device as the current one."""
     import torch
     fn = getattr(library(), name)
-    if torch.cuda.current_device() == pool.device.index:
+    if torch.cuda.current_device() == device:
         rc = fn(*args)
     else:
-        with torch.cuda.device(pool.device):
+        with torch.cuda.device(device):
             rc = fn(*args)
-    _check(rc, name)
+    if rc:
+        raise KdaError(rc, name)
 
 
 def kda_kv_append(pool, page_table, cu_seqlens, cache_lens, k, v, q=None, q_out=None, cos=None, sin=None,
@@ -639,47 +654,46 @@ def kda_kv_append(pool, page_table, cu_seqlens, cache_lens, k, v, q=None, q_out=
     or [T, q_heads, D] of the same type, turned into q_out (contiguous); cos,
     sin: None, or float32 [n_positions, rot_dim / 2]."""
     import torch
-    P = make_kv_pool(pool)
-    tables = _kv_tables(pool, page_table, cu_seqlens, cache_lens)
-    T, dtype = k.shape[0], k.dtype
-    kp, ks = _rows(k, "k", pool, P.H, P.D, dtype, T)
-    vp, vs = _rows(v, "v", pool, P.H, P.D, dtype, T)
+    P, dev = make_kv_pool(pool), pool.get_device()
+    tables, n_seq = _kv_tables(dev, page_table, cu_seqlens, cache_lens)
+    T, dtype, H, D = k.shape[0], k.dtype, P.H, P.D
+    kp, ks = _kv_rows(k, "k", dev, dtype, T, H, D)
+    vp, vs = _kv_rows(v, "v", dev, dtype, T, H, D)
     qp = qs = qo = heads = 0
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
     if q is not None:
         heads = q.shape[1] if q.dim() == 3 else -1
-        qp, qs = _rows(q, "q", pool, heads, P.D, dtype, T)
-        qo, _ = _rows(q_out, "q_out", pool, heads, P.D, dtype, T)
-        if not q_out.is_contiguous():
-            raise ValueError("q_out must be contiguous")
+        qp, qs = _kv_rows(q, "q", dev, dtype, T, heads, D)
+        qo, _ = _kv_rows(q_out, "q_out", dev, dtype, T, heads, D, gaps=False)
     cp = sp = positions = half = 0
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin go together")
     if cos is not None:
-        if cos.dim() != 2 or cos.shape != sin.shape:
-            raise ValueError("cos and sin must be [n_positions, rot_dim / 2], both")
+        _kv_tensor(cos, "cos", dev, torch.float32)
+        _kv_tensor(sin, "sin", dev, torch.float32)
+        if cos.dim() != 2 or cos.shape != sin.shape or not (cos.is_contiguous() and sin.is_contiguous()):
+            raise ValueError("cos and sin must be contiguous [n_positions, rot_dim / 2], both")
         positions, half = cos.shape
-        cp, sp = (_dev(t, n, torch.float32, pool.device) for t, n in ((cos, "cos"), (sin, "sin")))
-    _kv_call("kda_kv_append", pool, ctypes.byref(P), tables[0], tables[1], tables[2], tables[3], kp, vp, ks, vs, qp, qs,
-             qo, cp, sp, positions, 2 * half, int(interleaved), tables[4], T, heads, dtype_code(dtype),
-             _kv_stream(pool, stream))
+        cp, sp = cos.data_ptr(), sin.data_ptr()
+    _kv_call("kda_kv_append", dev, ctypes.byref(P), *tables, kp, vp, ks, vs, qp, qs, qo, cp, sp, positions, 2 * half,
+             int(interleaved), n_seq, T, heads, dtype_code(dtype), _kv_stream(dev, stream))
 
 
 def kda_kv_read(pool, page_table, cu_seqlens, first, k_out=None, v_out=None, stream=None) -> None:
     """Reads cached keys and values back (see kda_kv_read in
     include/kda_decode.h): token i of sequence s gets position first[s] + i.
     k_out, v_out: [T, H, D] of one floating type; either may be None."""
-    P = make_kv_pool(pool)
-    tables = _kv_tables(pool, page_table, cu_seqlens, first)
+    P, dev = make_kv_pool(pool), pool.get_device()
+    tables, n_seq = _kv_tables(dev, page_table, cu_seqlens, first)
     some = k_out if k_out is not None else v_out
     if some is None:
         raise ValueError("nothing to read into: k_out and v_out are both None")
     T, dtype = some.shape[0], some.dtype
-    kp, ks = (0, 0) if k_out is None else _rows(k_out, "k_out", pool, P.H, P.D, dtype, T)
-    vp, vs = (0, 0) if v_out is None else _rows(v_out, "v_out", pool, P.H, P.D, dtype, T)
-    _kv_call("kda_kv_read", pool, ctypes.byref(P), tables[0], tables[1], tables[2], tables[3], kp, vp, ks, vs, tables[4],
-             T, dtype_code(dtype), _kv_stream(pool, stream))
+    kp, ks = (0, 0) if k_out is None else _kv_rows(k_out, "k_out", dev, dtype, T, P.H, P.D)
+    vp, vs = (0, 0) if v_out is None else _kv_rows(v_out, "v_out", dev, dtype, T, P.H, P.D)
+    _kv_call("kda_kv_read", dev, ctypes.byref(P), *tables, kp, vp, ks, vs, n_seq, T, dtype_code(dtype),
+             _kv_stream(dev, stream))
 
 
 def kda_kv_attend_workspace(pool, page_table, n_tokens: int, q_heads: int, max_rows: int, max_kv_len: int = 0,
@@ -703,33 +717,31 @@ def kda_kv_attend(pool, page_table, cu_seqlens, cache_lens, q, out, max_rows: in
     workspace: a contiguous uint8 tensor of kda_kv_attend_workspace bytes, or
     None to take one from torch's allocator on the launch's stream."""
     import torch
-    P = make_kv_pool(pool)
-    tables = _kv_tables(pool, page_table, cu_seqlens, cache_lens)
+    P, dev = make_kv_pool(pool), pool.get_device()
+    tables, n_seq = _kv_tables(dev, page_table, cu_seqlens, cache_lens)
     if q.dim() != 3:
         raise ValueError("q must be [T, q_heads, D], got %s" % list(q.shape))
-    T, heads, dtype = q.shape[0], q.shape[1], q.dtype
-    qp, qs = _rows(q, "q", pool, heads, P.D, dtype, T)
-    op, _ = _rows(out, "out", pool, heads, P.D, dtype, T)
-    if not out.is_contiguous():
-        raise ValueError("out must be contiguous")
-    rows, code = T if max_rows is None else int(max_rows), dtype_code(dtype)
-    st = _kv_stream(pool, stream)
+    (T, heads, _), dtype, D = q.shape, q.dtype, P.D
+    qp, qs = _kv_rows(q, "q", dev, dtype, T, heads, D)
+    op, _ = _kv_rows(out, "out", dev, dtype, T, heads, D, gaps=False)
+    rows, kv, code, st = T if max_rows is None else int(max_rows), int(max_kv_len), dtype_code(dtype), _kv_stream(dev, stream)
+    pool_ref = ctypes.byref(P)
     if workspace is None:
-        n = library().kda_kv_attend_workspace(ctypes.byref(P), tables[1], tables[4], T, rows, int(max_kv_len), heads,
-                                              code)
-        if n:
-            current = torch.cuda.current_stream(pool.device)
-            if st == current.cuda_stream:
-                workspace = torch.empty(n, dtype=torch.uint8, device=pool.device)
-            else:
-                # memory of that stream: the allocator hands it on in its order
-                on = torch.cuda.ExternalStream(st, device=pool.device) if st else torch.cuda.default_stream(pool.device)
-                with torch.cuda.stream(on):
-                    workspace = torch.empty(n, dtype=torch.uint8, device=pool.device)
-    wp, wn = (0, 0) if workspace is None else (_dev(workspace, "workspace", torch.uint8, pool.device),
-                                               workspace.numel())
-    _kv_call("kda_kv_attend", pool, ctypes.byref(P), tables[0], tables[1], tables[2], tables[3], qp, qs, op, tables[4], T,
-             rows, int(max_kv_len), heads, code, 1.0 / math.sqrt(P.D) if scale is None else float(scale), wp, wn, st)
+        wn = library().kda_kv_attend_workspace(pool_ref, tables[1], n_seq, T, rows, kv, heads, code)
+        if wn == 0 or st == torch._C._cuda_getCurrentRawStream(dev):
+            workspace = torch.empty(wn, dtype=torch.uint8, device=pool.device)
+        else:
+            # memory of that stream: the allocator hands it on in its order
+            on = torch.cuda.ExternalStream(st, device=pool.device) if st else torch.cuda.default_stream(pool.device)
+            with torch.cuda.stream(on):
+                workspace = torch.empty(wn, dtype=torch.uint8, device=pool.device)
+    else:
+        _kv_tensor(workspace, "workspace", dev, torch.uint8)
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        wn = workspace.numel()
+    _kv_call("kda_kv_attend", dev, pool_ref, *tables, qp, qs, op, n_seq, T, rows, kv, heads, code,
+             1.0 / math.sqrt(D) if scale is None else float(scale), workspace.data_ptr(), wn, st)
 
 
 def kda_kv_validate(pool_desc: kda_kv_pool, page_table_host, cu_seqlens_host, cache_lens_host, n_tokens: int) -> int:

@@ -195,13 +195,52 @@ __device__ __forceinline__ float sticky_float(double d) {
   return __uint_as_float((mag < (897u << 20) ? 0u : f) | (hi & 0x80000000u));
 }
 
+// 8 channels as they lie in memory
+template <int DT>
+struct Raw8 {
+  u4 w[DT == KDA_F32 ? 2 : 1];
+
+  __device__ __forceinline__ void load(const void* p, int64_t at) {
+    const u4* s = reinterpret_cast<const u4*>(static_cast<const uint8_t*>(p) + at * elem_bytes<DT>());
+    w[0] = s[0];
+    if constexpr (DT == KDA_F32) w[1] = s[1];
+  }
+  // those of another lane
+  __device__ __forceinline__ Raw8 of(int lane) const {
+    Raw8 r;
+#pragma unroll
+    for (int i = 0; i < (DT == KDA_F32 ? 2 : 1); ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) r.w[i][e] = __builtin_amdgcn_ds_bpermute(4 * lane, w[i][e]);
+    return r;
+  }
+  __device__ __forceinline__ void numbers(float (&x)[8]) const {
+    if constexpr (DT == KDA_F32) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(w[e / 4][e % 4]);
+    } else if constexpr (DT == KDA_F16) {
+      const h8 a = __builtin_bit_cast(h8, w[0]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = static_cast<float>(a[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[2 * e] = __uint_as_float(w[0][e] << 16);
+        x[2 * e + 1] = __uint_as_float(w[0][e] & 0xFFFF0000u);
+      }
+    }
+  }
+};
+
 // One group of D / 8 lanes takes one token and walks over its units (cached
 // heads, then query heads), 8 channels a lane: the token's place and its
-// angles are looked up once.  Neighbouring groups take neighbouring tokens of
-// the same unit, so a wave writes 256 contiguous bytes of codes.
+// angles are looked up once, and a pair's other half, when another lane holds
+// it, comes from that lane.  Neighbouring groups take neighbouring tokens of
+// the same unit, so a wave writes 256 contiguous bytes of codes.  Queries are
+// most of the bytes: four heads' loads are in flight together.
 template <int DT, int D>
 __global__ __launch_bounds__(256) void kda_kv_append_kernel(KvAppendArgs a) {
-  constexpr int W = D / 8;
+  constexpr int W = D / 8, AT_ONCE = 4;
   const int li = threadIdx.x % W;
   const int64_t tile = blockIdx.x / a.unit_blocks;
   const int ub = blockIdx.x % a.unit_blocks;
@@ -212,11 +251,11 @@ __global__ __launch_bounds__(256) void kda_kv_append_kernel(KvAppendArgs a) {
   if (at.what == kOutside) return;
 
   // out[e] = x[e] * cs[e] + partner[e] * sn[e]
-  const int c0 = 8 * li;
-  const bool turned = c0 < 2 * a.half;
+  const int c0 = 8 * li, lane = threadIdx.x % 64;
+  const bool turned = c0 < 2 * a.half && at.what == kPlaced;
   float cs[8], sn[8];
-  int partner = 0;  // channels to the partner's eight
-  if (turned && at.what == kPlaced) {
+  int other = lane;  // the lane of the pairs' other halves
+  if (turned) {
     if (a.interleaved) {
       const f4 c = *reinterpret_cast<const f4*>(a.cos + static_cast<int64_t>(at.pos) * a.half + c0 / 2);
       const f4 s = *reinterpret_cast<const f4*>(a.sin + static_cast<int64_t>(at.pos) * a.half + c0 / 2);
@@ -227,93 +266,86 @@ __global__ __launch_bounds__(256) void kda_kv_append_kernel(KvAppendArgs a) {
       const int64_t row = static_cast<int64_t>(at.pos) * a.half + (first ? c0 : c0 - a.half);
       load8<KDA_F32>(a.cos, row, cs);
       load8<KDA_F32>(a.sin, row, sn);
-      partner = first ? a.half : -a.half;
+      other = first ? lane + a.half / 8 : lane - a.half / 8;
 #pragma unroll
       for (int e = 0; e < 8; ++e) sn[e] = first ? -sn[e] : sn[e];
     }
   }
+  // x and its partners; every lane takes part
+  auto pairs = [&](const Raw8<DT>& r, float (&x)[8], float (&p)[8]) __attribute__((always_inline)) {
+    r.numbers(x);
+    if (a.half == 0) return;
+    if (a.interleaved) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) p[e] = x[e ^ 1];
+    } else {
+      r.of(other).numbers(p);
+    }
+  };
   const int block_bytes = kv_block_bytes(a.t.P, D);
-  const int lane = threadIdx.x % 64;
   const uint64_t mine = ((1ull << W) - 1) << (lane - li);
 
-  for (int u = u0; u < u1; ++u) {
-    if (u < a.t.H) {
-      if (at.what != kPlaced) continue;
-      float x[8], v[8];
-      const int64_t kat = token * a.k_stride + u * D + c0;
-      load8<DT>(a.k, kat, x);
-      load8<DT>(a.v, token * a.v_stride + u * D + c0, v);
-      // the keys' rotation and scaling in 64 bits: a code next to a rounding
-      // border comes out as the definition has it
-      double y[8];
-      if (turned) {
-        float p[8];
-        if (a.interleaved) {
+  int u = u0;
+  for (; u < u1 && u < a.t.H; ++u) {
+    Raw8<DT> rk;
+    float x[8], p[8], v[8];
+    rk.load(a.k, token * a.k_stride + u * D + c0);
+    load8<DT>(a.v, token * a.v_stride + u * D + c0, v);
+    pairs(rk, x, p);
+    // the keys' rotation and scaling in 64 bits: a code next to a rounding
+    // border comes out as the definition has it
+    double y[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) p[e] = x[e ^ 1];
-        } else {
-          load8<DT>(a.k, kat + partner, p);
-        }
+    for (int e = 0; e < 8; ++e) y[e] = static_cast<double>(x[e]);
+    if (turned) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          y[e] = static_cast<double>(x[e]) * static_cast<double>(cs[e]) +
-                 static_cast<double>(p[e]) * static_cast<double>(sn[e]);
-      } else {
+      for (int e = 0; e < 8; ++e)
+        y[e] = y[e] * static_cast<double>(cs[e]) + static_cast<double>(p[e]) * static_cast<double>(sn[e]);
+    }
+    int ek = 0, ev = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = static_cast<double>(x[e]);
-      }
-      int ek = 0, ev = 0;
+    for (int e = 0; e < 8; ++e) {
+      const int k = static_cast<int>(__builtin_bit_cast(uint64_t, y[e]) >> 52) & 0x7FF;
+      const int w = static_cast<int>(bits(v[e]) >> 23) & 0xFF;
+      ek = ek > k ? ek : k;
+      ev = ev > w ? ev : w;
+    }
+    ek = quad_max(ek);
+    ev = quad_max(ev);
+    const bool poison = (__ballot(ek == 0x7FF || ev == 0xFF) & mine) != 0;
+    const int kb = clamp_exp(ek - 1023 - 2 + 127), vb = clamp_exp(ev - 2);
+    const double km = __builtin_bit_cast(double, static_cast<uint64_t>(1023 + 127 - kb) << 52);
+    const float vm = exp_scale(254 - vb);
+    float ka[8], va[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int k = static_cast<int>(__builtin_bit_cast(uint64_t, y[e]) >> 52) & 0x7FF;
-        const int w = static_cast<int>(bits(v[e]) >> 23) & 0xFF;
-        ek = ek > k ? ek : k;
-        ev = ev > w ? ev : w;
-      }
-      ek = quad_max(ek);
-      ev = quad_max(ev);
-      const bool poison = (__ballot(ek == 0x7FF || ev == 0xFF) & mine) != 0;
-      const int kb = clamp_exp(ek - 1023 - 2 + 127), vb = clamp_exp(ev - 2);
-      const double km = __builtin_bit_cast(double, static_cast<uint64_t>(1023 + 127 - kb) << 52);
-      const float vm = exp_scale(254 - vb);
-      float ka[8], va[8];
+    for (int e = 0; e < 8; ++e) {
+      ka[e] = sticky_float(y[e] * km);
+      va[e] = v[e] * vm;
+    }
+    if (at.what != kPlaced) continue;
+    uint8_t* block = at.block + static_cast<int64_t>(u) * block_bytes;
+    const int code = at.row * (D / 2) + 4 * li;
+    *reinterpret_cast<uint32_t*>(block + code) = poison ? 0 : quant8(ka);
+    *reinterpret_cast<uint32_t*>(block + kv_value_codes(a.t.P, D) + code) = poison ? 0 : quant8(va);
+    if (li % 4 == 0) {
+      block[kv_key_exps(a.t.P, D) + at.row * (D / kKvGroup) + li / 4] = static_cast<uint8_t>(poison ? kKvPoison : kb);
+      block[kv_value_exps(a.t.P, D) + (li / 4) * a.t.P + at.row] = static_cast<uint8_t>(poison ? kKvMinExp : vb);
+    }
+  }
+  for (; u < u1; u += AT_ONCE) {
+    Raw8<DT> r[AT_ONCE];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        ka[e] = sticky_float(y[e] * km);
-        va[e] = v[e] * vm;
-      }
-      uint8_t* block = at.block + static_cast<int64_t>(u) * block_bytes;
-      const int code = at.row * (D / 2) + 4 * li;
-      *reinterpret_cast<uint32_t*>(block + code) = poison ? 0 : quant8(ka);
-      *reinterpret_cast<uint32_t*>(block + kv_value_codes(a.t.P, D) + code) = poison ? 0 : quant8(va);
-      if (li % 4 == 0) {
-        block[kv_key_exps(a.t.P, D) + at.row * (D / kKvGroup) + li / 4] =
-            static_cast<uint8_t>(poison ? kKvPoison : kb);
-        block[kv_value_exps(a.t.P, D) + (li / 4) * a.t.P + at.row] = static_cast<uint8_t>(poison ? kKvMinExp : vb);
-      }
-    } else {
-      const int h = u - a.t.H;
-      float x[8], o[8];
-      const int64_t qat = token * a.q_stride + h * D + c0;
-      load8<DT>(a.q, qat, x);
+    for (int i = 0; i < AT_ONCE; ++i)
+      if (u + i < u1) r[i].load(a.q, token * a.q_stride + (u + i - a.t.H) * D + c0);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = x[e];
-      if (turned && at.what == kPlaced) {
-        float p[8];
-        if (a.interleaved) {
+    for (int i = 0; i < AT_ONCE; ++i) {
+      if (u + i >= u1) break;
+      float x[8], p[8];
+      pairs(r[i], x, p);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) p[e] = x[e ^ 1];
-        } else {
-          load8<DT>(a.q, qat + partner, p);
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = x[e] * cs[e] + p[e] * sn[e];
-      }
-      if (at.what == kBad) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = __builtin_nanf("");
-      }
-      store8<DT>(a.q_out, (token * a.q_heads + h) * D + c0, o);
+      for (int e = 0; e < 8; ++e)
+        x[e] = at.what == kBad ? __builtin_nanf("") : turned ? x[e] * cs[e] + p[e] * sn[e] : x[e];
+      store8<DT>(a.q_out, (token * a.q_heads + u + i - a.t.H) * D + c0, x);
     }
   }
 }
@@ -322,9 +354,17 @@ __global__ __launch_bounds__(256) void kda_kv_append_kernel(KvAppendArgs a) {
 // Read back
 // ---------------------------------------------------------------------------
 
+// Channels a lane takes: 16 bytes of them, so that a store instruction writes
+// whole lines (8 fp32 channels, two stores 16 bytes apart: 403 us instead of 351
+// for 102392 tokens of 12 heads).
 template <int DT>
-__device__ __forceinline__ void store_codes(void* p, int64_t at, uint32_t c, uint32_t e, bool nan) {
+constexpr int kv_read_channels() { return DT == KDA_F32 ? 4 : 8; }
+
+// the codes of a lane's channels, as numbers
+template <int DT>
+__device__ __forceinline__ void store_codes(void* p, int64_t at, uint32_t c, uint32_t e) {
   const float s = exp_scale(e);
+  const bool nan = e == kKvPoison;
   if constexpr (DT == KDA_BF16) {
     u4 o = {dequant2<0>(c, s), dequant2<1>(c, s), dequant2<2>(c, s), dequant2<3>(c, s)};
     if (nan) o = u4{0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};
@@ -332,19 +372,26 @@ __device__ __forceinline__ void store_codes(void* p, int64_t at, uint32_t c, uin
   } else {
     const f2 y0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 0);
     const f2 y1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 1);
-    const f2 y2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 2);
-    const f2 y3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 3);
-    float x[8] = {y0[0], y0[1], y1[0], y1[1], y2[0], y2[1], y3[0], y3[1]};
+    const float none = __builtin_nanf("");
+    if constexpr (DT == KDA_F32) {
+      store4<DT>(p, at, nan ? f4{none, none, none, none} : f4{y0[0], y0[1], y1[0], y1[1]});
+    } else {
+      const f2 y2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 2);
+      const f2 y3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 3);
+      float x[8] = {y0[0], y0[1], y1[0], y1[1], y2[0], y2[1], y3[0], y3[1]};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = nan ? __builtin_nanf("") : x[i];
-    store8<DT>(p, at, x);
+      for (int i = 0; i < 8; ++i) x[i] = nan ? none : x[i];
+      store8<DT>(p, at, x);
+    }
   }
 }
 
-// Groups of lanes as in the append: one token each, 8 channels a lane.
+// Groups of lanes as in the append, one token each.  Bound by HBM, mostly by
+// what is written: 1.43 GB in 351 us, 4.06 TB/s of a copy's 4.72.
 template <int DT, int D>
 __global__ __launch_bounds__(256) void kda_kv_read_kernel(KvReadArgs a) {
-  constexpr int W = D / 8;
+  constexpr int CH = kv_read_channels<DT>(), W = D / CH;
+  using Codes = std::conditional_t<CH == 4, uint16_t, uint32_t>;
   const int li = threadIdx.x % W;
   const int64_t tile = blockIdx.x / a.head_blocks;
   const int hb = blockIdx.x % a.head_blocks;
@@ -354,21 +401,18 @@ __global__ __launch_bounds__(256) void kda_kv_read_kernel(KvReadArgs a) {
   const TokenPlace at = find_token<W>(a.t, token, INT32_MAX);
   if (at.what == kOutside) return;
   const int block_bytes = kv_block_bytes(a.t.P, D);
-  const bool bad = at.what == kBad;
-  const int code = at.row * (D / 2) + 4 * li;
+  const int code = at.row * (D / 2) + CH / 2 * li, grp = CH * li / kKvGroup;
+  const int k_exp = kv_key_exps(a.t.P, D) + at.row * (D / kKvGroup) + grp;
+  const int v_exp = kv_value_exps(a.t.P, D) + grp * a.t.P + at.row;
   for (int h = h0; h < h1; ++h) {
+    // a token without a page reads page 0, and is NaN
     const uint8_t* block = at.block + static_cast<int64_t>(h) * block_bytes;
-    uint32_t kc = 0, vc = 0, ke = kKvPoison, ve = kKvPoison;
-    if (!bad) {
-      kc = *reinterpret_cast<const uint32_t*>(block + code);
-      vc = *reinterpret_cast<const uint32_t*>(block + kv_value_codes(a.t.P, D) + code);
-      ke = block[kv_key_exps(a.t.P, D) + at.row * (D / kKvGroup) + li / 4];
-      ve = block[kv_value_exps(a.t.P, D) + (li / 4) * a.t.P + at.row];
-    }
-    if (a.k_out != nullptr)
-      store_codes<DT>(a.k_out, token * a.k_stride + h * D + 8 * li, kc, ke, ke == kKvPoison);
-    if (a.v_out != nullptr)
-      store_codes<DT>(a.v_out, token * a.v_stride + h * D + 8 * li, vc, ve, ve == kKvPoison);
+    const uint32_t kc = *reinterpret_cast<const Codes*>(block + code);
+    const uint32_t vc = *reinterpret_cast<const Codes*>(block + kv_value_codes(a.t.P, D) + code);
+    uint32_t ke = block[k_exp], ve = block[v_exp];
+    if (at.what == kBad) ke = ve = kKvPoison;
+    if (a.k_out != nullptr) store_codes<DT>(a.k_out, token * a.k_stride + h * D + CH * li, kc, ke);
+    if (a.v_out != nullptr) store_codes<DT>(a.v_out, token * a.v_stride + h * D + CH * li, vc, ve);
   }
 }
 
@@ -1303,7 +1347,8 @@ extern "C" int kda_kv_read(const kda_kv_pool* kv, const int32_t* page_table, int
   a.v_out = v_out;
   a.k_stride = k_stride;
   a.v_stride = v_stride;
-  const int64_t tiles = (n_tokens + 256 / (kv->D / 8) - 1) / (256 / (kv->D / 8));
+  const int per = 256 / (kv->D / (dtype == KDA_F32 ? 4 : 8));  // tokens a block
+  const int64_t tiles = (n_tokens + per - 1) / per;
   a.heads_per_block = heads_a_block(tiles, kv->H);
   a.head_blocks = (kv->H + a.heads_per_block - 1) / a.heads_per_block;
   if (tiles * a.head_blocks > INT32_MAX) return KDA_ERR_ARG;
