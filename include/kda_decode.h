@@ -601,7 +601,7 @@ int kda_kv_read(const kda_kv_pool* kv, const int32_t* page_table, int32_t max_pa
  *                  tokens including them (0: all that max_pages covers).  Both
  *                  only lay out the launch: longer sequences are taken as
  *                  well, more slowly.
- *  q_heads         a multiple of H; n_tokens * q_heads / H < 2^30.
+ *  q_heads         a multiple of H; n_tokens * q_heads / H < 2^29.
  *  scale           finite.
  *  workspace       kda_kv_attend_workspace() bytes for the same arguments (may
  *                  be NULL for 0), 16-byte aligned, free for use again once

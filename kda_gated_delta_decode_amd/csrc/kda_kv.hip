@@ -25,12 +25,17 @@ namespace {
 using bf2 = __bf16 __attribute__((ext_vector_type(2)));
 using bf8 = __bf16 __attribute__((ext_vector_type(8)));
 using f16v = float __attribute__((ext_vector_type(16)));
+using h2 = _Float16 __attribute__((ext_vector_type(2)));
+using u16x2 = uint16_t __attribute__((ext_vector_type(2)));
 using u2 = uint32_t __attribute__((ext_vector_type(2)));
 using u4 = uint32_t __attribute__((ext_vector_type(4)));
 
 // Loads of uniform addresses through the scalar cache, apart from the vector
 // loads' counter: a page id can be waited for while cache rows are in flight.
 using const_i32 = const int32_t __attribute__((address_space(4)));
+
+// A launch's arguments where they lie.
+using kernel_args = const KvAttendArgs __attribute__((address_space(4)))*;
 
 template <int DT>
 constexpr int elem_bytes() { return DT == KDA_F32 ? 4 : 2; }
@@ -455,12 +460,9 @@ template <int DT>
 constexpr int q_pieces() { return DT == KDA_F32 ? 3 : DT == KDA_F16 ? 2 : 1; }
 // Softmax weights are fp32.  fp32 outputs take all 24 bits of them; for 16-bit
 // outputs two pieces leave less than 2^-15 of one, a sixteenth of fp16's half
-// step.  Prompts in bf16 take one, rounded to nearest: each weight is off by
-// at most the output's own half step, at random, and the product runs once.
+// step.
 template <int DT>
 constexpr int w_pieces() { return DT == KDA_F32 ? 3 : 2; }
-template <int DT>
-constexpr int w_pieces_tiles() { return DT == KDA_BF16 ? 1 : w_pieces<DT>(); }
 
 // Splits pairs of numbers into N packed bf16 pieces by truncation: what is
 // left after each piece is exact, and 3 pieces hold all of an fp32.
@@ -560,7 +562,7 @@ __global__ __launch_bounds__(64 * NW, kv_rows_waves<NT>()) void kda_kv_rows_kern
   const int pages0 = load_pages(t0 + 32 * wave);
   const Seq q = seq_of(a.t, s);
   if (q.skip) return;
-  const int64_t all_rows = static_cast<int64_t>(q.rows) * a.group;
+  const int all_rows = q.rows * a.group;
 
   const int block_bytes = kv_block_bytes(a.t.P, D);
   const uint8_t* head0 = a.t.base + static_cast<int64_t>(h) * block_bytes;
@@ -570,9 +572,8 @@ __global__ __launch_bounds__(64 * NW, kv_rows_waves<NT>()) void kda_kv_rows_kern
   const uint32_t ve_off = (i16 * C / kKvGroup) * a.t.P + 4 * j;
 
   // Tiles beyond those the launch has blocks for are walked by the same blocks.
-  for (int64_t rt = rt0; rt * R < all_rows; rt += a.row_tiles) {
-    const int row0 = static_cast<int>(rt * R);
-    const int last_row = static_cast<int>(row0 + R < all_rows ? row0 + R : all_rows) - 1;
+  for (int row0 = rt0 * R; row0 < all_rows; row0 += a.row_tiles * R) {
+    const int last_row = (row0 + R < all_rows ? row0 + R : all_rows) - 1;
     const int vis = q.past + last_row / a.group + 1;  // tokens the last row sees
     const int splits = q.bad ? 1 : kv_splits(vis, a);
     if (sp >= splits) continue;
@@ -828,13 +829,40 @@ __device__ __forceinline__ void each_of(F f, std::integer_sequence<int, I...>) {
   (f(std::integral_constant<int, I>{}), ...);
 }
 
-// Waves a SIMD for the registers: two where they fit in 256, else one.
-template <int DT, int D>
-constexpr int kv_tiles_waves() { return DT == KDA_BF16 || (DT == KDA_F16 && D == 64) ? 2 : 1; }
-
+// in bf16, or in fp16
+template <bool HALF>
 __device__ __forceinline__ f16v mfma32(u4 a, u4 b, f16v c) {
-  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8, a), __builtin_bit_cast(bf8, b), c, 0, 0, 0);
+  if constexpr (HALF)
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, a), __builtin_bit_cast(h8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8, a), __builtin_bit_cast(bf8, b), c, 0, 0, 0);
 }
+
+template <bool HALF, int SEL>
+__device__ __forceinline__ uint32_t dequant2_as(uint32_t c, float scale) {
+  if constexpr (HALF)
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, scale, SEL));
+  else
+    return dequant2<SEL>(c, scale);
+}
+
+// Exponent bytes whose values fp16 holds exactly: 0.5 * 2^-23 = 2^-24 to
+// 6 * 2^13 = 49152; and kKvMinExp, which 32 zeros have (and numbers below 2^-122).
+constexpr int kHalfMinExp = 104, kHalfMaxExp = 140;
+
+// The largest exponent byte of those seen, and the smallest but kKvMinExp.
+struct ExpRange {
+  u16x2 top = {0, 0}, low = {0xFFFF, 0xFFFF};
+  __device__ __forceinline__ void take2(uint32_t e) {  // two bytes, in bits 0..7 and 16..23
+    const u16x2 x = __builtin_bit_cast(u16x2, e);
+    top = __builtin_elementwise_max(top, x);
+    low = __builtin_elementwise_min(low, static_cast<u16x2>(x - static_cast<uint16_t>(kKvMinExp + 1)));
+  }
+  __device__ __forceinline__ bool in_half() const {
+    constexpr int least = kHalfMinExp - (kKvMinExp + 1);
+    return top[0] <= kHalfMaxExp && top[1] <= kHalfMaxExp && low[0] >= least && low[1] >= least;
+  }
+};
 
 // Many rows: 128 rows of one sequence and cached head (32 a wave) against one
 // split of its tokens, 64 of them at a time.
@@ -851,9 +879,16 @@ __device__ __forceinline__ f16v mfma32(u4 a, u4 b, f16v c) {
 // multiplied while this one's weights are formed, and the codes of later
 // tiles are turned while the values are multiplied.  Keys are therefore
 // staged one tile further ahead than values; one barrier a tile.
+//
+// 16-bit types first take everything in fp16: E2M1 times 2^(e - 127) is exact
+// there for e in 104..140, an fp16 query is itself, a bf16 query divided by its
+// row's power of two loses at most 2^-25 of the row's largest channel, and
+// weights, at most 2^15, keep 11 bits down to 2^-21 of the largest.  One product
+// for each operand then does what two or three bf16 pieces do.  The exponents
+// are looked at on the way; a block that meets another one throws its sums
+// away and starts again in bf16 pieces.
 template <int DT, int D>
-__global__ __launch_bounds__(256, (kv_tiles_waves<DT, D>())) void kda_kv_tiles_kernel(KvAttendArgs a) {
-  constexpr int NQ = q_pieces<DT>(), NP = w_pieces_tiles<DT>();
+__global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tiles_kernel(KvAttendArgs a) {
   constexpr int KT = 64;            // tokens of a tile
   constexpr int KS = D / 16;        // products over the channels
   constexpr int CB = D / 32;        // 32-channel blocks
@@ -876,7 +911,7 @@ __global__ __launch_bounds__(256, (kv_tiles_waves<DT, D>())) void kda_kv_tiles_k
   const int h = unit % a.t.H, s = unit / a.t.H;
   const Seq q = seq_of(a.t, s);
   if (q.skip) return;
-  const int64_t all_rows = static_cast<int64_t>(q.rows) * a.group;
+  const int all_rows = q.rows * a.group;
   const int block_bytes = kv_block_bytes(a.t.P, D);
   const uint8_t* head0 = a.t.base + static_cast<int64_t>(h) * block_bytes;
   const_i32* table = (const_i32*)(a.t.page_table + static_cast<int64_t>(s) * a.t.max_pages);
@@ -890,10 +925,13 @@ __global__ __launch_bounds__(256, (kv_tiles_waves<DT, D>())) void kda_kv_tiles_k
   const int k_to = kt * KROW + 16 * kj * (D / 32);
   const int v_to = vo * VROW + 16 * (2 * (vt / 4) + vt % 2) + 8 * ((vt / 2) % 2);
   const int k_at = i32 * KROW + 16 * half, v_at = i32 * VROW + 16 * half;
+  // and in a block, from the first token row of the wave's 16
+  const uint32_t k_off = kt % 16 * (D / 2) + kj * (D / 8);
+  const uint32_t v_off = 4 * (lane % 4) * (D / 2) + vo * (VC / 2);
+  const uint32_t ve_off = (vo * VC / kKvGroup) * a.t.P + 4 * (lane % 4);
 
-  for (int64_t rt = rt0; rt * R < all_rows; rt += a.row_tiles) {
-    const int row0 = static_cast<int>(rt * R);
-    const int last_row = static_cast<int>(row0 + R < all_rows ? row0 + R : all_rows) - 1;
+  for (int row0 = rt0 * R; row0 < all_rows; row0 += a.row_tiles * R) {
+    const int last_row = (row0 + R < all_rows ? row0 + R : all_rows) - 1;
     const int vis = q.past + last_row / a.group + 1;
     const int splits = q.bad ? 1 : kv_splits(vis, a);
     if (sp >= splits) continue;
@@ -905,15 +943,57 @@ __global__ __launch_bounds__(256, (kv_tiles_waves<DT, D>())) void kda_kv_tiles_k
     const int r_in = row <= last_row ? row : last_row;
     const int tok = r_in / a.group, g = r_in - tok * a.group;
     const int limit = row <= last_row ? q.past + tok : -1;
+    // All of the tile; with HALF in fp16, and false if that does not do.
+    auto attend = [&](auto in_half) __attribute__((always_inline)) {
+    constexpr bool HALF = decltype(in_half)::value;
+    constexpr int NQ = HALF ? 1 : q_pieces<DT>(), NP = HALF ? 1 : w_pieces<DT>();
+    // fp16's second try keeps two pieces of queries and weights, and has no
+    // registers for a second tile's scores
+    constexpr bool PIPED = HALF || DT == KDA_F32;
+    float scale = a.scale;
     u4 qf[NQ][KS];
+    kernel_args args0 = (kernel_args)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(args0));
+    const int64_t q_at = (q.n0 + tok) * args0->q_stride + (static_cast<int64_t>(h) * args0->group + g) * D + 8 * half;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-      u4 x[NQ];
-      load_query<DT>(a.q, (q.n0 + tok) * a.q_stride + (static_cast<int64_t>(h) * a.group + g) * D + 16 * ks + 8 * half,
-                     a.sign, x);
+      if constexpr (HALF && DT == KDA_F16) {
+        qf[0][ks] = *reinterpret_cast<const u4*>(static_cast<const uint16_t*>(args0->q) + q_at + 16 * ks);
+        const uint32_t flip = args0->sign < 0.0f ? 0x80008000u : 0u;
 #pragma unroll
-      for (int p = 0; p < NQ; ++p) qf[p][ks] = x[p];
+        for (int k = 0; k < 4; ++k) qf[0][ks][k] ^= flip;
+      } else {
+        u4 x[q_pieces<DT>()];
+        load_query<DT>(args0->q, q_at + 16 * ks, args0->sign, x);
+#pragma unroll
+        for (int p = 0; p < NQ; ++p) qf[p][ks] = x[p];
+      }
     }
+    if constexpr (HALF && DT == KDA_BF16) {
+      // the row's largest exponent, from both lanes that hold it
+      u16x2 top = {0, 0};
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, qf[0][ks][k] & 0x7FFF7FFFu));
+      int ex = (top[0] > top[1] ? top[0] : top[1]) >> 7;
+      const auto both = __builtin_amdgcn_permlane32_swap(ex, ex, false, false);
+      ex = static_cast<int>(both[0] > both[1] ? both[0] : both[1]);
+      ex = ex == 0 ? 127 : ex < 253 ? ex : 253;
+      const float down = exp_scale(254 - ex);
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t w = qf[0][ks][k];
+          const h2 y = {static_cast<_Float16>(__uint_as_float(w << 16) * down),
+                        static_cast<_Float16>(__uint_as_float(w & 0xFFFF0000u) * down)};
+          qf[0][ks][k] = __builtin_bit_cast(uint32_t, y);
+        }
+      scale = fmaxf(scale * exp_scale(ex), 0x1p-126f);  // above zero, as a.scale
+    }
+    ExpRange seen;
 
     uint32_t kc[D / 32], ke, vc[4], ve;
     auto page_of = [&](int tb) __attribute__((always_inline)) {
@@ -925,16 +1005,17 @@ __global__ __launch_bounds__(256, (kv_tiles_waves<DT, D>())) void kda_kv_tiles_k
       const int page = page_of(tb);
       if (page >= 0) {
         const uint8_t* blk = head0 + page * a.t.page_bytes;
-        const int r = (tb + kt) & (a.t.P - 1);
+        const uint32_t r = (tb + 16 * wave) & (a.t.P - 1);
+        const uint8_t* at = blk + r * (D / 2);
         if constexpr (D == 128) {
-          const u4 x = *reinterpret_cast<const u4*>(blk + r * (D / 2) + 16 * kj);
+          const u4 x = *reinterpret_cast<const u4*>(at + k_off);
 #pragma unroll
           for (int m = 0; m < 4; ++m) kc[m] = x[m];
         } else {
-          const u2 x = *reinterpret_cast<const u2*>(blk + r * (D / 2) + 8 * kj);
+          const u2 x = *reinterpret_cast<const u2*>(at + k_off);
           kc[0] = x[0], kc[1] = x[1];
         }
-        ke = blk[kv_key_exps(a.t.P, D) + r * (D / kKvGroup) + kj * (D / 4) / kKvGroup];
+        ke = (blk + kv_key_exps(a.t.P, D) + r * (D / kKvGroup))[k_off / 16];  // 16 bytes of codes an exponent
       } else {
         ke = kKvPoison;  // scores NaN, seen only where the mask lets them
 #pragma unroll
@@ -945,27 +1026,32 @@ __global__ __launch_bounds__(256, (kv_tiles_waves<DT, D>())) void kda_kv_tiles_k
       const int page = page_of(tb);
       if (page >= 0) {
         const uint8_t* blk = head0 + page * a.t.page_bytes;
-        const int r = (tb + 4 * vt) & (a.t.P - 1);
-        const uint8_t* vp = blk + kv_value_codes(a.t.P, D) + r * (D / 2) + vo * (VC / 2);
+        const uint32_t r = (tb + 16 * wave) & (a.t.P - 1);
+        const uint8_t* at = blk + kv_value_codes(a.t.P, D) + r * (D / 2);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           if constexpr (D == 128)
-            vc[e] = *reinterpret_cast<const uint32_t*>(vp + e * (D / 2));
+            vc[e] = *reinterpret_cast<const uint32_t*>(at + v_off + e * (D / 2));
           else
-            vc[e] = *reinterpret_cast<const uint16_t*>(vp + e * (D / 2));
+            vc[e] = *reinterpret_cast<const uint16_t*>(at + v_off + e * (D / 2));
         }
-        ve = *reinterpret_cast<const uint32_t*>(blk + kv_value_exps(a.t.P, D) + (vo * VC / kKvGroup) * a.t.P + r);
+        ve = *reinterpret_cast<const uint32_t*>(blk + kv_value_exps(a.t.P, D) + r + ve_off);
       } else {
         ve = 0x7F7F7F7Fu;
 #pragma unroll
         for (int e = 0; e < 4; ++e) vc[e] = 0;
       }
     };
-    // dword m of the key's codes
-    auto stage_key = [&](int buf, int m) __attribute__((always_inline)) {
+    // dword m of the codes of the key in tile tb
+    auto stage_key = [&](int buf, int m, int tb) __attribute__((always_inline)) {
       const float ks = exp_scale(ke);
-      u4 x = {dequant2<0>(kc[m], ks), dequant2<1>(kc[m], ks), dequant2<2>(kc[m], ks), dequant2<3>(kc[m], ks)};
-      if (m == 0) x[0] |= ke == kKvPoison ? ~0u : 0u;
+      u4 x = {dequant2_as<HALF, 0>(kc[m], ks), dequant2_as<HALF, 1>(kc[m], ks), dequant2_as<HALF, 2>(kc[m], ks),
+              dequant2_as<HALF, 3>(kc[m], ks)};
+      if constexpr (HALF) {  // a poisoned key does not fit
+        if (m == 0) seen.take2((tb + kt < t1 ? ke : 127u) * 0x10001u);
+      } else if (m == 0) {
+        x[0] |= ke == kKvPoison ? ~0u : 0u;
+      }
       *reinterpret_cast<u4*>(k_sh + buf * KBUF + k_to + 16 * m) = x;
     };
     // values behind the last token may be anything: zeros
@@ -982,9 +1068,13 @@ __global__ __launch_bounds__(256, (kv_tiles_waves<DT, D>())) void kda_kv_tiles_k
     // channels 2 c2 and 2 c2 + 1 of the 4 values
     auto stage_value = [&](int buf, auto pick) __attribute__((always_inline)) {
       constexpr int c2 = decltype(pick)::value;
+      if constexpr (HALF && c2 == 0) {
+        seen.take2(ve & 0x00FF00FFu);
+        seen.take2((ve >> 8) & 0x00FF00FFu);
+      }
       uint32_t x[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = dequant2<c2>(vc[e], exp_scale((ve >> (8 * e)) & 0xFF));
+      for (int e = 0; e < 4; ++e) x[e] = dequant2_as<HALF, c2>(vc[e], exp_scale((ve >> (8 * e)) & 0xFF));
       *reinterpret_cast<u2*>(v_sh + buf * VBUF + 32 * c2 * VROW + v_to) = u2{pack_lo(x[0], x[1]), pack_lo(x[2], x[3])};
       *reinterpret_cast<u2*>(v_sh + buf * VBUF + (32 * c2 + 16) * VROW + v_to) =
           u2{pack_hi(x[0], x[1]), pack_hi(x[2], x[3])};
@@ -999,7 +1089,7 @@ __global__ __launch_bounds__(256, (kv_tiles_waves<DT, D>())) void kda_kv_tiles_k
     };
     auto score = [&](int i, u4 kf, f16v (&out)[2]) __attribute__((always_inline)) {
 #pragma unroll
-      for (int p = 0; p < NQ; ++p) out[i % 2] = mfma32(kf, qf[p][i / 2], i / 2 == 0 && p == 0 ? zero : out[i % 2]);
+      for (int p = 0; p < NQ; ++p) out[i % 2] = mfma32<HALF>(kf, qf[p][i / 2], i / 2 == 0 && p == 0 ? zero : out[i % 2]);
     };
     // product i of the outputs: tokens 16 (i / CB).., rows 32 (i % CB)..
     auto value_piece = [&](int buf, int i) __attribute__((always_inline)) {
@@ -1014,7 +1104,7 @@ __global__ __launch_bounds__(256, (kv_tiles_waves<DT, D>())) void kda_kv_tiles_k
     load_keys(t0);
     load_values(t0);
 #pragma unroll
-    for (int m = 0; m < D / 32; ++m) stage_key(0, m);
+    for (int m = 0; m < D / 32; ++m) stage_key(0, m, t0);
     load_keys(t0 + KT);
     end_values(t0);
     stage_value(0, std::integral_constant<int, 0>{});
@@ -1025,20 +1115,31 @@ __global__ __launch_bounds__(256, (kv_tiles_waves<DT, D>())) void kda_kv_tiles_k
     }
     load_values(t0 + KT);
 #pragma unroll
-    for (int m = 0; m < D / 32; ++m) stage_key(1, m);
+    for (int m = 0; m < D / 32; ++m) stage_key(1, m, t0 + KT);
     load_keys(t0 + 2 * KT);
     __syncthreads();
+    if constexpr (PIPED) {
 #pragma unroll
-    for (int i = 0; i < 2 * KS; ++i) score(i, key_piece(0, i), sc0);
+      for (int i = 0; i < 2 * KS; ++i) score(i, key_piece(0, i), sc0);
+    }
     auto top_score = [&](const f16v (&x)[2]) __attribute__((always_inline)) {
       float y = -INFINITY;
 #pragma unroll
       for (int e = 0; e < 16; ++e) y = max_nan(y, max_nan(x[0][e], x[1][e]));
       return y;
     };
-    float best = top_score(sc0);
+    float best = PIPED ? top_score(sc0) : 0.0f;
     auto step = [&](int tb, auto which, f16v (&sc)[2], f16v (&next)[2]) __attribute__((always_inline)) {
       constexpr int buf = decltype(which)::value;
+      if constexpr (!PIPED) {
+#pragma unroll
+        for (int i = 0; i < 2 * KS; ++i) {
+          score(i, key_piece(buf, i), sc);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        best = top_score(sc);
+        __syncthreads();  // this buffer's next keys are written below
+      }
       if (tb + KT - 1 > w_first) {
         const int left = limit - tb - 4 * half;  // the last of the lane's tokens its row sees
 #pragma unroll
@@ -1048,8 +1149,8 @@ __global__ __launch_bounds__(256, (kv_tiles_waves<DT, D>())) void kda_kv_tiles_k
         best = top_score(sc);
       }
       // the running maximum moves only when a score passes it by 8
-      if (__ballot(best * a.scale > mx + 8.0f) != 0) {
-        const float to = fmaxf(max_xor32(best * a.scale), mx);
+      if (__ballot(best * scale > mx + 8.0f) != 0) {
+        const float to = fmaxf(max_xor32(best * scale), mx);
         const float keep = mx == to ? 1.0f : exp2_hw(mx - to);
         mx = to;
         sum *= keep;
@@ -1057,27 +1158,31 @@ __global__ __launch_bounds__(256, (kv_tiles_waves<DT, D>())) void kda_kv_tiles_k
         for (int c = 0; c < CB; ++c) o[c] *= keep;
       }
       end_values(tb + KT);
-      const float base = mx == -INFINITY ? 0.0f : -mx;
+      // weights in fp16 are taken 2^7 times larger, at most 2^15
+      const float base = (mx == -INFINITY ? 0.0f : -mx) + (HALF ? 7.0f : 0.0f);
       // -- this tile's weights, the next one's scores: after each product the
       // vector work that fits beside it, operands read AHEAD products early
       constexpr int AHEAD = 2;
       u4 pf[4][NP], ring[AHEAD + 1];
+      if constexpr (PIPED) {
 #pragma unroll
-      for (int i = 0; i < AHEAD; ++i) ring[i] = key_piece(buf ^ 1, i);
+        for (int i = 0; i < AHEAD; ++i) ring[i] = key_piece(buf ^ 1, i);
+      }
 #pragma unroll
       for (int i = 0; i < 2 * KS; ++i) {
-        if (i + AHEAD < 2 * KS) ring[(i + AHEAD) % (AHEAD + 1)] = key_piece(buf ^ 1, i + AHEAD);
-        score(i, ring[i % (AHEAD + 1)], next);
+        if constexpr (PIPED) {
+          if (i + AHEAD < 2 * KS) ring[(i + AHEAD) % (AHEAD + 1)] = key_piece(buf ^ 1, i + AHEAD);
+          score(i, ring[i % (AHEAD + 1)], next);
+        }
         constexpr int EACH = 16 / KS;  // weights beside a product
 #pragma unroll
         for (int k = EACH * i; k < EACH * (i + 1); k += 2) {
           const int b = k / 16, e = k % 16;
-          const float w0 = exp2_hw(fmaf(sc[b][e], a.scale, base)), w1 = exp2_hw(fmaf(sc[b][e + 1], a.scale, base));
+          const float w0 = exp2_hw(fmaf(sc[b][e], scale, base)), w1 = exp2_hw(fmaf(sc[b][e + 1], scale, base));
           sum += w0 + w1;
           uint32_t x[NP];
-          if constexpr (NP == 1) {
-            const bf2 y = {static_cast<__bf16>(w0), static_cast<__bf16>(w1)};
-            x[0] = __builtin_bit_cast(uint32_t, y);
+          if constexpr (HALF) {
+            x[0] = __builtin_bit_cast(uint32_t, h2{static_cast<_Float16>(w0), static_cast<_Float16>(w1)});
           } else {
             split_pair<NP>(w0, w1, x);
           }
@@ -1094,11 +1199,13 @@ __global__ __launch_bounds__(256, (kv_tiles_waves<DT, D>())) void kda_kv_tiles_k
         constexpr int i = decltype(at)::value, G = 4 * CB, E = 32 / G;
         if (i + AHEAD < G) ring[(i + AHEAD) % (AHEAD + 1)] = value_piece(buf, i + AHEAD);
 #pragma unroll
-        for (int p = 0; p < NP; ++p) o[i % CB] = mfma32(ring[i % (AHEAD + 1)], pf[i / CB][p], o[i % CB]);
-        if constexpr (i % 4 == 0) stage_key(buf, i / 4);
+        for (int p = 0; p < NP; ++p) o[i % CB] = mfma32<HALF>(ring[i % (AHEAD + 1)], pf[i / CB][p], o[i % CB]);
+        if constexpr (i % 4 == 0) stage_key(buf, i / 4, tb + 2 * KT);
         if constexpr (i % 4 == 2) stage_value(buf ^ 1, std::integral_constant<int, i / 4>{});
+        if constexpr (PIPED) {
 #pragma unroll
-        for (int k = E * i; k < E * (i + 1); ++k) best = max_nan(best, next[k % 2][k / 2]);
+          for (int k = E * i; k < E * (i + 1); ++k) best = max_nan(best, next[k % 2][k / 2]);
+        }
         __builtin_amdgcn_sched_barrier(0);
       };
       each_of(output, std::make_integer_sequence<int, 4 * CB>{});
@@ -1109,34 +1216,56 @@ __global__ __launch_bounds__(256, (kv_tiles_waves<DT, D>())) void kda_kv_tiles_k
     for (int tb = t0; tb < t1; tb += 2 * KT) {
       step(tb, std::integral_constant<int, 0>{}, sc0, sc1);
       if (tb + KT >= t1) break;
-      step(tb + KT, std::integral_constant<int, 1>{}, sc1, sc0);
+      if constexpr (PIPED)
+        step(tb + KT, std::integral_constant<int, 1>{}, sc1, sc0);
+      else
+        step(tb + KT, std::integral_constant<int, 1>{}, sc0, sc1);
+    }
+    if constexpr (HALF) {
+      if (!__syncthreads_and(seen.in_half())) return false;
     }
 
+    // The lane's row and the arguments once more, from an opaque thread id and
+    // address: kept from above, they would be spilled over the steps.
+    int again = tid;
+    kernel_args args = (kernel_args)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+v"(again), "+s"(args));
     // -- rows out: element e of block c is row 8 (e / 4) + 4 half + e % 4 of
     // 32 c.., channel 2 c + e / 8 of the VC at VC (row % 16)
     sum = sum_xor32(sum);
-    if (row <= last_row) {
-      const int64_t at = (q.n0 + tok) * a.q_heads + static_cast<int64_t>(h) * a.group + g;
-      const int64_t slot = static_cast<int64_t>(sp) * a.t.n_tokens * a.q_heads + at;
+    const int out_half = again % 64 / 32, out_row = row0 + 32 * wave + again % 32;
+    if (out_row <= last_row) {
+      const int ot = out_row / args->group, og = out_row - ot * args->group;
+      const int64_t at = (q.n0 + ot) * args->q_heads + static_cast<int64_t>(h) * args->group + og;
+      const int64_t slot = static_cast<int64_t>(sp) * args->t.n_tokens * args->q_heads + at;
       const float inv = splits > 1 ? 1.0f : q.bad ? __builtin_nanf("") : sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int64_t c0 = VC * (8 * (e / 4) + 4 * half + e % 4);
+        const int64_t c0 = VC * (8 * (e / 4) + 4 * out_half + e % 4);
         float x[VC];
 #pragma unroll
         for (int n = 0; n < VC; ++n) x[n] = o[n / 2][8 * (n % 2) + e] * inv;
         if (splits == 1)
-          store_channels<DT>(a.out, at * D + c0, x);
+          store_channels<DT>(args->out, at * D + c0, x);
         else
-          store_channels<KDA_F32>(a.part, slot * D + c0, x);
+          store_channels<KDA_F32>(args->part, slot * D + c0, x);
       }
-      if (splits > 1 && half == 0) {
-        a.part_ml[2 * slot] = mx;
-        a.part_ml[2 * slot + 1] = sum;
+      if (splits > 1 && out_half == 0) {
+        args->part_ml[2 * slot] = mx - (HALF ? 7.0f : 0.0f);
+        args->part_ml[2 * slot + 1] = sum;
       }
     }
+    return true;
+    };
+    if constexpr (DT == KDA_F32) {
+      attend(std::false_type{});
+    } else {
+      if (!attend(std::true_type{})) attend(std::false_type{});
+    }
+    __syncthreads();
   }
 }
+
 
 // Joins the splits of a row, ROWS rows a block of four waves: with few splits a
 // wave a row, with many all four on one.  D / 8 lanes lie across the channels,
@@ -1157,14 +1286,13 @@ __global__ __launch_bounds__(256) void kda_kv_join_kernel(KvAttendArgs a, int ti
   const int s = id / slices / a.row_tiles / a.t.H;
   const Seq q = seq_of(a.t, s);
   if (q.skip || q.bad) return;
-  const int64_t all_rows = static_cast<int64_t>(q.rows) * a.group;
+  const int all_rows = q.rows * a.group;
   const int64_t stride = a.t.n_tokens * a.q_heads;
-  for (int64_t rt = rt0; rt * tile_rows + r < all_rows; rt += a.row_tiles) {
-    const int64_t row = rt * tile_rows + r;
-    const int64_t last = (rt + 1) * tile_rows < all_rows ? (rt + 1) * tile_rows - 1 : all_rows - 1;
-    const int splits = kv_splits(q.past + static_cast<int>(last / a.group) + 1, a);
+  for (int row = rt0 * tile_rows + r; row < all_rows; row += a.row_tiles * tile_rows) {
+    const int end = row - r + tile_rows;  // of the tile
+    const int splits = kv_splits(q.past + ((end < all_rows ? end : all_rows) - 1) / a.group + 1, a);
     if (splits <= 1) continue;  // written already
-    const int tok = static_cast<int>(row / a.group), g = static_cast<int>(row - static_cast<int64_t>(tok) * a.group);
+    const int tok = row / a.group, g = row - tok * a.group;
     const int64_t at = (q.n0 + tok) * a.q_heads + static_cast<int64_t>(h) * a.group + g;
     float acc[8] = {}, total = 0.0f, top = -INFINITY;
     // (m, l, x) joins this lane's; a side without a finite maximum holds
@@ -1372,7 +1500,7 @@ extern "C" int kda_kv_attend(const kda_kv_pool* kv, const int32_t* page_table, i
   if (q_heads < 1 || q_heads > 65535 || q_heads % kv->H != 0) return KDA_ERR_SHAPE;
   if (max_rows < 0 || max_kv_len < 0 || !std::isfinite(scale)) return KDA_ERR_ARG;
   // a row index is token * group + head within the group
-  if (n_tokens * (q_heads / kv->H) > INT32_MAX / 2) return KDA_ERR_ARG;
+  if (n_tokens * (q_heads / kv->H) > INT32_MAX / 4) return KDA_ERR_ARG;
   if (n_seq == 0 || n_tokens == 0) return KDA_OK;
   if (page_table == nullptr || cu_seqlens == nullptr || cache_lens == nullptr || q == nullptr || out == nullptr)
     return KDA_ERR_NULL;
