@@ -564,7 +564,8 @@ def kv_pool_shape(n_pages: int, H: int, page_tokens: int, D: int):
 def make_kv_pool(pool) -> kda_kv_pool:
     """kda_kv_pool describing a contiguous uint8 GPU tensor of kv_pool_shape."""
     import torch
-    _on_gpu(pool, "pool")
+    if not isinstance(pool, torch.Tensor) or not pool.is_cuda:
+        _on_gpu(pool, "pool")
     if pool.dtype is not torch.uint8 or pool.dim() != 4 or not pool.is_contiguous():
         raise ValueError("a cache must be a contiguous uint8 tensor [n_pages, H, page_tokens, 17 D / 16]")
     n_pages, H, P, width = pool.shape
@@ -573,23 +574,31 @@ def make_kv_pool(pool) -> kda_kv_pool:
     return kda_kv_pool(pool.data_ptr(), n_pages, P, H, width // 17 * 16)
 
 
-def _kv_tensor(t, name, device, dtype):
-    """Refuses what is not a tensor of this type on this GPU (its index).  A
-    decode step's launches take a few microseconds each: these checks are kept
-    to one attribute read apiece."""
+def _kv_refuse(t, name, device, dtype):
+    """Says what is wrong with a tensor that is not of this type on this GPU."""
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch tensor" % name)
     if t.get_device() != device:
         raise TypeError("%s is on %s, the pool on GPU %d" % (name, t.device, device))
-    if t.dtype is not dtype:
-        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+
+
+# A decode step's launches take a few microseconds each, so the checks below
+# read each attribute once and leave the wording of a refusal to the above.
+
+def _kv_is(t, device, dtype):
+    try:
+        return t.get_device() == device and t.dtype is dtype
+    except AttributeError:
+        return False
 
 
 def _kv_rows(t, name, device, dtype, n_tokens, heads, D, gaps=True):
     """Address and token stride of a token tensor [n_tokens, heads, D] whose
     heads and channels lie without gaps (nor its tokens, unless gaps)."""
-    _kv_tensor(t, name, device, dtype)
+    if not _kv_is(t, device, dtype):
+        _kv_refuse(t, name, device, dtype)
     if t.shape != (n_tokens, heads, D):
         raise ValueError("%s must be [%d, %d, %d], got %s" % (name, n_tokens, heads, D, list(t.shape)))
     row, head, channel = t.stride()
@@ -600,14 +609,13 @@ def _kv_rows(t, name, device, dtype, n_tokens, heads, D, gaps=True):
     return t.data_ptr(), row
 
 
-def _kv_tables(device, page_table, cu_seqlens, lens):
+def _kv_tables(device, i32, page_table, cu_seqlens, lens):
     """The checked tables of a cache launch: addresses of the page table,
     max_pages, addresses of cu_seqlens and lengths; n_seq."""
-    import torch
-    i32 = torch.int32
-    _kv_tensor(page_table, "page_table", device, i32)
-    _kv_tensor(cu_seqlens, "cu_seqlens", device, i32)
-    _kv_tensor(lens, "cache_lens", device, i32)
+    if not (_kv_is(page_table, device, i32) and _kv_is(cu_seqlens, device, i32) and _kv_is(lens, device, i32)):
+        for t, name in ((page_table, "page_table"), (cu_seqlens, "cu_seqlens"), (lens, "cache_lens")):
+            if not _kv_is(t, device, i32):
+                _kv_refuse(t, name, device, i32)
     if not (page_table.is_contiguous() and cu_seqlens.is_contiguous() and lens.is_contiguous()):
         raise ValueError("page_table, cu_seqlens and cache_lens must be contiguous")
     if page_table.dim() != 2:
@@ -618,9 +626,8 @@ def _kv_tables(device, page_table, cu_seqlens, lens):
     return (page_table.data_ptr(), max_pages, cu_seqlens.data_ptr(), lens.data_ptr()), n_seq
 
 
-def _kv_stream(device, stream):
+def _kv_stream(torch, device, stream):
     """The stream's address: by default the current one of the pool's device."""
-    import torch
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(device)
     if isinstance(stream, int):
@@ -630,10 +637,9 @@ def _kv_stream(device, stream):
     return stream.cuda_stream
 
 
-def _kv_call(name, device, *args):
+def _kv_call(torch, name, device, *args):
     """Calls the library with the pool's device as the current one."""
-    import torch
-    fn = getattr(library(), name)
+    fn = getattr(_lib or library(), name)
     if torch.cuda.current_device() == device:
         rc = fn(*args)
     else:
@@ -655,7 +661,7 @@ def kda_kv_append(pool, page_table, cu_seqlens, cache_lens, k, v, q=None, q_out=
     sin: None, or float32 [n_positions, rot_dim / 2]."""
     import torch
     P, dev = make_kv_pool(pool), pool.get_device()
-    tables, n_seq = _kv_tables(dev, page_table, cu_seqlens, cache_lens)
+    tables, n_seq = _kv_tables(dev, torch.int32, page_table, cu_seqlens, cache_lens)
     T, dtype, H, D = k.shape[0], k.dtype, P.H, P.D
     kp, ks = _kv_rows(k, "k", dev, dtype, T, H, D)
     vp, vs = _kv_rows(v, "v", dev, dtype, T, H, D)
@@ -670,30 +676,32 @@ def kda_kv_append(pool, page_table, cu_seqlens, cache_lens, k, v, q=None, q_out=
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin go together")
     if cos is not None:
-        _kv_tensor(cos, "cos", dev, torch.float32)
-        _kv_tensor(sin, "sin", dev, torch.float32)
+        for t, name in ((cos, "cos"), (sin, "sin")):
+            if not _kv_is(t, dev, torch.float32):
+                _kv_refuse(t, name, dev, torch.float32)
         if cos.dim() != 2 or cos.shape != sin.shape or not (cos.is_contiguous() and sin.is_contiguous()):
             raise ValueError("cos and sin must be contiguous [n_positions, rot_dim / 2], both")
         positions, half = cos.shape
         cp, sp = cos.data_ptr(), sin.data_ptr()
-    _kv_call("kda_kv_append", dev, ctypes.byref(P), *tables, kp, vp, ks, vs, qp, qs, qo, cp, sp, positions, 2 * half,
-             int(interleaved), n_seq, T, heads, dtype_code(dtype), _kv_stream(dev, stream))
+    _kv_call(torch, "kda_kv_append", dev, ctypes.byref(P), *tables, kp, vp, ks, vs, qp, qs, qo, cp, sp, positions, 2 * half,
+             int(interleaved), n_seq, T, heads, dtype_code(dtype), _kv_stream(torch, dev, stream))
 
 
 def kda_kv_read(pool, page_table, cu_seqlens, first, k_out=None, v_out=None, stream=None) -> None:
     """Reads cached keys and values back (see kda_kv_read in
     include/kda_decode.h): token i of sequence s gets position first[s] + i.
     k_out, v_out: [T, H, D] of one floating type; either may be None."""
+    import torch
     P, dev = make_kv_pool(pool), pool.get_device()
-    tables, n_seq = _kv_tables(dev, page_table, cu_seqlens, first)
+    tables, n_seq = _kv_tables(dev, torch.int32, page_table, cu_seqlens, first)
     some = k_out if k_out is not None else v_out
     if some is None:
         raise ValueError("nothing to read into: k_out and v_out are both None")
     T, dtype = some.shape[0], some.dtype
     kp, ks = (0, 0) if k_out is None else _kv_rows(k_out, "k_out", dev, dtype, T, P.H, P.D)
     vp, vs = (0, 0) if v_out is None else _kv_rows(v_out, "v_out", dev, dtype, T, P.H, P.D)
-    _kv_call("kda_kv_read", dev, ctypes.byref(P), *tables, kp, vp, ks, vs, n_seq, T, dtype_code(dtype),
-             _kv_stream(dev, stream))
+    _kv_call(torch, "kda_kv_read", dev, ctypes.byref(P), *tables, kp, vp, ks, vs, n_seq, T, dtype_code(dtype),
+             _kv_stream(torch, dev, stream))
 
 
 def kda_kv_attend_workspace(pool, page_table, n_tokens: int, q_heads: int, max_rows: int, max_kv_len: int = 0,
@@ -718,16 +726,16 @@ def kda_kv_attend(pool, page_table, cu_seqlens, cache_lens, q, out, max_rows: in
     None to take one from torch's allocator on the launch's stream."""
     import torch
     P, dev = make_kv_pool(pool), pool.get_device()
-    tables, n_seq = _kv_tables(dev, page_table, cu_seqlens, cache_lens)
+    tables, n_seq = _kv_tables(dev, torch.int32, page_table, cu_seqlens, cache_lens)
     if q.dim() != 3:
         raise ValueError("q must be [T, q_heads, D], got %s" % list(q.shape))
     (T, heads, _), dtype, D = q.shape, q.dtype, P.D
     qp, qs = _kv_rows(q, "q", dev, dtype, T, heads, D)
     op, _ = _kv_rows(out, "out", dev, dtype, T, heads, D, gaps=False)
-    rows, kv, code, st = T if max_rows is None else int(max_rows), int(max_kv_len), dtype_code(dtype), _kv_stream(dev, stream)
+    rows, kv, code, st = T if max_rows is None else int(max_rows), int(max_kv_len), dtype_code(dtype), _kv_stream(torch, dev, stream)
     pool_ref = ctypes.byref(P)
     if workspace is None:
-        wn = library().kda_kv_attend_workspace(pool_ref, tables[1], n_seq, T, rows, kv, heads, code)
+        wn = (_lib or library()).kda_kv_attend_workspace(pool_ref, tables[1], n_seq, T, rows, kv, heads, code)
         if wn == 0 or st == torch._C._cuda_getCurrentRawStream(dev):
             workspace = torch.empty(wn, dtype=torch.uint8, device=pool.device)
         else:
@@ -736,11 +744,12 @@ def kda_kv_attend(pool, page_table, cu_seqlens, cache_lens, q, out, max_rows: in
             with torch.cuda.stream(on):
                 workspace = torch.empty(wn, dtype=torch.uint8, device=pool.device)
     else:
-        _kv_tensor(workspace, "workspace", dev, torch.uint8)
+        if not _kv_is(workspace, dev, torch.uint8):
+            _kv_refuse(workspace, "workspace", dev, torch.uint8)
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
         wn = workspace.numel()
-    _kv_call("kda_kv_attend", dev, pool_ref, *tables, qp, qs, op, n_seq, T, rows, kv, heads, code,
+    _kv_call(torch, "kda_kv_attend", dev, pool_ref, *tables, qp, qs, op, n_seq, T, rows, kv, heads, code,
              1.0 / math.sqrt(D) if scale is None else float(scale), workspace.data_ptr(), wn, st)
 
 
