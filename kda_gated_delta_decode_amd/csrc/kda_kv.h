@@ -80,6 +80,7 @@ struct KvPlan {
   int32_t row_tiles;
   int32_t chunk;
   int32_t n_splits;
+  int32_t waves;      // of a workgroup
 };
 
 KvPlan kv_plan(int32_t H, int32_t D, int32_t n_seq, int64_t n_tokens, int32_t max_rows,

@@ -512,9 +512,10 @@ __device__ __forceinline__ float max_xor32(float x) {
 
 // Waves a SIMD: three in 168 registers hide more of a step's latency than two
 // (64 ragged requests at up to 8192 tokens: 85 -> 81 us; four would spill); with
-// two row tiles two (32 rows of 8 requests at 4097 tokens: 28 -> 26 us).
-template <int NT>
-constexpr int kv_rows_waves() { return NT == 1 ? 3 : 2; }
+// two row tiles two (32 rows of 8 requests at 4097 tokens: 28 -> 26 us).  Eight
+// waves a workgroup are for launches that leave most of the chip idle: two.
+template <int NT, int NW>
+constexpr int kv_rows_waves() { return NT == 1 && NW == 4 ? 3 : 2; }
 
 // Few rows: 16 * NT rows of one sequence and cached head against one split of
 // its tokens, over NW waves.
@@ -532,7 +533,7 @@ constexpr int kv_rows_waves() { return NT == 1 ? 3 : 2; }
 // loaded as soon as the scores have used this step's, its values likewise, so
 // one set of registers keeps loads in flight all the time.
 template <int DT, int D, int NT, int NW>
-__global__ __launch_bounds__(64 * NW, kv_rows_waves<NT>()) void kda_kv_rows_kernel(KvAttendArgs a) {
+__global__ __launch_bounds__(64 * NW, (kv_rows_waves<NT, NW>())) void kda_kv_rows_kernel(KvAttendArgs a) {
   constexpr int NQ = q_pieces<DT>(), NP = w_pieces<DT>();
   constexpr int M = D / 32;   // products over the channels
   constexpr int C = D / 16;   // channels of a lane in the second product, and its row tiles
@@ -1538,6 +1539,8 @@ extern "C" int kda_kv_attend(const kda_kv_pool* kv, const int32_t* page_table, i
     const dim3 grid(static_cast<uint32_t>(blocks));
     if (p.tile_rows == 128)
       hipLaunchKernelGGL((kda_kv_tiles_kernel<DT, D>), grid, dim3(256), 0, st, a);
+    else if (p.waves == 8)
+      hipLaunchKernelGGL((kda_kv_rows_kernel<DT, D, 1, 8>), grid, dim3(512), 0, st, a);
     else if (DT == KDA_F32 || p.tile_rows == 16)
       hipLaunchKernelGGL((kda_kv_rows_kernel<DT, D, 1, 4>), grid, dim3(256), 0, st, a);
     else if constexpr (DT != KDA_F32)

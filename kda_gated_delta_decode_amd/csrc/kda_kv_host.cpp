@@ -45,7 +45,14 @@ KvPlan kv_plan(int32_t H, int32_t D, int32_t n_seq, int64_t n_tokens, int32_t ma
     return c < least ? least : c;
   };
   int64_t chunk;
-  if (p.tile_rows < 128) {
+  p.waves = 4;
+  if (p.tile_rows == 16 && units <= 256 && max_kv_len <= 512) {
+    // Small: eight waves take at most two steps each, and no second launch
+    // joins splits (one token at 256, 512: 5.6, 6.8 us against 7.5, 7.6; at
+    // 1001 it would be 9.5 against 8.1).
+    p.waves = 8;
+    chunk = max_kv_len;
+  } else if (p.tile_rows < 128) {
     // Few rows.  768 workgroups are resident at once (three a compute unit).
     // One sequence: its splits are all alike, and one round of them is best
     // (131072 tokens, 8 cached heads: 38 us; 39.5 with 1024, 43 with 1536).
