@@ -1268,25 +1268,27 @@ __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tiles_kerne
 }
 
 
-// Joins the splits of a row, ROWS rows a block of four waves: with few splits a
-// wave a row, with many all four on one.  D / 8 lanes lie across the channels,
-// the others (and the waves) across the splits, each with a maximum and sum of
-// its own, so that no load waits for another split's.
-template <int DT, int D, int ROWS>
+// Joins the splits of rows, D / 8 lanes across a row's channels.  Few splits:
+// the lanes take theirs one after the other, four loads in flight, and a block
+// takes 256 / (D / 8) rows.  MANY: a row has a whole block, splits lie across
+// its lane groups, each with a maximum and sum of its own, so that no load
+// waits for another split's.
+template <int DT, int D, bool MANY>
 __global__ __launch_bounds__(256) void kda_kv_join_kernel(KvAttendArgs a, int tile_rows) {
-  constexpr int PER = D / 8, W = 4 / ROWS;  // lanes of a row's channels, waves of a row
-  constexpr int G = 64 / PER * W;           // splits taken at once
+  constexpr int PER = D / 8, W = MANY ? 4 : 1;      // lanes of a row's channels, waves of a row
+  constexpr int ROWS = MANY ? 1 : 256 / PER;
+  constexpr int G = MANY ? 256 / PER : 1;           // splits taken at once
   __shared__ float part_sh[W][PER][10];
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-  const int c = 8 * (lane % PER), grp = lane / PER + (W > 1 ? 64 / PER * wave : 0);
-  const int slices = tile_rows / ROWS;
+  const int c = 8 * (lane % PER), grp = MANY ? threadIdx.x / PER : 0;
+  const int slices = (tile_rows + ROWS - 1) / ROWS;
   const int id = blockIdx.x;
-  const int r = (id % slices) * ROWS + (W > 1 ? 0 : wave);
+  const int r = (id % slices) * ROWS + (MANY ? 0 : threadIdx.x / PER);
   const int rt0 = (id / slices) % a.row_tiles;
   const int h = (id / slices / a.row_tiles) % a.t.H;
   const int s = id / slices / a.row_tiles / a.t.H;
   const Seq q = seq_of(a.t, s);
-  if (q.skip || q.bad) return;
+  if (q.skip || q.bad || r >= tile_rows) return;
   const int all_rows = q.rows * a.group;
   const int64_t stride = a.t.n_tokens * a.q_heads;
   for (int row = rt0 * tile_rows + r; row < all_rows; row += a.row_tiles * tile_rows) {
@@ -1313,15 +1315,15 @@ __global__ __launch_bounds__(256) void kda_kv_join_kernel(KvAttendArgs a, int ti
       load8<KDA_F32>(a.part, slot * D + c, x);
       join(a.part_ml[2 * slot], a.part_ml[2 * slot + 1], x);
     }
+    if constexpr (MANY) {
 #pragma unroll
-    for (int m = PER; m < 64; m *= 2) {
-      float x[8];
+      for (int m = PER; m < 64; m *= 2) {
+        float x[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = __shfl_xor(acc[e], m);
-      const float om = __shfl_xor(top, m), ol = __shfl_xor(total, m);
-      join(om, ol, x);
-    }
-    if constexpr (W > 1) {
+        for (int e = 0; e < 8; ++e) x[e] = __shfl_xor(acc[e], m);
+        const float om = __shfl_xor(top, m), ol = __shfl_xor(total, m);
+        join(om, ol, x);
+      }
       if (lane < PER) {
         part_sh[wave][lane][8] = top;
         part_sh[wave][lane][9] = total;
@@ -1343,7 +1345,7 @@ __global__ __launch_bounds__(256) void kda_kv_join_kernel(KvAttendArgs a, int ti
     const float inv = total == 0.0f ? 0.0f : 1.0f / total;
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] *= inv;
-    if (lane < PER && (W == 1 || wave == 0)) store8<DT>(a.out, at * D + c, acc);
+    if (!MANY || threadIdx.x < PER) store8<DT>(a.out, at * D + c, acc);
   }
 }
 
@@ -1547,13 +1549,14 @@ extern "C" int kda_kv_attend(const kda_kv_pool* kv, const int32_t* page_table, i
       hipLaunchKernelGGL((kda_kv_rows_kernel<DT, D, 2, 4>), grid, dim3(256), 0, st, a);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && p.n_splits > 1) {
-      // one wave up to 8 splits a row (2 rounds of loads), else a block
+      // up to 8 splits a row in two rounds of loads, more side by side
       const uint32_t tiles = static_cast<uint32_t>(n_seq) * kv->H * p.row_tiles;
+      constexpr int rows = 256 / (D / 8);
       if (p.n_splits <= 8)
-        hipLaunchKernelGGL((kda_kv_join_kernel<DT, D, 4>), dim3(tiles * (p.tile_rows / 4)), dim3(256), 0, st, a,
-                           p.tile_rows);
+        hipLaunchKernelGGL((kda_kv_join_kernel<DT, D, false>), dim3(tiles * ((p.tile_rows + rows - 1) / rows)), dim3(256),
+                           0, st, a, p.tile_rows);
       else
-        hipLaunchKernelGGL((kda_kv_join_kernel<DT, D, 1>), dim3(tiles * p.tile_rows), dim3(256), 0, st, a, p.tile_rows);
+        hipLaunchKernelGGL((kda_kv_join_kernel<DT, D, true>), dim3(tiles * p.tile_rows), dim3(256), 0, st, a, p.tile_rows);
       e = hipGetLastError();
     }
     return e;
