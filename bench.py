@@ -20,8 +20,8 @@ one HIP graph, back to back), against the 8 TB/s HBM peak; traffic =
 hardware byte counters of the committed rocprofv3 summary when it was taken
 on this kernel source, else null; cpu_baseline = the CPU oracle timed on a
 bounded sample of the same workload.  Extra keys report the other workloads
-(fp16 pool, 8 x 8 speculative rows, a 69-layer step) and a plain-copy
-bandwidth probe.
+(fp16 pool, 8 x 8 speculative rows, a 69-layer step, decode steps over the
+4-bit key/value cache) and a plain-copy bandwidth probe.
 """
 from __future__ import annotations
 
@@ -467,6 +467,7 @@ def main():
             extras["prefill_" + args.dtype] = prefill_extra(args.dtype, B, torch, 20)
         if args.extras == "all":
             extras["long_run_8192"] = long_run_extra(B, torch)
+            extras["kv_cache_bf16"] = kv_extra(B, torch, 20)
         # a 69-layer decode step: 69 independent 64-slot pools, one launch each
         for dt in (("f32", "f16") if args.extras == "all" else ()):
             extras["layers69_" + dt] = layers69(dt, B, torch, steps=10, warmup=2)
@@ -724,6 +725,54 @@ def prefill_extra(dtype, B, torch, steps):
                         "traffic": None, "algorithmic_flops_per_launch": flops},
            "hbm_GB/s": round(inp.io_bytes() / (us * 1e-6) / 1e9, 1)}
     del pool, t, out
+    return res
+
+
+def kv_extra(B, torch, steps):
+    """Time the 4-bit key/value cache of the softmax-attention layers on decode
+    steps (bf16, H = 12 cached heads of 128 channels, 128-token pages, 4096
+    tokens a request): 64 requests x 1 token, and 8 requests x 8 chained rows.
+    A step is one append (with the rotation) and one attention.  Successive
+    steps rotate over caches of more than 256 MiB in all; cache GB/s counts
+    each visible token's key and value once."""
+    dev = torch.device("cuda", 0)
+    H, D, P, past = 12, 128, 128, 4088
+    res = {}
+    for n_req, rows in ((64, 1), (8, 8)):
+        need = (past + rows + P - 1) // P
+        copies = max(2, math.ceil((1 << 29) / (n_req * need * H * P * 136)))
+        pools = [torch.randint(0, 256, B.kv_pool_shape(n_req * need, H, P, D), dtype=torch.uint8, device=dev)
+                 for _ in range(copies)]
+        for pool in pools:  # random codes; exponents of ordinary activations
+            pool.view(n_req * need, H, -1)[..., P * D:] = 125
+        table = torch.randperm(n_req * need, device=dev).to(torch.int32).view(n_req, need)
+        cu = torch.arange(0, n_req * rows + 1, rows, dtype=torch.int32, device=dev)
+        lens = torch.full((n_req,), past, dtype=torch.int32, device=dev)
+        qkv = torch.randn((n_req * rows, 3 * H, D), device=dev).to(torch.bfloat16)
+        q, k, v = qkv.split(H, 1)
+        angle = torch.arange(past + rows, device=dev).unsqueeze(1) * 10000.0 ** (-torch.arange(64, device=dev) / 64)
+        cos, sin = angle.cos(), angle.sin()
+        q_out, out = (torch.empty((n_req * rows, H, D), dtype=torch.bfloat16, device=dev) for _ in range(2))
+
+        def append(i):
+            B.kda_kv_append(pools[i % copies], table, cu, lens, k, v, q=q, q_out=q_out, cos=cos, sin=sin)
+
+        def attend(i):
+            B.kda_kv_attend(pools[i % copies], table, cu, lens, q_out, out, max_rows=rows, max_kv_len=past + rows)
+
+        def step(i):
+            append(i)
+            attend(i)
+
+        step(0)
+        us = {name: time_launches(fn, steps, 3, torch)["ms_per_step"] * 1e3
+              for name, fn in (("append", append), ("attend", attend), ("step", step))}
+        read = n_req * (past + rows) * H * 136
+        res["%dx%d" % (n_req, rows)] = {"us_per_" + n: round(t, 2) for n, t in us.items()}
+        res["%dx%d" % (n_req, rows)].update(
+            {"cache_bytes_read": read, "attend_cache_GB/s": round(read / us["attend"] / 1e3, 1),
+             "frac_of_hbm_peak": round(read / us["attend"] / 1e3 / HBM_PEAK_GBS, 4)})
+        del pools
     return res
 
 

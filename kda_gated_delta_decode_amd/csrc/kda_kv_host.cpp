@@ -64,10 +64,10 @@ KvPlan kv_plan(int32_t H, int32_t D, int32_t n_seq, int64_t n_tokens, int32_t ma
     if (per(max_kv_len, chunk) * units < 256) chunk = chunk_of(256, 128);
   } else {
     // Many rows, two workgroups a compute unit: one round of them for one
-    // sequence, two for several, whose rows and lengths differ (4 chunks of up
-    // to 700 rows on up to 16000 tokens: 305 us with 3 splits; 450, 380 and 335
-    // with 1, 2 and 4).
-    chunk = n_seq > 1 ? chunk_of(per(1024, units) * units, 1024) : chunk_of(512, 1024);
+    // sequence (512 rows on 15000 tokens: 165 us; 190, 220 for 1024, 1536), three
+    // for several, whose rows and lengths differ (4 chunks of up to 700 rows on up
+    // to 16000 tokens: 213 us; 231, 296 for 1024, 512).
+    chunk = n_seq > 1 ? chunk_of(per(1536, units) * units, 1024) : chunk_of(512, 1024);
   }
   chunk = per(chunk, 128) * 128;
   if (chunk < 128) chunk = 128;
