@@ -203,21 +203,52 @@ __device__ __forceinline__ float sticky_float(double d) {
 // 8 channels as they lie in memory
 template <int DT>
 struct Raw8 {
-  u4 w[DT == KDA_F32 ? 2 : 1];
+  static constexpr int N = DT == KDA_F32 ? 2 : 1;
+  u4 w[N];
 
+  template <bool STREAM>
   __device__ __forceinline__ void load(const void* p, int64_t at) {
     const u4* s = reinterpret_cast<const u4*>(static_cast<const uint8_t*>(p) + at * elem_bytes<DT>());
-    w[0] = s[0];
-    if constexpr (DT == KDA_F32) w[1] = s[1];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if constexpr (STREAM)
+        w[i] = __builtin_nontemporal_load(s + i);
+      else
+        w[i] = s[i];
+    }
+  }
+  template <bool STREAM>
+  __device__ __forceinline__ void store(void* p, int64_t at) const {
+    u4* d = reinterpret_cast<u4*>(static_cast<uint8_t*>(p) + at * elem_bytes<DT>());
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if constexpr (STREAM)
+        __builtin_nontemporal_store(w[i], d + i);
+      else
+        d[i] = w[i];
+    }
   }
   // those of another lane
   __device__ __forceinline__ Raw8 of(int lane) const {
     Raw8 r;
 #pragma unroll
-    for (int i = 0; i < (DT == KDA_F32 ? 2 : 1); ++i)
+    for (int i = 0; i < N; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) r.w[i][e] = __builtin_amdgcn_ds_bpermute(4 * lane, w[i][e]);
     return r;
+  }
+  // rounded to nearest even, once
+  __device__ __forceinline__ void set(const float (&x)[8]) {
+    if constexpr (DT == KDA_F32) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e / 4][e % 4] = bits(x[e]);
+    } else {
+      using T = std::conditional_t<DT == KDA_F16, _Float16, __bf16>;
+      T __attribute__((ext_vector_type(8))) y;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = static_cast<T>(x[e]);
+      w[0] = __builtin_bit_cast(u4, y);
+    }
   }
   __device__ __forceinline__ void numbers(float (&x)[8]) const {
     if constexpr (DT == KDA_F32) {
@@ -242,8 +273,9 @@ struct Raw8 {
 // angles are looked up once, and a pair's other half, when another lane holds
 // it, comes from that lane.  Neighbouring groups take neighbouring tokens of
 // the same unit, so a wave writes 256 contiguous bytes of codes.  Queries are
-// most of the bytes: four heads' loads are in flight together.
-template <int DT, int D>
+// most of the bytes: four heads' loads are in flight together.  STREAM: inputs
+// that the caches cannot hold anyway pass them by.
+template <int DT, int D, bool STREAM>
 __global__ __launch_bounds__(256) void kda_kv_append_kernel(KvAppendArgs a) {
   constexpr int W = D / 8, AT_ONCE = 4;
   const int li = threadIdx.x % W;
@@ -294,7 +326,8 @@ __global__ __launch_bounds__(256) void kda_kv_append_kernel(KvAppendArgs a) {
   for (; u < u1 && u < a.t.H; ++u) {
     Raw8<DT> rk;
     float x[8], p[8], v[8];
-    rk.load(a.k, token * a.k_stride + u * D + c0);
+    rk.template load<STREAM>(a.k, token * a.k_stride + u * D + c0);
+    // (values without the hint: 8192 fp32 tokens 85 us, with it 96)
     load8<DT>(a.v, token * a.v_stride + u * D + c0, v);
     pairs(rk, x, p);
     // the keys' rotation and scaling in 64 bits: a code next to a rounding
@@ -341,7 +374,7 @@ __global__ __launch_bounds__(256) void kda_kv_append_kernel(KvAppendArgs a) {
     Raw8<DT> r[AT_ONCE];
 #pragma unroll
     for (int i = 0; i < AT_ONCE; ++i)
-      if (u + i < u1) r[i].load(a.q, token * a.q_stride + (u + i - a.t.H) * D + c0);
+      if (u + i < u1) r[i].template load<STREAM>(a.q, token * a.q_stride + (u + i - a.t.H) * D + c0);
 #pragma unroll
     for (int i = 0; i < AT_ONCE; ++i) {
       if (u + i >= u1) break;
@@ -350,7 +383,8 @@ __global__ __launch_bounds__(256) void kda_kv_append_kernel(KvAppendArgs a) {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
         x[e] = at.what == kBad ? __builtin_nanf("") : turned ? x[e] * cs[e] + p[e] * sn[e] : x[e];
-      store8<DT>(a.q_out, (token * a.q_heads + u + i - a.t.H) * D + c0, x);
+      r[i].set(x);
+      r[i].template store<STREAM>(a.q_out, (token * a.q_heads + u + i - a.t.H) * D + c0);
     }
   }
 }
@@ -1449,8 +1483,15 @@ extern "C" int kda_kv_append(const kda_kv_pool* kv, const int32_t* page_table, i
   if (tiles * a.unit_blocks > INT32_MAX) return KDA_ERR_ARG;
   hipStream_t st = static_cast<hipStream_t>(stream);
   return status(by_type(dtype, kv->D, [&](auto t, auto d) {
-    hipLaunchKernelGGL((kda_kv_append_kernel<decltype(t)::value, decltype(d)::value>),
-                       dim3(static_cast<uint32_t>(tiles * a.unit_blocks)), dim3(256), 0, st, a);
+    constexpr int DT = decltype(t)::value, D = decltype(d)::value;
+    const dim3 grid(static_cast<uint32_t>(tiles * a.unit_blocks));
+    // From 96 MiB of inputs on loads and stores pass the caches by (32 query and
+    // 8 cached heads in bf16: 8192 tokens 63 -> 58 us, 32768 188 -> 166; 4096, which
+    // the last-level cache still holds from the projection before, 28.7 -> 30.7).
+    if ((kv_row * 2 + q_row) * size * n_tokens >= (96ll << 20))
+      hipLaunchKernelGGL((kda_kv_append_kernel<DT, D, true>), grid, dim3(256), 0, st, a);
+    else
+      hipLaunchKernelGGL((kda_kv_append_kernel<DT, D, false>), grid, dim3(256), 0, st, a);
     return hipGetLastError();
   }));
 }
