@@ -16,6 +16,7 @@ constexpr int kKvMinExp = 2;      // exponent bytes stored: every value a normal
 constexpr int kKvMaxExp = 252;    //   and 6 * 2^(252 - 127) finite
 constexpr int kKvPoison = 255;    // key exponent of a token whose key or value was not finite
 constexpr int kKvMaxHeads = 4096;
+constexpr int64_t kKvMaxBlocks = INT32_MAX / 512;  // a launch's threads stay below 2^31
 
 // Bytes of one (page, head) block of P tokens of D channels: key codes
 // [P][D/2], value codes [P][D/2], key exponents [P][D/32], value exponents
@@ -70,6 +71,7 @@ struct KvAttendArgs {
   int32_t q_heads, group;       // group: query heads of one cached head
   int32_t chunk, n_splits;      // tokens a split covers
   int32_t row_tiles;            // tiles of rows a sequence is given blocks for
+  int32_t slots;                // 128-row tiles: places for all sequences' tiles
   float scale;                  // |scale| * log2(e)
   float sign;                   // of scale: queries are multiplied by it
 };
@@ -77,7 +79,8 @@ struct KvAttendArgs {
 // How kda_kv_attend takes a launch.
 struct KvPlan {
   int32_t tile_rows;  // rows (tokens x query heads of one cached head) a workgroup takes
-  int32_t row_tiles;
+  int32_t row_tiles;  // as in KvAttendArgs
+  int32_t slots;
   int32_t chunk;
   int32_t n_splits;
   int32_t waves;      // of a workgroup

@@ -488,6 +488,28 @@ __device__ __forceinline__ int kv_splits(int vis, const KvAttendArgs& a) {
   return n < a.n_splits ? n : a.n_splits;
 }
 
+// Tiles of 128 rows lie in slots, sequence s's from slot
+// floor(cu[s] group / 128) + s on: no fewer slots than tiles, and n_tokens group
+// / 128 + n_seq of them in all, however the rows are spread over sequences.
+constexpr int kTileRows = 128;
+struct TileAt {
+  int s, tile;  // tile < 0: none
+};
+__device__ __forceinline__ TileAt tile_of_slot(const KvAttendArgs& a, int slot) {
+  const int lane = threadIdx.x % 64;
+  int lo = 0, hi = a.t.n_seq;
+  while (hi - lo > 1) {  // 64 lanes search together, as find_token
+    const int step = (hi - lo + 63) / 64;
+    const int i = lo + step * (lane + 1);
+    const bool before = i < hi && static_cast<int64_t>(a.t.cu[i]) * a.group / kTileRows + i <= slot;
+    lo += step * __popcll(__ballot(before));
+    hi = lo + step < hi ? lo + step : hi;
+  }
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  const int64_t first = static_cast<int64_t>(a.t.cu[lo]) * a.group / kTileRows + lo;
+  return {lo, first > slot ? -1 : static_cast<int>(slot - first)};
+}
+
 // bf16 pieces that represent a type's numbers exactly: 24, 11 or 8
 // significant bits, 8 a piece.
 template <int DT>
@@ -928,7 +950,7 @@ __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tiles_kerne
   constexpr int KS = D / 16;        // products over the channels
   constexpr int CB = D / 32;        // 32-channel blocks
   constexpr int VC = D / 16;        // channels of a thread's values
-  constexpr int R = 128;
+  constexpr int R = kTileRows;
   constexpr int KROW = 2 * D + 16, VROW = 2 * KT + 16;  // LDS bytes of a token's key, of a channel's values
   constexpr int KBUF = KT * KROW, VBUF = D * VROW;
   __shared__ __attribute__((aligned(16))) char k_sh[2 * KBUF];
@@ -936,17 +958,18 @@ __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tiles_kerne
 
   const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
   const int i32 = lane % 32, half = lane / 32;
-  // The last row tiles see the most tokens and go first.  One sequence: a
-  // cached head's tiles stay on one XCD and its L2.  Several: lengths differ,
-  // and every XCD gets some of each.
-  const int units = a.t.n_seq * a.t.H;
-  const int turn = blockIdx.x / units;
-  const int unit = (blockIdx.x + (a.t.n_seq > 1 ? turn : 0)) % units;
-  const int sp = turn % a.n_splits, rt0 = a.row_tiles - 1 - turn / a.n_splits;
-  const int h = unit % a.t.H, s = unit / a.t.H;
+  // A sequence's last tiles see the most tokens and go first.  Heads go round
+  // the XCDs: with 8 of them each stays on one, and in its L2.
+  const int h = blockIdx.x % a.t.H, turn = blockIdx.x / a.t.H;
+  const int sp = turn % a.n_splits;
+  const TileAt mine = tile_of_slot(a, a.slots - 1 - turn / a.n_splits);
+  if (mine.tile < 0) return;
+  const int s = mine.s;
   const Seq q = seq_of(a.t, s);
   if (q.skip) return;
   const int all_rows = q.rows * a.group;
+  if (mine.tile >= (all_rows + R - 1) / R) return;
+  const int row0 = mine.tile * R;
   const int block_bytes = kv_block_bytes(a.t.P, D);
   const uint8_t* head0 = a.t.base + static_cast<int64_t>(h) * block_bytes;
   const_i32* table = (const_i32*)(a.t.page_table + static_cast<int64_t>(s) * a.t.max_pages);
@@ -965,349 +988,345 @@ __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tiles_kerne
   const uint32_t v_off = 4 * (lane % 4) * (D / 2) + vo * (VC / 2);
   const uint32_t ve_off = (vo * VC / kKvGroup) * a.t.P + 4 * (lane % 4);
 
-  for (int row0 = rt0 * R; row0 < all_rows; row0 += a.row_tiles * R) {
-    const int last_row = (row0 + R < all_rows ? row0 + R : all_rows) - 1;
-    const int vis = q.past + last_row / a.group + 1;
-    const int splits = q.bad ? 1 : kv_splits(vis, a);
-    if (sp >= splits) continue;
-    const int t0 = q.bad ? 0 : sp * a.chunk;
-    const int t1 = q.bad ? 0 : sp == splits - 1 ? vis : t0 + a.chunk;
-    const int w_first = q.past + (row0 + 32 * wave) / a.group;  // the last token all of the wave's rows see
+  const int last_row = (row0 + R < all_rows ? row0 + R : all_rows) - 1;
+  const int vis = q.past + last_row / a.group + 1;
+  const int splits = q.bad ? 1 : kv_splits(vis, a);
+  if (sp >= splits) return;
+  const int t0 = q.bad ? 0 : sp * a.chunk;
+  const int t1 = q.bad ? 0 : sp == splits - 1 ? vis : t0 + a.chunk;
+  const int w_first = q.past + (row0 + 32 * wave) / a.group;  // the last token all of the wave's rows see
 
-    const int row = row0 + 32 * wave + i32;
-    const int r_in = row <= last_row ? row : last_row;
-    const int tok = r_in / a.group, g = r_in - tok * a.group;
-    const int limit = row <= last_row ? q.past + tok : -1;
-    // All of the tile; with HALF in fp16, and false if that does not do.
-    auto attend = [&](auto in_half) __attribute__((always_inline)) {
-    constexpr bool HALF = decltype(in_half)::value;
-    constexpr int NQ = HALF ? 1 : q_pieces<DT>(), NP = HALF ? 1 : w_pieces<DT>();
-    // fp16's second try keeps two pieces of queries and weights, and has no
-    // registers for a second tile's scores
-    constexpr bool PIPED = HALF || DT == KDA_F32;
-    float scale = a.scale;
-    u4 qf[NQ][KS];
-    kernel_args args0 = (kernel_args)__builtin_amdgcn_kernarg_segment_ptr();
-    asm volatile("" : "+s"(args0));
-    const int64_t q_at = (q.n0 + tok) * args0->q_stride + (static_cast<int64_t>(h) * args0->group + g) * D + 8 * half;
+  const int row = row0 + 32 * wave + i32;
+  const int r_in = row <= last_row ? row : last_row;
+  const int tok = r_in / a.group, g = r_in - tok * a.group;
+  const int limit = row <= last_row ? q.past + tok : -1;
+  // All of the tile; with HALF in fp16, and false if that does not do.
+  auto attend = [&](auto in_half) __attribute__((always_inline)) {
+  constexpr bool HALF = decltype(in_half)::value;
+  constexpr int NQ = HALF ? 1 : q_pieces<DT>(), NP = HALF ? 1 : w_pieces<DT>();
+  // fp16's second try keeps two pieces of queries and weights, and has no
+  // registers for a second tile's scores
+  constexpr bool PIPED = HALF || DT == KDA_F32;
+  float scale = a.scale;
+  u4 qf[NQ][KS];
+  kernel_args args0 = (kernel_args)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(args0));
+  const int64_t q_at = (q.n0 + tok) * args0->q_stride + (static_cast<int64_t>(h) * args0->group + g) * D + 8 * half;
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      if constexpr (HALF && DT == KDA_F16) {
-        qf[0][ks] = *reinterpret_cast<const u4*>(static_cast<const uint16_t*>(args0->q) + q_at + 16 * ks);
-        const uint32_t flip = args0->sign < 0.0f ? 0x80008000u : 0u;
+  for (int ks = 0; ks < KS; ++ks) {
+    if constexpr (HALF && DT == KDA_F16) {
+      qf[0][ks] = *reinterpret_cast<const u4*>(static_cast<const uint16_t*>(args0->q) + q_at + 16 * ks);
+      const uint32_t flip = args0->sign < 0.0f ? 0x80008000u : 0u;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) qf[0][ks][k] ^= flip;
-      } else {
-        u4 x[q_pieces<DT>()];
-        load_query<DT>(args0->q, q_at + 16 * ks, args0->sign, x);
+      for (int k = 0; k < 4; ++k) qf[0][ks][k] ^= flip;
+    } else {
+      u4 x[q_pieces<DT>()];
+      load_query<DT>(args0->q, q_at + 16 * ks, args0->sign, x);
 #pragma unroll
-        for (int p = 0; p < NQ; ++p) qf[p][ks] = x[p];
+      for (int p = 0; p < NQ; ++p) qf[p][ks] = x[p];
+    }
+  }
+  if constexpr (HALF && DT == KDA_BF16) {
+    // the row's largest exponent, from both lanes that hold it
+    u16x2 top = {0, 0};
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, qf[0][ks][k] & 0x7FFF7FFFu));
+    int ex = (top[0] > top[1] ? top[0] : top[1]) >> 7;
+    const auto both = __builtin_amdgcn_permlane32_swap(ex, ex, false, false);
+    ex = static_cast<int>(both[0] > both[1] ? both[0] : both[1]);
+    ex = ex == 0 ? 127 : ex < 253 ? ex : 253;
+    const float down = exp_scale(254 - ex);
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t w = qf[0][ks][k];
+        const h2 y = {static_cast<_Float16>(__uint_as_float(w << 16) * down),
+                      static_cast<_Float16>(__uint_as_float(w & 0xFFFF0000u) * down)};
+        qf[0][ks][k] = __builtin_bit_cast(uint32_t, y);
       }
-    }
-    if constexpr (HALF && DT == KDA_BF16) {
-      // the row's largest exponent, from both lanes that hold it
-      u16x2 top = {0, 0};
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, qf[0][ks][k] & 0x7FFF7FFFu));
-      int ex = (top[0] > top[1] ? top[0] : top[1]) >> 7;
-      const auto both = __builtin_amdgcn_permlane32_swap(ex, ex, false, false);
-      ex = static_cast<int>(both[0] > both[1] ? both[0] : both[1]);
-      ex = ex == 0 ? 127 : ex < 253 ? ex : 253;
-      const float down = exp_scale(254 - ex);
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t w = qf[0][ks][k];
-          const h2 y = {static_cast<_Float16>(__uint_as_float(w << 16) * down),
-                        static_cast<_Float16>(__uint_as_float(w & 0xFFFF0000u) * down)};
-          qf[0][ks][k] = __builtin_bit_cast(uint32_t, y);
-        }
-      scale = fmaxf(scale * exp_scale(ex), 0x1p-126f);  // above zero, as a.scale
-    }
-    ExpRange seen;
+    scale = fmaxf(scale * exp_scale(ex), 0x1p-126f);  // above zero, as a.scale
+  }
+  ExpRange seen;
 
-    uint32_t kc[D / 32], ke, vc[4], ve;
-    auto page_of = [&](int tb) __attribute__((always_inline)) {
-      const int t = tb + 16 * wave;
-      const int page = t < t1 ? table[t >> a.t.log_p] : -1;
-      return page < a.t.n_pages ? page : -1;
-    };
-    auto load_keys = [&](int tb) __attribute__((always_inline)) {
-      const int page = page_of(tb);
-      if (page >= 0) {
-        const uint8_t* blk = head0 + page * a.t.page_bytes;
-        const uint32_t r = (tb + 16 * wave) & (a.t.P - 1);
-        const uint8_t* at = blk + r * (D / 2);
-        if constexpr (D == 128) {
-          const u4 x = *reinterpret_cast<const u4*>(at + k_off);
+  uint32_t kc[D / 32], ke, vc[4], ve;
+  auto page_of = [&](int tb) __attribute__((always_inline)) {
+    const int t = tb + 16 * wave;
+    const int page = t < t1 ? table[t >> a.t.log_p] : -1;
+    return page < a.t.n_pages ? page : -1;
+  };
+  auto load_keys = [&](int tb) __attribute__((always_inline)) {
+    const int page = page_of(tb);
+    if (page >= 0) {
+      const uint8_t* blk = head0 + page * a.t.page_bytes;
+      const uint32_t r = (tb + 16 * wave) & (a.t.P - 1);
+      const uint8_t* at = blk + r * (D / 2);
+      if constexpr (D == 128) {
+        const u4 x = *reinterpret_cast<const u4*>(at + k_off);
 #pragma unroll
-          for (int m = 0; m < 4; ++m) kc[m] = x[m];
-        } else {
-          const u2 x = *reinterpret_cast<const u2*>(at + k_off);
-          kc[0] = x[0], kc[1] = x[1];
-        }
-        ke = (blk + kv_key_exps(a.t.P, D) + r * (D / kKvGroup))[k_off / 16];  // 16 bytes of codes an exponent
+        for (int m = 0; m < 4; ++m) kc[m] = x[m];
       } else {
-        ke = kKvPoison;  // scores NaN, seen only where the mask lets them
-#pragma unroll
-        for (int m = 0; m < D / 32; ++m) kc[m] = 0;
+        const u2 x = *reinterpret_cast<const u2*>(at + k_off);
+        kc[0] = x[0], kc[1] = x[1];
       }
-    };
-    auto load_values = [&](int tb) __attribute__((always_inline)) {
-      const int page = page_of(tb);
-      if (page >= 0) {
-        const uint8_t* blk = head0 + page * a.t.page_bytes;
-        const uint32_t r = (tb + 16 * wave) & (a.t.P - 1);
-        const uint8_t* at = blk + kv_value_codes(a.t.P, D) + r * (D / 2);
+      ke = (blk + kv_key_exps(a.t.P, D) + r * (D / kKvGroup))[k_off / 16];  // 16 bytes of codes an exponent
+    } else {
+      ke = kKvPoison;  // scores NaN, seen only where the mask lets them
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if constexpr (D == 128)
-            vc[e] = *reinterpret_cast<const uint32_t*>(at + v_off + e * (D / 2));
-          else
-            vc[e] = *reinterpret_cast<const uint16_t*>(at + v_off + e * (D / 2));
+      for (int m = 0; m < D / 32; ++m) kc[m] = 0;
+    }
+  };
+  auto load_values = [&](int tb) __attribute__((always_inline)) {
+    const int page = page_of(tb);
+    if (page >= 0) {
+      const uint8_t* blk = head0 + page * a.t.page_bytes;
+      const uint32_t r = (tb + 16 * wave) & (a.t.P - 1);
+      const uint8_t* at = blk + kv_value_codes(a.t.P, D) + r * (D / 2);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (D == 128)
+          vc[e] = *reinterpret_cast<const uint32_t*>(at + v_off + e * (D / 2));
+        else
+          vc[e] = *reinterpret_cast<const uint16_t*>(at + v_off + e * (D / 2));
+      }
+      ve = *reinterpret_cast<const uint32_t*>(blk + kv_value_exps(a.t.P, D) + r + ve_off);
+    } else {
+      ve = 0x7F7F7F7Fu;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) vc[e] = 0;
+    }
+  };
+  // dword m of the codes of the key in tile tb
+  auto stage_key = [&](int buf, int m, int tb) __attribute__((always_inline)) {
+    const float ks = exp_scale(ke);
+    u4 x = {dequant2_as<HALF, 0>(kc[m], ks), dequant2_as<HALF, 1>(kc[m], ks), dequant2_as<HALF, 2>(kc[m], ks),
+            dequant2_as<HALF, 3>(kc[m], ks)};
+    if constexpr (HALF) {  // a poisoned key does not fit
+      if (m == 0) seen.take2((tb + kt < t1 ? ke : 127u) * 0x10001u);
+    } else if (m == 0) {
+      x[0] |= ke == kKvPoison ? ~0u : 0u;
+    }
+    *reinterpret_cast<u4*>(k_sh + buf * KBUF + k_to + 16 * m) = x;
+  };
+  // values behind the last token may be anything: zeros
+  auto end_values = [&](int tb) __attribute__((always_inline)) {
+    if (tb + KT > t1) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (tb + 4 * vt + e >= t1) {
+          vc[e] = 0;
+          ve = (ve & ~(0xFFu << (8 * e))) | (127u << (8 * e));
         }
-        ve = *reinterpret_cast<const uint32_t*>(blk + kv_value_exps(a.t.P, D) + r + ve_off);
-      } else {
-        ve = 0x7F7F7F7Fu;
+    }
+  };
+  // channels 2 c2 and 2 c2 + 1 of the 4 values
+  auto stage_value = [&](int buf, auto pick) __attribute__((always_inline)) {
+    constexpr int c2 = decltype(pick)::value;
+    if constexpr (HALF && c2 == 0) {
+      seen.take2(ve & 0x00FF00FFu);
+      seen.take2((ve >> 8) & 0x00FF00FFu);
+    }
+    uint32_t x[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) vc[e] = 0;
-      }
-    };
-    // dword m of the codes of the key in tile tb
-    auto stage_key = [&](int buf, int m, int tb) __attribute__((always_inline)) {
-      const float ks = exp_scale(ke);
-      u4 x = {dequant2_as<HALF, 0>(kc[m], ks), dequant2_as<HALF, 1>(kc[m], ks), dequant2_as<HALF, 2>(kc[m], ks),
-              dequant2_as<HALF, 3>(kc[m], ks)};
-      if constexpr (HALF) {  // a poisoned key does not fit
-        if (m == 0) seen.take2((tb + kt < t1 ? ke : 127u) * 0x10001u);
-      } else if (m == 0) {
-        x[0] |= ke == kKvPoison ? ~0u : 0u;
-      }
-      *reinterpret_cast<u4*>(k_sh + buf * KBUF + k_to + 16 * m) = x;
-    };
-    // values behind the last token may be anything: zeros
-    auto end_values = [&](int tb) __attribute__((always_inline)) {
-      if (tb + KT > t1) {
+    for (int e = 0; e < 4; ++e) x[e] = dequant2_as<HALF, c2>(vc[e], exp_scale((ve >> (8 * e)) & 0xFF));
+    *reinterpret_cast<u2*>(v_sh + buf * VBUF + 32 * c2 * VROW + v_to) = u2{pack_lo(x[0], x[1]), pack_lo(x[2], x[3])};
+    *reinterpret_cast<u2*>(v_sh + buf * VBUF + (32 * c2 + 16) * VROW + v_to) =
+        u2{pack_hi(x[0], x[1]), pack_hi(x[2], x[3])};
+  };
+  f16v zero;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (tb + 4 * vt + e >= t1) {
-            vc[e] = 0;
-            ve = (ve & ~(0xFFu << (8 * e))) | (127u << (8 * e));
-          }
-      }
-    };
-    // channels 2 c2 and 2 c2 + 1 of the 4 values
-    auto stage_value = [&](int buf, auto pick) __attribute__((always_inline)) {
-      constexpr int c2 = decltype(pick)::value;
-      if constexpr (HALF && c2 == 0) {
-        seen.take2(ve & 0x00FF00FFu);
-        seen.take2((ve >> 8) & 0x00FF00FFu);
-      }
-      uint32_t x[4];
+  for (int e = 0; e < 16; ++e) zero[e] = 0.0f;
+  // product i of a tile's scores: channels 16 (i / 2).., tokens 32 (i % 2)..
+  auto key_piece = [&](int buf, int i) __attribute__((always_inline)) {
+    const int ks = i / 2, b = i % 2;
+    return *reinterpret_cast<const u4*>(k_sh + buf * KBUF + k_at + 32 * ks + 32 * b * KROW);
+  };
+  auto score = [&](int i, u4 kf, f16v (&out)[2]) __attribute__((always_inline)) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = dequant2_as<HALF, c2>(vc[e], exp_scale((ve >> (8 * e)) & 0xFF));
-      *reinterpret_cast<u2*>(v_sh + buf * VBUF + 32 * c2 * VROW + v_to) = u2{pack_lo(x[0], x[1]), pack_lo(x[2], x[3])};
-      *reinterpret_cast<u2*>(v_sh + buf * VBUF + (32 * c2 + 16) * VROW + v_to) =
-          u2{pack_hi(x[0], x[1]), pack_hi(x[2], x[3])};
-    };
-    f16v zero;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) zero[e] = 0.0f;
-    // product i of a tile's scores: channels 16 (i / 2).., tokens 32 (i % 2)..
-    auto key_piece = [&](int buf, int i) __attribute__((always_inline)) {
-      const int ks = i / 2, b = i % 2;
-      return *reinterpret_cast<const u4*>(k_sh + buf * KBUF + k_at + 32 * ks + 32 * b * KROW);
-    };
-    auto score = [&](int i, u4 kf, f16v (&out)[2]) __attribute__((always_inline)) {
-#pragma unroll
-      for (int p = 0; p < NQ; ++p) out[i % 2] = mfma32<HALF>(kf, qf[p][i / 2], i / 2 == 0 && p == 0 ? zero : out[i % 2]);
-    };
-    // product i of the outputs: tokens 16 (i / CB).., rows 32 (i % CB)..
-    auto value_piece = [&](int buf, int i) __attribute__((always_inline)) {
-      return *reinterpret_cast<const u4*>(v_sh + buf * VBUF + v_at + 32 * (i / CB) + 32 * (i % CB) * VROW);
-    };
-    f16v sc0[2], sc1[2];  // scores of tiles in turn
+    for (int p = 0; p < NQ; ++p) out[i % 2] = mfma32<HALF>(kf, qf[p][i / 2], i / 2 == 0 && p == 0 ? zero : out[i % 2]);
+  };
+  // product i of the outputs: tokens 16 (i / CB).., rows 32 (i % CB)..
+  auto value_piece = [&](int buf, int i) __attribute__((always_inline)) {
+    return *reinterpret_cast<const u4*>(v_sh + buf * VBUF + v_at + 32 * (i / CB) + 32 * (i % CB) * VROW);
+  };
+  f16v sc0[2], sc1[2];  // scores of tiles in turn
 
-    f16v o[CB];
+  f16v o[CB];
 #pragma unroll
-    for (int c = 0; c < CB; ++c) o[c] = zero;
-    float mx = -INFINITY, sum = 0.0f;
-    load_keys(t0);
-    load_values(t0);
+  for (int c = 0; c < CB; ++c) o[c] = zero;
+  float mx = -INFINITY, sum = 0.0f;
+  load_keys(t0);
+  load_values(t0);
 #pragma unroll
-    for (int m = 0; m < D / 32; ++m) stage_key(0, m, t0);
-    load_keys(t0 + KT);
-    end_values(t0);
-    stage_value(0, std::integral_constant<int, 0>{});
-    stage_value(0, std::integral_constant<int, 1>{});
-    if constexpr (D == 128) {
-      stage_value(0, std::integral_constant<int, 2>{});
-      stage_value(0, std::integral_constant<int, 3>{});
-    }
-    load_values(t0 + KT);
+  for (int m = 0; m < D / 32; ++m) stage_key(0, m, t0);
+  load_keys(t0 + KT);
+  end_values(t0);
+  stage_value(0, std::integral_constant<int, 0>{});
+  stage_value(0, std::integral_constant<int, 1>{});
+  if constexpr (D == 128) {
+    stage_value(0, std::integral_constant<int, 2>{});
+    stage_value(0, std::integral_constant<int, 3>{});
+  }
+  load_values(t0 + KT);
 #pragma unroll
-    for (int m = 0; m < D / 32; ++m) stage_key(1, m, t0 + KT);
-    load_keys(t0 + 2 * KT);
-    __syncthreads();
-    if constexpr (PIPED) {
+  for (int m = 0; m < D / 32; ++m) stage_key(1, m, t0 + KT);
+  load_keys(t0 + 2 * KT);
+  __syncthreads();
+  if constexpr (PIPED) {
 #pragma unroll
-      for (int i = 0; i < 2 * KS; ++i) score(i, key_piece(0, i), sc0);
-    }
-    auto top_score = [&](const f16v (&x)[2]) __attribute__((always_inline)) {
-      float y = -INFINITY;
+    for (int i = 0; i < 2 * KS; ++i) score(i, key_piece(0, i), sc0);
+  }
+  auto top_score = [&](const f16v (&x)[2]) __attribute__((always_inline)) {
+    float y = -INFINITY;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) y = max_nan(y, max_nan(x[0][e], x[1][e]));
-      return y;
-    };
-    float best = PIPED ? top_score(sc0) : 0.0f;
-    auto step = [&](int tb, auto which, f16v (&sc)[2], f16v (&next)[2]) __attribute__((always_inline)) {
-      constexpr int buf = decltype(which)::value;
-      if constexpr (!PIPED) {
-#pragma unroll
-        for (int i = 0; i < 2 * KS; ++i) {
-          score(i, key_piece(buf, i), sc);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-        best = top_score(sc);
-        __syncthreads();  // this buffer's next keys are written below
-      }
-      if (tb + KT - 1 > w_first) {
-        const int left = limit - tb - 4 * half;  // the last of the lane's tokens its row sees
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) sc[b][e] = 32 * b + 8 * (e / 4) + e % 4 > left ? -INFINITY : sc[b][e];
-        best = top_score(sc);
-      }
-      // the running maximum moves only when a score passes it by 8
-      if (__ballot(best * scale > mx + 8.0f) != 0) {
-        const float to = fmaxf(max_xor32(best * scale), mx);
-        const float keep = mx == to ? 1.0f : exp2_hw(mx - to);
-        mx = to;
-        sum *= keep;
-#pragma unroll
-        for (int c = 0; c < CB; ++c) o[c] *= keep;
-      }
-      end_values(tb + KT);
-      // weights in fp16 are taken 2^7 times larger, at most 2^15
-      const float base = (mx == -INFINITY ? 0.0f : -mx) + (HALF ? 7.0f : 0.0f);
-      // -- this tile's weights, the next one's scores: after each product the
-      // vector work that fits beside it, operands read AHEAD products early
-      constexpr int AHEAD = 2;
-      u4 pf[4][NP], ring[AHEAD + 1];
-      if constexpr (PIPED) {
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i) ring[i] = key_piece(buf ^ 1, i);
-      }
+    for (int e = 0; e < 16; ++e) y = max_nan(y, max_nan(x[0][e], x[1][e]));
+    return y;
+  };
+  float best = PIPED ? top_score(sc0) : 0.0f;
+  auto step = [&](int tb, auto which, f16v (&sc)[2], f16v (&next)[2]) __attribute__((always_inline)) {
+    constexpr int buf = decltype(which)::value;
+    if constexpr (!PIPED) {
 #pragma unroll
       for (int i = 0; i < 2 * KS; ++i) {
-        if constexpr (PIPED) {
-          if (i + AHEAD < 2 * KS) ring[(i + AHEAD) % (AHEAD + 1)] = key_piece(buf ^ 1, i + AHEAD);
-          score(i, ring[i % (AHEAD + 1)], next);
-        }
-        constexpr int EACH = 16 / KS;  // weights beside a product
-#pragma unroll
-        for (int k = EACH * i; k < EACH * (i + 1); k += 2) {
-          const int b = k / 16, e = k % 16;
-          const float w0 = exp2_hw(fmaf(sc[b][e], scale, base)), w1 = exp2_hw(fmaf(sc[b][e + 1], scale, base));
-          sum += w0 + w1;
-          uint32_t x[NP];
-          if constexpr (HALF) {
-            x[0] = __builtin_bit_cast(uint32_t, h2{static_cast<_Float16>(w0), static_cast<_Float16>(w1)});
-          } else {
-            split_pair<NP>(w0, w1, x);
-          }
-#pragma unroll
-          for (int p = 0; p < NP; ++p) pf[2 * b + e / 8][p][(e % 8) / 2] = x[p];
-        }
+        score(i, key_piece(buf, i), sc);
         __builtin_amdgcn_sched_barrier(0);
       }
-      // -- this tile's values; later tiles' codes; the next scores' maximum
-      best = -INFINITY;
+      best = top_score(sc);
+      __syncthreads();  // this buffer's next keys are written below
+    }
+    if (tb + KT - 1 > w_first) {
+      const int left = limit - tb - 4 * half;  // the last of the lane's tokens its row sees
 #pragma unroll
-      for (int i = 0; i < AHEAD; ++i) ring[i] = value_piece(buf, i);
-      auto output = [&](auto at) __attribute__((always_inline)) {
-        constexpr int i = decltype(at)::value, G = 4 * CB, E = 32 / G;
-        if (i + AHEAD < G) ring[(i + AHEAD) % (AHEAD + 1)] = value_piece(buf, i + AHEAD);
+      for (int b = 0; b < 2; ++b)
 #pragma unroll
-        for (int p = 0; p < NP; ++p) o[i % CB] = mfma32<HALF>(ring[i % (AHEAD + 1)], pf[i / CB][p], o[i % CB]);
-        if constexpr (i % 4 == 0) stage_key(buf, i / 4, tb + 2 * KT);
-        if constexpr (i % 4 == 2) stage_value(buf ^ 1, std::integral_constant<int, i / 4>{});
-        if constexpr (PIPED) {
+        for (int e = 0; e < 16; ++e) sc[b][e] = 32 * b + 8 * (e / 4) + e % 4 > left ? -INFINITY : sc[b][e];
+      best = top_score(sc);
+    }
+    // the running maximum moves only when a score passes it by 8
+    if (__ballot(best * scale > mx + 8.0f) != 0) {
+      const float to = fmaxf(max_xor32(best * scale), mx);
+      const float keep = mx == to ? 1.0f : exp2_hw(mx - to);
+      mx = to;
+      sum *= keep;
 #pragma unroll
-          for (int k = E * i; k < E * (i + 1); ++k) best = max_nan(best, next[k % 2][k / 2]);
+      for (int c = 0; c < CB; ++c) o[c] *= keep;
+    }
+    end_values(tb + KT);
+    // weights in fp16 are taken 2^7 times larger, at most 2^15
+    const float base = (mx == -INFINITY ? 0.0f : -mx) + (HALF ? 7.0f : 0.0f);
+    // -- this tile's weights, the next one's scores: after each product the
+    // vector work that fits beside it, operands read AHEAD products early
+    constexpr int AHEAD = 2;
+    u4 pf[4][NP], ring[AHEAD + 1];
+    if constexpr (PIPED) {
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) ring[i] = key_piece(buf ^ 1, i);
+    }
+#pragma unroll
+    for (int i = 0; i < 2 * KS; ++i) {
+      if constexpr (PIPED) {
+        if (i + AHEAD < 2 * KS) ring[(i + AHEAD) % (AHEAD + 1)] = key_piece(buf ^ 1, i + AHEAD);
+        score(i, ring[i % (AHEAD + 1)], next);
+      }
+      constexpr int EACH = 16 / KS;  // weights beside a product
+#pragma unroll
+      for (int k = EACH * i; k < EACH * (i + 1); k += 2) {
+        const int b = k / 16, e = k % 16;
+        const float w0 = exp2_hw(fmaf(sc[b][e], scale, base)), w1 = exp2_hw(fmaf(sc[b][e + 1], scale, base));
+        sum += w0 + w1;
+        uint32_t x[NP];
+        if constexpr (HALF) {
+          x[0] = __builtin_bit_cast(uint32_t, h2{static_cast<_Float16>(w0), static_cast<_Float16>(w1)});
+        } else {
+          split_pair<NP>(w0, w1, x);
         }
-        __builtin_amdgcn_sched_barrier(0);
-      };
-      each_of(output, std::make_integer_sequence<int, 4 * CB>{});
-      load_keys(tb + 3 * KT);
-      load_values(tb + 2 * KT);
-      __syncthreads();
-    };
-    for (int tb = t0; tb < t1; tb += 2 * KT) {
-      step(tb, std::integral_constant<int, 0>{}, sc0, sc1);
-      if (tb + KT >= t1) break;
-      if constexpr (PIPED)
-        step(tb + KT, std::integral_constant<int, 1>{}, sc1, sc0);
-      else
-        step(tb + KT, std::integral_constant<int, 1>{}, sc0, sc1);
-    }
-    if constexpr (HALF) {
-      if (!__syncthreads_and(seen.in_half())) return false;
-    }
-
-    // The lane's row and the arguments once more, from an opaque thread id and
-    // address: kept from above, they would be spilled over the steps.
-    int again = tid;
-    kernel_args args = (kernel_args)__builtin_amdgcn_kernarg_segment_ptr();
-    asm volatile("" : "+v"(again), "+s"(args));
-    // -- rows out: element e of block c is row 8 (e / 4) + 4 half + e % 4 of
-    // 32 c.., channel 2 c + e / 8 of the VC at VC (row % 16)
-    sum = sum_xor32(sum);
-    const int out_half = again % 64 / 32, out_row = row0 + 32 * wave + again % 32;
-    if (out_row <= last_row) {
-      const int ot = out_row / args->group, og = out_row - ot * args->group;
-      const int64_t at = (q.n0 + ot) * args->q_heads + static_cast<int64_t>(h) * args->group + og;
-      const int64_t slot = static_cast<int64_t>(sp) * args->t.n_tokens * args->q_heads + at;
-      const float inv = splits > 1 ? 1.0f : q.bad ? __builtin_nanf("") : sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int64_t c0 = VC * (8 * (e / 4) + 4 * out_half + e % 4);
-        float x[VC];
+        for (int p = 0; p < NP; ++p) pf[2 * b + e / 8][p][(e % 8) / 2] = x[p];
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    // -- this tile's values; later tiles' codes; the next scores' maximum
+    best = -INFINITY;
 #pragma unroll
-        for (int n = 0; n < VC; ++n) x[n] = o[n / 2][8 * (n % 2) + e] * inv;
-        if (splits == 1)
-          store_channels<DT>(args->out, at * D + c0, x);
-        else
-          store_channels<KDA_F32>(args->part, slot * D + c0, x);
+    for (int i = 0; i < AHEAD; ++i) ring[i] = value_piece(buf, i);
+    auto output = [&](auto at) __attribute__((always_inline)) {
+      constexpr int i = decltype(at)::value, G = 4 * CB, E = 32 / G;
+      if (i + AHEAD < G) ring[(i + AHEAD) % (AHEAD + 1)] = value_piece(buf, i + AHEAD);
+#pragma unroll
+      for (int p = 0; p < NP; ++p) o[i % CB] = mfma32<HALF>(ring[i % (AHEAD + 1)], pf[i / CB][p], o[i % CB]);
+      if constexpr (i % 4 == 0) stage_key(buf, i / 4, tb + 2 * KT);
+      if constexpr (i % 4 == 2) stage_value(buf ^ 1, std::integral_constant<int, i / 4>{});
+      if constexpr (PIPED) {
+#pragma unroll
+        for (int k = E * i; k < E * (i + 1); ++k) best = max_nan(best, next[k % 2][k / 2]);
       }
-      if (splits > 1 && out_half == 0) {
-        args->part_ml[2 * slot] = mx - (HALF ? 7.0f : 0.0f);
-        args->part_ml[2 * slot + 1] = sum;
-      }
-    }
-    return true;
+      __builtin_amdgcn_sched_barrier(0);
     };
-    if constexpr (DT == KDA_F32) {
-      attend(std::false_type{});
-    } else {
-      if (!attend(std::true_type{})) attend(std::false_type{});
-    }
+    each_of(output, std::make_integer_sequence<int, 4 * CB>{});
+    load_keys(tb + 3 * KT);
+    load_values(tb + 2 * KT);
     __syncthreads();
+  };
+  for (int tb = t0; tb < t1; tb += 2 * KT) {
+    step(tb, std::integral_constant<int, 0>{}, sc0, sc1);
+    if (tb + KT >= t1) break;
+    if constexpr (PIPED)
+      step(tb + KT, std::integral_constant<int, 1>{}, sc1, sc0);
+    else
+      step(tb + KT, std::integral_constant<int, 1>{}, sc0, sc1);
+  }
+  if constexpr (HALF) {
+    if (!__syncthreads_and(seen.in_half())) return false;
+  }
+
+  // The lane's row and the arguments once more, from an opaque thread id and
+  // address: kept from above, they would be spilled over the steps.
+  int again = tid;
+  kernel_args args = (kernel_args)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+v"(again), "+s"(args));
+  // -- rows out: element e of block c is row 8 (e / 4) + 4 half + e % 4 of
+  // 32 c.., channel 2 c + e / 8 of the VC at VC (row % 16)
+  sum = sum_xor32(sum);
+  const int out_half = again % 64 / 32, out_row = row0 + 32 * wave + again % 32;
+  if (out_row <= last_row) {
+    const int ot = out_row / args->group, og = out_row - ot * args->group;
+    const int64_t at = (q.n0 + ot) * args->q_heads + static_cast<int64_t>(h) * args->group + og;
+    const int64_t slot = static_cast<int64_t>(sp) * args->t.n_tokens * args->q_heads + at;
+    const float inv = splits > 1 ? 1.0f : q.bad ? __builtin_nanf("") : sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int64_t c0 = VC * (8 * (e / 4) + 4 * out_half + e % 4);
+      float x[VC];
+#pragma unroll
+      for (int n = 0; n < VC; ++n) x[n] = o[n / 2][8 * (n % 2) + e] * inv;
+      if (splits == 1)
+        store_channels<DT>(args->out, at * D + c0, x);
+      else
+        store_channels<KDA_F32>(args->part, slot * D + c0, x);
+    }
+    if (splits > 1 && out_half == 0) {
+      args->part_ml[2 * slot] = mx - (HALF ? 7.0f : 0.0f);
+      args->part_ml[2 * slot + 1] = sum;
+    }
+  }
+  return true;
+  };
+  if constexpr (DT == KDA_F32) {
+    attend(std::false_type{});
+  } else {
+    if (!attend(std::true_type{})) attend(std::false_type{});
   }
 }
-
 
 // Joins the splits of rows, D / 8 lanes across a row's channels.  Few splits:
 // the lanes take theirs one after the other, four loads in flight, and a block
 // takes 256 / (D / 8) rows.  MANY: a row has a whole block, splits lie across
 // its lane groups, each with a maximum and sum of its own, so that no load
 // waits for another split's.
-template <int DT, int D, bool MANY>
+template <int DT, int D, bool MANY, bool TILES>
 __global__ __launch_bounds__(256) void kda_kv_join_kernel(KvAttendArgs a, int tile_rows) {
   constexpr int PER = D / 8, W = MANY ? 4 : 1;      // lanes of a row's channels, waves of a row
   constexpr int ROWS = MANY ? 1 : 256 / PER;
@@ -1318,14 +1337,22 @@ __global__ __launch_bounds__(256) void kda_kv_join_kernel(KvAttendArgs a, int ti
   const int slices = (tile_rows + ROWS - 1) / ROWS;
   const int id = blockIdx.x;
   const int r = (id % slices) * ROWS + (MANY ? 0 : threadIdx.x / PER);
-  const int rt0 = (id / slices) % a.row_tiles;
-  const int h = (id / slices / a.row_tiles) % a.t.H;
-  const int s = id / slices / a.row_tiles / a.t.H;
+  // TILES: the tiles kernel's slots; else a.row_tiles tiles for each sequence
+  const int tiles = TILES ? a.slots : a.row_tiles;
+  const int h = id / slices / tiles % a.t.H;
+  int rt0 = id / slices % tiles, s = id / slices / tiles / a.t.H;
+  if constexpr (TILES) {
+    const TileAt mine = tile_of_slot(a, rt0);
+    if (mine.tile < 0) return;
+    rt0 = mine.tile, s = mine.s;
+  }
   const Seq q = seq_of(a.t, s);
   if (q.skip || q.bad || r >= tile_rows) return;
   const int all_rows = q.rows * a.group;
   const int64_t stride = a.t.n_tokens * a.q_heads;
-  for (int row = rt0 * tile_rows + r; row < all_rows; row += a.row_tiles * tile_rows) {
+  for (int64_t row0 = static_cast<int64_t>(rt0) * tile_rows + r; row0 < all_rows;
+       row0 += TILES ? all_rows : a.row_tiles * tile_rows) {
+    const int row = static_cast<int>(row0);
     const int end = row - r + tile_rows;  // of the tile
     const int splits = kv_splits(q.past + ((end < all_rows ? end : all_rows) - 1) / a.group + 1, a);
     if (splits <= 1) continue;  // written already
@@ -1480,7 +1507,7 @@ extern "C" int kda_kv_append(const kda_kv_pool* kv, const int32_t* page_table, i
   const int64_t tiles = (n_tokens + 256 / (kv->D / 8) - 1) / (256 / (kv->D / 8));
   a.units_per_block = heads_a_block(tiles, a.units);
   a.unit_blocks = (a.units + a.units_per_block - 1) / a.units_per_block;
-  if (tiles * a.unit_blocks > INT32_MAX) return KDA_ERR_ARG;
+  if (tiles * a.unit_blocks > kKvMaxBlocks) return KDA_ERR_ARG;
   hipStream_t st = static_cast<hipStream_t>(stream);
   return status(by_type(dtype, kv->D, [&](auto t, auto d) {
     constexpr int DT = decltype(t)::value, D = decltype(d)::value;
@@ -1523,7 +1550,7 @@ extern "C" int kda_kv_read(const kda_kv_pool* kv, const int32_t* page_table, int
   const int64_t tiles = (n_tokens + per - 1) / per;
   a.heads_per_block = heads_a_block(tiles, kv->H);
   a.head_blocks = (kv->H + a.heads_per_block - 1) / a.heads_per_block;
-  if (tiles * a.head_blocks > INT32_MAX) return KDA_ERR_ARG;
+  if (tiles * a.head_blocks > kKvMaxBlocks) return KDA_ERR_ARG;
   hipStream_t st = static_cast<hipStream_t>(stream);
   return status(by_type(dtype, kv->D, [&](auto t, auto d) {
     hipLaunchKernelGGL((kda_kv_read_kernel<decltype(t)::value, decltype(d)::value>),
@@ -1568,19 +1595,20 @@ extern "C" int kda_kv_attend(const kda_kv_pool* kv, const int32_t* page_table, i
   a.chunk = p.chunk;
   a.n_splits = p.n_splits;
   a.row_tiles = p.row_tiles;
+  a.slots = p.slots;
   // a zero scale stays above zero, so that a masked score (-infinity) times it
   // is what it was; 2^-126 times any score leaves its weight 1
   a.scale = std::fmax(std::fabs(scale) * 1.44269504088896340736f, 0x1p-126f);
   a.sign = scale < 0.0f ? -1.0f : 1.0f;
   a.part = static_cast<float*>(workspace);
   a.part_ml = a.part == nullptr ? nullptr : a.part + static_cast<int64_t>(p.n_splits) * n_tokens * q_heads * kv->D;
-  const int64_t blocks = static_cast<int64_t>(n_seq) * kv->H * p.row_tiles * p.n_splits;
-  if (blocks > INT32_MAX) return KDA_ERR_ARG;
+  const int64_t tiles = (p.slots > 0 ? p.slots : static_cast<int64_t>(n_seq) * p.row_tiles) * kv->H;
+  if (tiles * p.n_splits > kKvMaxBlocks) return KDA_ERR_ARG;  // (many splits: few tiles, so the join's blocks fit too)
   hipStream_t st = static_cast<hipStream_t>(stream);
   return status(by_type(dtype, kv->D, [&](auto t, auto d) {
     constexpr int DT = decltype(t)::value, D = decltype(d)::value;
-    const dim3 grid(static_cast<uint32_t>(blocks));
-    if (p.tile_rows == 128)
+    const dim3 grid(static_cast<uint32_t>(tiles * p.n_splits));
+    if (p.tile_rows == kTileRows)
       hipLaunchKernelGGL((kda_kv_tiles_kernel<DT, D>), grid, dim3(256), 0, st, a);
     else if (p.waves == 8)
       hipLaunchKernelGGL((kda_kv_rows_kernel<DT, D, 1, 8>), grid, dim3(512), 0, st, a);
@@ -1591,13 +1619,17 @@ extern "C" int kda_kv_attend(const kda_kv_pool* kv, const int32_t* page_table, i
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && p.n_splits > 1) {
       // up to 8 splits a row in two rounds of loads, more side by side
-      const uint32_t tiles = static_cast<uint32_t>(n_seq) * kv->H * p.row_tiles;
       constexpr int rows = 256 / (D / 8);
-      if (p.n_splits <= 8)
-        hipLaunchKernelGGL((kda_kv_join_kernel<DT, D, false>), dim3(tiles * ((p.tile_rows + rows - 1) / rows)), dim3(256),
-                           0, st, a, p.tile_rows);
+      const bool many = p.n_splits > 8, in_slots = p.tile_rows == kTileRows;
+      const dim3 joins(static_cast<uint32_t>(tiles * (many ? p.tile_rows : (p.tile_rows + rows - 1) / rows)));
+      if (many && in_slots)
+        hipLaunchKernelGGL((kda_kv_join_kernel<DT, D, true, true>), joins, dim3(256), 0, st, a, p.tile_rows);
+      else if (many)
+        hipLaunchKernelGGL((kda_kv_join_kernel<DT, D, true, false>), joins, dim3(256), 0, st, a, p.tile_rows);
+      else if (in_slots)
+        hipLaunchKernelGGL((kda_kv_join_kernel<DT, D, false, true>), joins, dim3(256), 0, st, a, p.tile_rows);
       else
-        hipLaunchKernelGGL((kda_kv_join_kernel<DT, D, true>), dim3(tiles * p.tile_rows), dim3(256), 0, st, a, p.tile_rows);
+        hipLaunchKernelGGL((kda_kv_join_kernel<DT, D, false, false>), joins, dim3(256), 0, st, a, p.tile_rows);
       e = hipGetLastError();
     }
     return e;

@@ -24,7 +24,6 @@ int kv_check(const kda_kv_pool* kv, int32_t max_pages, int32_t n_seq, int64_t n_
 KvPlan kv_plan(int32_t H, int32_t D, int32_t n_seq, int64_t n_tokens, int32_t max_rows,
                int64_t max_kv_len, int32_t q_heads, kda_dtype dtype) {
   (void)D;
-  (void)dtype;
   KvPlan p;
   const int64_t rows = static_cast<int64_t>(max_rows < n_tokens ? max_rows : n_tokens) * (q_heads / H);
   // 128-row tiles share a tile's turned codes through LDS; below that every
@@ -34,9 +33,16 @@ KvPlan kv_plan(int32_t H, int32_t D, int32_t n_seq, int64_t n_tokens, int32_t ma
   // are faster as more workgroups of 16 (64 rows: 38 us, 46 in 32s, 40 in
   // 128s; 96 rows: 95, and 76 in 128s).
   p.tile_rows = rows > 64 ? 128 : rows > 16 && rows <= 32 && dtype != KDA_F32 ? 32 : 16;
-  p.row_tiles = static_cast<int32_t>((rows + p.tile_rows - 1) / p.tile_rows);
-  if (p.row_tiles < 1) p.row_tiles = 1;
-  const int64_t units = static_cast<int64_t>(n_seq < 1 ? 1 : n_seq) * H * p.row_tiles;
+  const int64_t row_tiles = rows < 1 ? 1 : (rows + p.tile_rows - 1) / p.tile_rows;
+  p.row_tiles = static_cast<int32_t>(row_tiles);
+  int64_t units = (n_seq < 1 ? 1 : n_seq) * row_tiles * H;
+  p.slots = 0;
+  if (p.tile_rows == 128) {
+    // as many slots as any spread of the rows over the sequences may need
+    const int64_t slots = n_tokens * (q_heads / H) / 128 + n_seq;
+    p.slots = slots > INT32_MAX ? INT32_MAX : static_cast<int32_t>(slots);
+    if (n_seq > 1) units = static_cast<int64_t>(p.slots) * H;
+  }
   const auto per = [](int64_t x, int64_t n) { return (x + n - 1) / n; };
   // n splits of a cache, none shorter than `least`
   const auto chunk_of = [&](int64_t blocks, int64_t least) {
@@ -64,10 +70,10 @@ KvPlan kv_plan(int32_t H, int32_t D, int32_t n_seq, int64_t n_tokens, int32_t ma
     if (per(max_kv_len, chunk) * units < 256) chunk = chunk_of(256, 128);
   } else {
     // Many rows, two workgroups a compute unit: one round of them for one
-    // sequence (512 rows on 15000 tokens: 165 us; 190, 220 for 1024, 1536), three
-    // for several, whose rows and lengths differ (4 chunks of up to 700 rows on up
-    // to 16000 tokens: 213 us; 231, 296 for 1024, 512).
-    chunk = n_seq > 1 ? chunk_of(per(1536, units) * units, 1024) : chunk_of(512, 1024);
+    // sequence (512 rows on 15000 tokens: 165 us; 190, 220 for 1024, 1536), at least
+    // one for several, whose rows and lengths differ (4 chunks of up to 700 rows
+    // on up to 16000 tokens, 226 slots: 3 splits 174 us, 2 or 4 some 210).
+    chunk = n_seq > 1 ? chunk_of(per(512, units) * units, 1024) : chunk_of(512, 1024);
   }
   chunk = per(chunk, 128) * 128;
   if (chunk < 128) chunk = 128;

@@ -317,12 +317,27 @@ int main() {
     const int64_t kv = 1 + rand() % 200000;
     const kda_dtype dt = static_cast<kda_dtype>(rand() % 3);
     const KvPlan p = kv_plan(H, rand() % 2 ? 64 : 128, n_seq, static_cast<int64_t>(n_seq) * rows, rows, kv, H * G, dt);
-    if (static_cast<int64_t>(p.row_tiles) * p.tile_rows < static_cast<int64_t>(rows) * G ||
+    const int64_t tiles = p.tile_rows == 128 ? p.slots : p.row_tiles;
+    if (tiles * p.tile_rows < static_cast<int64_t>(rows) * G ||
         static_cast<int64_t>(p.n_splits) * p.chunk < kv || p.chunk % 32 != 0 || p.n_splits < 1 ||
         (p.n_splits > 1 && static_cast<int64_t>(p.n_splits - 1) * p.chunk >= kv)) {
       std::printf("plan %d: %d x %d rows, %d x %d tokens\n", it, p.row_tiles, p.tile_rows, p.n_splits, p.chunk);
       return 1;
     }
+  }
+  // slots hold every sequence's tiles, one after the other
+  for (int it = 0; it < 20000; ++it) {
+    const int G = 1 + rand() % 9, n = 1 + rand() % 6, spare = rand() % 3 * 50;
+    int64_t cu = rand() % 30, next = 0;
+    int64_t ends[6];
+    for (int s = 0; s < n; ++s) {
+      const int64_t first = cu * G / 128 + s, rows = rand() % 4 ? rand() % 700 : rand() % 3;
+      if (first < next) { std::printf("slots of %d overlap\n", s); return 1; }
+      next = first + (rows * G + 127) / 128;
+      ends[s] = cu += rows;
+    }
+    const KvPlan p = kv_plan(1, 64, n, ends[n - 1] + spare, 1000, 5000, G, KDA_F32);
+    if (p.tile_rows == 128 && next > p.slots) { std::printf("%d slots, not %d\n", p.slots, (int)next); return 1; }
   }
   std::printf("kv host checks ok\n");
   return 0;

@@ -367,6 +367,20 @@ def test_the_hints_lay_out_the_launch_and_nothing_else(dtype):
     c.check(c.attend(max_rows=None))
 
 
+def test_a_prompt_among_many_steps():
+    # tiles of a launch with a long prompt between single tokens, sequences
+    # without rows, and spare rows at both ends
+    rows = [1, 0, 1, 1, 300, 1, 0, 0, 5, 1, 129, 1] + [1] * 70 + [0, 33]
+    past = [(37 * i) % 90 for i in range(len(rows))]
+    c = Case(rows, past, "f16", (6, 2), 64, 32, seed=30, lead=3, trail=40).fill()
+    out = torch.full((c.T, 6, 64), -7.0, dtype=torch.float16, device="cuda")
+    c.attend(out)
+    c.check(out)
+    assert bool((out[:3] == -7).all()) and bool((out[c.cu[-1]:] == -7).all())
+    c.attend(out, max_rows=0)       # the same rows in small tiles
+    c.check(out)
+
+
 @pytest.mark.parametrize("scale", [1.0, 0.0, -0.3])
 def test_any_scale(scale):
     c = Case([2, 20], [50, 3], "f16", (4, 1), 64, 16, seed=15).fill()
