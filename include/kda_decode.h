@@ -522,12 +522,15 @@ size_t kda_kv_pool_bytes(int32_t n_pages, int32_t page_tokens, int32_t H, int32_
  * The tables every kda_kv_* launch takes (device memory):
  *  page_table  int32 [n_seq, max_pages]: sequence s keeps position p on page
  *              page_table[s][p / page_tokens], at token p % page_tokens.
- *              Entries behind a sequence's last token are not read.
- *              max_pages * page_tokens < 2^31.
+ *              Entries behind a sequence's last token may hold anything (they
+ *              may be read, never used).  max_pages >= 1, and max_pages *
+ *              page_tokens <= 2^31 - 4096.
  *  cu_seqlens  int32 [n_seq + 1], non-decreasing: sequence s owns tokens
  *              cu_seqlens[s] .. cu_seqlens[s + 1] - 1 of the launch (none, one,
  *              chained rows or a prompt).  A sequence whose entries are
- *              out of range is skipped.  Tokens before the first or behind
+ *              out of range is skipped; entries that descend may take others
+ *              with them (memory outside the tables and tensors is never
+ *              touched).  Tokens before the first or behind
  *              the last sequence are left as they were.
  *  cache_lens  int32 [n_seq]: tokens sequence s had before this launch: its
  *              i-th token of the launch is at position cache_lens[s] + i.  The
@@ -540,7 +543,8 @@ size_t kda_kv_pool_bytes(int32_t n_pages, int32_t page_tokens, int32_t H, int32_
  * as they lie.  All device pointers 16-byte aligned (the tables: 4-byte).
  * Nothing is allocated or synchronised; launches are captured into graphs as
  * they are.  Calls on different streams may overlap as long as they do not
- * write the same pages, outputs or workspaces.
+ * write the same pages, outputs or workspaces, or read pages being written.  A
+ * launch of more than 4 million workgroups is KDA_ERR_ARG.
  * Checks run in the order: pool NULL, SHAPE (pool), ARG (counts, max_pages),
  * DTYPE_REFUSED, SHAPE (heads, rot_dim) and ARG (the other numbers), then, for
  * n_seq and n_tokens > 0 (either 0 is a valid no-op), NULL, ARG (strides),
@@ -598,18 +602,25 @@ int kda_kv_read(const kda_kv_pool* kv, const int32_t* page_table, int32_t max_pa
  *   out = sum_t softmax_t(scale * q . k_t) v_t
  *  q               [n_tokens, q_heads, D]; out: the same without gaps.
  *  max_rows        the longest sequence's rows in this launch, max_kv_len its
- *                  tokens including them (0: all that max_pages covers).  Both
- *                  only lay out the launch: longer sequences are taken as
- *                  well, more slowly.
- *  q_heads         a multiple of H; n_tokens * q_heads / H < 2^29.
+ *                  tokens including them (0: all that max_pages covers).  They
+ *                  choose the kernel and lay out its launch; longer sequences
+ *                  are taken as well, more slowly.
+ *  q_heads         a multiple of H, at most 65535; n_tokens * q_heads / H < 2^29.
+ *                  (0..65535 for kda_kv_append.)
  *  scale           finite.
  *  workspace       kda_kv_attend_workspace() bytes for the same arguments (may
  *                  be NULL for 0), 16-byte aligned, free for use again once
  *                  the launch has run.  Calls that may overlap need their own.
- * Products are exact: q enters the matrix cores as 3 (fp32), 2 (fp16) or 1
- * bf16 numbers that add up to it; scores, weights, their sums and the output's
- * sums are fp32.  The order of the sums depends on the launch's sizes, not on
- * timing: equal calls give equal bits.
+ * Cached values enter the matrix cores as they are.  So does q, as 3 (fp32), 2
+ * (fp16) or 1 bf16 numbers that add up to it; scores, weights, their sums and the
+ * output's sums are fp32, and weights lose less than 2^-15 of themselves where
+ * outputs have 16 bits.  Prompts of 16-bit types (more than 64 rows of a
+ * sequence and cached head) are multiplied in fp16 where the exponents they meet
+ * allow it (104..140, and 2, which zeros have): weights are then rounded to 11
+ * bits, and a bf16 query, divided by its row's power of two, is off by at most
+ * 2^-25 of the row's largest channel.  Other exponents are multiplied as above.
+ * The order of the sums depends on the launch's sizes, not on timing: equal calls
+ * give equal bits.
  * A row that sees a poisoned token or a page that does not exist is NaN in
  * that head; the rows of a sequence with a negative length or one that
  * max_pages cannot hold are NaN.  Errors: KDA_ERR_NULL and KDA_ERR_ARG also for

@@ -16,6 +16,8 @@ constexpr int kKvMinExp = 2;      // exponent bytes stored: every value a normal
 constexpr int kKvMaxExp = 252;    //   and 6 * 2^(252 - 127) finite
 constexpr int kKvPoison = 255;    // key exponent of a token whose key or value was not finite
 constexpr int kKvMaxHeads = 4096;
+// Positions stay so far below 2^31 that a kernel's look ahead in int32 cannot pass it.
+constexpr int64_t kKvMaxPositions = (1ll << 31) - 4096;
 constexpr int64_t kKvMaxBlocks = INT32_MAX / 512;  // a launch's threads stay below 2^31
 
 // Bytes of one (page, head) block of P tokens of D channels: key codes

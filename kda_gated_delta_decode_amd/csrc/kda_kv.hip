@@ -10,6 +10,7 @@
 // fp32, fp16 or bf16 number.
 #include <hip/hip_runtime.h>
 
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -937,7 +938,7 @@ struct ExpRange {
 // tiles are turned while the values are multiplied.  Keys are therefore
 // staged one tile further ahead than values; one barrier a tile.
 //
-// 16-bit types first take everything in fp16: E2M1 times 2^(e - 127) is exact
+// 16-bit types take everything in fp16 first: E2M1 times 2^(e - 127) is exact
 // there for e in 104..140, an fp16 query is itself, a bf16 query divided by its
 // row's power of two loses at most 2^-25 of the row's largest channel, and
 // weights, at most 2^15, keep 11 bits down to 2^-21 of the largest.  One product
@@ -1048,7 +1049,7 @@ __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tiles_kerne
                       static_cast<_Float16>(__uint_as_float(w & 0xFFFF0000u) * down)};
         qf[0][ks][k] = __builtin_bit_cast(uint32_t, y);
       }
-    scale = fmaxf(scale * exp_scale(ex), 0x1p-126f);  // above zero, as a.scale
+    scale = fminf(fmaxf(scale * exp_scale(ex), 0x1p-126f), FLT_MAX);  // as a.scale
   }
   ExpRange seen;
 
@@ -1596,9 +1597,10 @@ extern "C" int kda_kv_attend(const kda_kv_pool* kv, const int32_t* page_table, i
   a.n_splits = p.n_splits;
   a.row_tiles = p.row_tiles;
   a.slots = p.slots;
-  // a zero scale stays above zero, so that a masked score (-infinity) times it
-  // is what it was; 2^-126 times any score leaves its weight 1
-  a.scale = std::fmax(std::fabs(scale) * 1.44269504088896340736f, 0x1p-126f);
+  // Above zero, so that a masked score (-infinity) times it is what it was
+  // (2^-126 times any score leaves its weight 1), and finite, so that a score of
+  // zero is.
+  a.scale = std::fmin(std::fmax(std::fabs(scale) * 1.44269504088896340736f, 0x1p-126f), FLT_MAX);
   a.sign = scale < 0.0f ? -1.0f : 1.0f;
   a.part = static_cast<float*>(workspace);
   a.part_ml = a.part == nullptr ? nullptr : a.part + static_cast<int64_t>(p.n_splits) * n_tokens * q_heads * kv->D;

@@ -16,8 +16,7 @@ int kv_check(const kda_kv_pool* kv, int32_t max_pages, int32_t n_seq, int64_t n_
       kv->H > kKvMaxHeads || kv->n_pages < 1)
     return KDA_ERR_SHAPE;
   if (n_seq < 0 || n_tokens < 0 || n_tokens > INT32_MAX || max_pages < 1) return KDA_ERR_ARG;
-  // positions stay below 2^31
-  if (static_cast<int64_t>(max_pages) * kv->page_tokens > INT32_MAX) return KDA_ERR_ARG;
+  if (static_cast<int64_t>(max_pages) * kv->page_tokens > kKvMaxPositions) return KDA_ERR_ARG;
   return KDA_OK;
 }
 

@@ -147,6 +147,8 @@ def test_what_every_entry_point_refuses(call):
     assert call(n_tokens=1 << 31) == B.KDA_ERR_ARG
     assert call(max_pages=0) == B.KDA_ERR_ARG
     assert call(max_pages=1 << 27) == B.KDA_ERR_ARG          # 2^31 positions
+    assert call(max_pages=(1 << 27) - 255) == B.KDA_ERR_ARG  # 16 more than 2^31 - 4096
+    assert call(max_pages=(1 << 27) - 256, n_tokens=0) == B.KDA_OK
     for dtype in (3, 99, -1):
         assert call(dtype=dtype) == B.KDA_ERR_DTYPE_REFUSED
     for name in ("table", "cu"):

@@ -388,6 +388,16 @@ def test_any_scale(scale):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("rows", [2, 80])
+def test_a_scale_near_the_largest_number(dtype, rows):
+    # scores of zero stay zero
+    c = Case([rows], [50], dtype, (2, 1), 64, 16, seed=31)
+    O.append(c.pool, c.table[0], 0, np.zeros((50 + rows, 1, 64)), c.rng.standard_normal((50 + rows, 1, 64)))
+    c.d_pool = dev(c.pool)
+    c.check(c.attend(scale=3.3e38), scale=0.0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("rows", [1, 50])
 def test_strong_scores(dtype, rows):
     # one key far above the others, then one above that: the running maximum
@@ -545,6 +555,30 @@ def test_offsets_past_32_bits():
     O.append(c.pool, c.table[0], 70, c.k_np, c.v_np)
     for got, want in zip((k, v), O.read(c.pool, c.table[0], 70, 5)):
         np.testing.assert_array_equal(host(got), want)
+
+
+@pytest.mark.parametrize("rows", [1, 80])
+def test_the_last_positions(rows):
+    # all of 2^31 - 4096 positions on one page of 256 equal tokens: the mean of
+    # 1.5, over sums that fp32 holds exactly but for the join of the splits
+    n = (1 << 31) - 4096
+    c = Case([256], [0], "bf16", (1, 1), 64, 256, seed=32)
+    O.append(c.pool, c.table[0], 0, np.zeros((256, 1, 64)), np.full((256, 1, 64), 1.5))
+    pool = dev(c.pool)
+    table = torch.full((1, n // 256), int(c.table[0, 0]), dtype=torch.int32, device="cuda")
+    q = torch.ones((rows, 1, 64), dtype=torch.bfloat16, device="cuda")
+    out = torch.empty_like(q)
+    B.kda_kv_attend(pool, table, i32([0, rows]), i32([n - rows]), q, out, max_rows=rows)
+    torch.cuda.synchronize()
+    assert float((out.float() - 1.5).abs().max()) <= 2.0 ** -7  # a step of bf16
+    k, v = (torch.zeros((rows, 1, 64), device="cuda") for _ in range(2))
+    B.kda_kv_read(pool, table, i32([0, rows]), i32([n - rows]), k, v)
+    assert bool((v == 1.5).all())
+    B.kda_kv_append(pool, table, i32([0, rows]), i32([n - rows]), q, q)
+    B.kda_kv_read(pool, table, i32([0, rows]), i32([n - rows]), k, v)
+    assert bool((k == 1).all()) and bool((v == 1).all())
+    B.kda_kv_attend(pool, table, i32([0, rows]), i32([n - rows + 1]), q, out, max_rows=rows)
+    assert bool(out.isnan().all())  # one position too many
 
 
 def test_other_streams_and_own_workspaces():
