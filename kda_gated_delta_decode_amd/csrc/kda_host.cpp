@@ -154,7 +154,9 @@ const char* kda_strerror(int code) {
     case KDA_ERR_NULL: return "a required pointer is NULL";
     case KDA_ERR_DTYPE_REFUSED: return "state dtype refused: only fp32 and fp16 pools are supported (bf16 is refused, not reinterpreted)";
     case KDA_ERR_DTYPE_MISMATCH: return "state dtype does not match the pool's dtype (it would be read at the wrong element size)";
-    case KDA_ERR_SHAPE: return "unsupported shape: K and V must be 128, H in [1, 65535], n_slots at least 1";
+    case KDA_ERR_SHAPE: return "unsupported shape: K and V must be 128, H in [1, 65535], n_slots at least 1 (a 4-bit cache: "
+                                "D 64 or 128, H in [1, 4096], pages of 16, 32, 64, 128 or 256 tokens, q_heads a multiple of H, "
+                                "rot_dim a multiple of 16 up to D)";
     case KDA_ERR_ROWS: return "rows per request must be in [1, 8]";
     case KDA_ERR_SLOT: return "slot id out of range or repeated, or more rows than slots";
     case KDA_ERR_ALIGN: return "a device pointer is not 16-byte aligned";
