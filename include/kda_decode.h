@@ -600,7 +600,8 @@ int kda_kv_read(const kda_kv_pool* kv, const int32_t* page_table, int32_t max_pa
  * step's tokens are appended first).  Query head i reads cached head
  * i / (q_heads / H).
  *   out = sum_t softmax_t(scale * q . k_t) v_t
- *  q               [n_tokens, q_heads, D]; out: the same without gaps.
+ *  q               [n_tokens, q_heads, D]; out: the same without gaps; may be q
+ *                  itself where q has no gaps either.
  *  max_rows        the longest sequence's rows in this launch, max_kv_len its
  *                  tokens including them (0: all that max_pages covers).  They
  *                  choose the kernel and lay out its launch; longer sequences

@@ -77,7 +77,11 @@ KvPlan kv_plan(int32_t H, int32_t D, int32_t n_seq, int64_t n_tokens, int32_t ma
   chunk = per(chunk, 128) * 128;
   if (chunk < 128) chunk = 128;
   p.chunk = static_cast<int32_t>(chunk);
-  p.n_splits = static_cast<int32_t>((max_kv_len + chunk - 1) / chunk);
+  // Of several sequences a rest of up to an eighth goes to the split before it
+  // (8 requests of 8 rows at 4097 tokens: fp32, 12 heads 24.0 -> 22.7 us, 32 query
+  // heads 34.8 -> 30.0); one sequence's splits all run at once, and a longer one
+  // would end last (131072 tokens: 36.8 -> 37.4 us).
+  p.n_splits = static_cast<int32_t>(per(max_kv_len - (n_seq > 1 ? chunk / 8 : 0), chunk));
   if (p.n_splits < 1) p.n_splits = 1;
   return p;
 }

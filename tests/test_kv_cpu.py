@@ -321,7 +321,8 @@ int main() {
     const KvPlan p = kv_plan(H, rand() % 2 ? 64 : 128, n_seq, static_cast<int64_t>(n_seq) * rows, rows, kv, H * G, dt);
     const int64_t tiles = p.tile_rows == 128 ? p.slots : p.row_tiles;
     if (tiles * p.tile_rows < static_cast<int64_t>(rows) * G ||
-        static_cast<int64_t>(p.n_splits) * p.chunk < kv || p.chunk % 32 != 0 || p.n_splits < 1 ||
+        static_cast<int64_t>(p.n_splits) * p.chunk + p.chunk / 8 < kv ||  // (the last split may be longer)
+        p.chunk % 32 != 0 || p.n_splits < 1 ||
         (p.n_splits > 1 && static_cast<int64_t>(p.n_splits - 1) * p.chunk >= kv)) {
       std::printf("plan %d: %d x %d rows, %d x %d tokens\n", it, p.row_tiles, p.tile_rows, p.n_splits, p.chunk);
       return 1;

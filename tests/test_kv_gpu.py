@@ -367,6 +367,21 @@ def test_the_hints_lay_out_the_launch_and_nothing_else(dtype):
     c.check(c.attend(max_rows=None))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,past,power", [([1, 2], [300, 4097], 0), ([1] * 3, [3000] * 3, 0), ([300, 40], [0, 2500], 0),
+                                             ([300, 40], [0, 2500], 20)])
+def test_outputs_over_the_queries(dtype, rows, past, power):
+    # one split and several, prompts that start again in bf16 pieces
+    c = Case(rows, past, dtype, (8, 4), 128, 32, seed=33, joint=False)
+    for s in range(c.n):
+        k = c.rng.standard_normal((past[s] + rows[s], 4, 128))
+        O.append(c.pool, c.table[s], 0, k, c.rng.standard_normal(k.shape) * 2.0 ** power)
+    c.d_pool = dev(c.pool)
+    want = c.attend()
+    assert torch.equal(c.attend(c.q), want)
+    c.check(want)
+
+
 def test_a_prompt_among_many_steps():
     # tiles of a launch with a long prompt between single tokens, sequences
     # without rows, and spare rows at both ends
