@@ -72,6 +72,9 @@ KvPlan kv_plan(int32_t H, int32_t D, int32_t n_seq, int64_t n_tokens, int32_t ma
     // sequence (512 rows on 15000 tokens: 165 us; 190, 220 for 1024, 1536), at least
     // one for several, whose rows and lengths differ (4 chunks of up to 700 rows
     // on up to 16000 tokens, 226 slots: 3 splits 174 us, 2 or 4 some 210).
+    // From 1024 tokens a split, whose first steps fill the pipeline and whose rows
+    // are joined (2 chunks of 262 rows on 4400 tokens: 36 us, 45 with 512; 512
+    // fp32 rows on 4000: 62 and 83).
     chunk = n_seq > 1 ? chunk_of(per(512, units) * units, 1024) : chunk_of(512, 1024);
   }
   chunk = per(chunk, 128) * 128;
