@@ -719,7 +719,7 @@ def kda_kv_attend(pool, page_table, cu_seqlens, cache_lens, q, out, max_rows: in
     include/kda_decode.h).
 
     q: [T, q_heads, D] of float32, float16 or bfloat16 (token stride free);
-    out: the same, contiguous.  max_rows: the longest sequence's rows in this
+    out: the same, contiguous, may be q.  max_rows: the longest sequence's rows in this
     launch (default T); max_kv_len: its tokens including them (default: what
     page_table covers): they lay out the launch, results hold for any.
     workspace: a contiguous uint8 tensor of kda_kv_attend_workspace bytes, or
