@@ -1187,6 +1187,7 @@ __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tiles_kerne
   if constexpr (PIPED) {
 #pragma unroll
     for (int i = 0; i < 2 * KS; ++i) score(i, key_piece(0, i), sc0);
+    __syncthreads();  // all waves have these keys: the first step writes over them
   }
   auto top_score = [&](const f16v (&x)[2]) __attribute__((always_inline)) {
     float y = -INFINITY;

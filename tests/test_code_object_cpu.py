@@ -324,3 +324,22 @@ def test_no_packed_fp32_instructions(disassembly):
     packed = {"v_pk_fma_f32", "v_pk_mul_f32", "v_pk_add_f32"}
     found = {n: sorted(packed & set(ops)) for n, ops in disassembly.items() if packed & set(ops)}
     assert not found, found
+
+
+def test_prompt_tiles_read_one_steps_operands_between_barriers(disassembly):
+    # The 4-bit cache's prompt kernel overwrites a key buffer in each step, which
+    # the barrier before that step has to part from the scores that read it.  A
+    # wave therefore never reads more than one step's operands (16-byte reads:
+    # D / 8 of keys, D / 8 of values) between two barriers around a write: were
+    # the first tile's scores in the first step's segment, it would read D / 8
+    # more, from the buffer that the step writes.
+    tiles = {n: ops for n, ops in disassembly.items() if "kda_kv_tiles_kernel" in n and not n.endswith(".kd")}
+    assert len(tiles) == 6
+    for name, ops in tiles.items():
+        dim = 128 if re.search(r"kda_kv_tiles_kernelILi\dELi128E", name) else 64
+        cuts = [i for i, op in enumerate(ops) if op == "s_barrier"]
+        reads = []
+        for a, b in zip(cuts, cuts[1:]):
+            if any(op.startswith("ds_write") for op in ops[a:b]):
+                reads.append(sum(op.startswith("ds_read_b128") for op in ops[a:b]))
+        assert reads and max(reads) <= dim // 4, (name, reads)
