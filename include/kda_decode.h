@@ -622,6 +622,10 @@ int kda_kv_read(const kda_kv_pool* kv, const int32_t* page_table, int32_t max_pa
  * 2^-25 of the row's largest channel.  Other exponents are multiplied as above.
  * The order of the sums depends on the launch's sizes, not on timing: equal calls
  * give equal bits.
+ * Scores are fp32 numbers: a row whose largest score is infinite, of either sign,
+ * is NaN (a score that passes the largest fp32 when multiplied by scale, or by a
+ * query with an infinity; where q . k alone passes it, bf16 prompts, which take
+ * the row's power of two out first, may still hold it).
  * A row that sees a poisoned token or a page that does not exist is NaN in
  * that head; the rows of a sequence with a negative length or one that
  * max_pages cannot hold are NaN.  Errors: KDA_ERR_NULL and KDA_ERR_ARG also for

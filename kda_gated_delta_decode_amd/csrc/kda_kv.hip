@@ -863,8 +863,9 @@ __global__ __launch_bounds__(64 * NW, (kv_rows_waves<NT, NW>())) void kda_kv_row
       const int tok = row / a.group, g = row - tok * a.group;
       const int64_t at = (q.n0 + tok) * a.q_heads + static_cast<int64_t>(h) * a.group + g;
       if (splits == 1) {
-        // a row that sees nothing is zero; a bad sequence's rows are NaN
-        const float inv = q.bad ? __builtin_nanf("") : total == 0.0f ? 0.0f : 1.0f / total;
+        // every row sees its own token: a sum of zero means that its largest
+        // score is infinite, and 0 / 0 makes the row NaN, as a bad sequence's are
+        const float inv = q.bad ? __builtin_nanf("") : 1.0f / total;
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] *= inv;
         store8<DT>(a.out, at * D + c, acc);
@@ -1305,7 +1306,7 @@ __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tiles_kerne
     const int ot = out_row / args->group, og = out_row - ot * args->group;
     const int64_t at = (q.n0 + ot) * args->q_heads + static_cast<int64_t>(h) * args->group + og;
     const int64_t slot = static_cast<int64_t>(sp) * args->t.n_tokens * args->q_heads + at;
-    const float inv = splits > 1 ? 1.0f : q.bad ? __builtin_nanf("") : sum == 0.0f ? 0.0f : 1.0f / sum;
+    const float inv = splits > 1 ? 1.0f : q.bad ? __builtin_nanf("") : 1.0f / sum;  // sum 0: NaN, as above
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int64_t c0 = VC * (8 * (e / 4) + 4 * out_half + e % 4);
@@ -1414,7 +1415,7 @@ __global__ __launch_bounds__(256) void kda_kv_join_kernel(KvAttendArgs a, int ti
       }
       __syncthreads();
     }
-    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+    const float inv = 1.0f / total;  // (a sum of zero: NaN, as above)
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] *= inv;
     if (!MANY || threadIdx.x < PER) store8<DT>(a.out, at * D + c, acc);

@@ -413,6 +413,31 @@ def test_a_scale_near_the_largest_number(dtype, rows):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("rows,past", [(2, 50), (80, 50), (2, 3000), (80, 3000)])
+@pytest.mark.parametrize("what", ["largest", "all", "query"])
+def test_rows_whose_largest_score_is_infinite_are_nan(dtype, rows, past, what):
+    # a key whose score passes the largest fp32 in the middle of the new rows;
+    # all scores below the lowest; a query with an infinity over keys that make
+    # every score minus infinity.  Other scores are 0: rows before are the mean.
+    c = Case([rows], [past], dtype, (2, 1), 64, 16, seed=34, joint=False)
+    k = np.zeros((past + rows, 1, 64))
+    first = past + rows // 2 if what == "largest" else 0    # the first token of which a row becomes NaN
+    k[first if what == "largest" else slice(0, None)] = 1.0 if what == "largest" else -1.0
+    O.append(c.pool, c.table[0], 0, k, c.rng.standard_normal(k.shape))
+    c.d_pool = dev(c.pool)
+    c.q = torch.ones_like(c.q)
+    if what == "query":
+        c.q[:, :, 5] = float("inf")
+    got = c.attend(scale=3.3e38 if what != "query" else 0.125)
+    sees = past + np.arange(rows) >= first
+    np.testing.assert_array_equal(np.isnan(host(got)).all((1, 2)), sees)
+    assert not np.isnan(host(got)[~sees]).any()
+    c.rows, c.cu = [int((~sees).sum())], np.array([0, (~sees).sum()])
+    c.hq_np = np.zeros_like(c.hq_np)
+    c.check(got, scale=0.0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("rows", [1, 50])
 def test_strong_scores(dtype, rows):
     # one key far above the others, then one above that: the running maximum
