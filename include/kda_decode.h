@@ -626,6 +626,8 @@ int kda_kv_read(const kda_kv_pool* kv, const int32_t* page_table, int32_t max_pa
  * is NaN (a score that passes the largest fp32 when multiplied by scale, or by a
  * query with an infinity; where q . k alone passes it, bf16 prompts, which take
  * the row's power of two out first, may still hold it).
+ * Rows are computed in tiles of up to 128, and where a row's sums are rounded may
+ * depend on what its tile's other rows see; nothing else of a row does.
  * A row that sees a poisoned token or a page that does not exist is NaN in
  * that head; the rows of a sequence with a negative length or one that
  * max_pages cannot hold are NaN.  Errors: KDA_ERR_NULL and KDA_ERR_ARG also for

@@ -949,7 +949,7 @@ struct ExpRange {
 // weights, at most 2^15, keep 11 bits down to 2^-21 of the largest.  One product
 // for each operand then does what two or three bf16 pieces do.  The exponents
 // are looked at on the way; a block that meets another one throws its sums
-// away and starts again in bf16 pieces.
+// away and starts again in bf16 pieces.  (Poisoned keys are NaN in fp16 too.)
 //
 // Bound by the matrix cores and the vector work beside them: 8192 bf16 rows of 32
 // query heads 560 us, 980 TFLOP/s of the 1211 that a large bf16 matrix product
@@ -1114,10 +1114,10 @@ __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tiles_kerne
     const float ks = exp_scale(ke);
     u4 x = {dequant2_as<HALF, 0>(kc[m], ks), dequant2_as<HALF, 1>(kc[m], ks), dequant2_as<HALF, 2>(kc[m], ks),
             dequant2_as<HALF, 3>(kc[m], ks)};
-    if constexpr (HALF) {  // a poisoned key does not fit
-      if (m == 0) seen.take2((tb + kt < t1 ? ke : 127u) * 0x10001u);
-    } else if (m == 0) {
-      x[0] |= ke == kKvPoison ? ~0u : 0u;
+    if (m == 0) {
+      const bool poison = ke == kKvPoison;  // NaN in either type
+      if constexpr (HALF) seen.take2((tb + kt < t1 && !poison ? ke : 127u) * 0x10001u);
+      x[0] |= poison ? ~0u : 0u;
     }
     *reinterpret_cast<u4*>(k_sh + buf * KBUF + k_to + 16 * m) = x;
   };

@@ -550,6 +550,29 @@ def test_prompts_over_zeros_and_poison(dtype):
     assert (np.abs(got[:110, 2:] - host(clean)[:110, 2:]) <= 2.0 ** -7).all()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("rows", [8, 200])
+@pytest.mark.parametrize("how", ["poison", "page"])
+def test_rows_before_a_poisoned_token_keep_their_bits(dtype, rows, how):
+    # scores so small that the running maximum moves in the first tile alone:
+    # then nothing of a row depends on its tile's other rows
+    past = 130
+    c = Case([rows], [past], dtype, (4, 2), 64, 16, seed=35, joint=False).fill()
+    c.q *= 2.0 ** -6
+    clean = c.attend().clone()
+    at = past + (5 if rows == 8 else 110)
+    if how == "poison":
+        O.append(c.pool, c.table[0], at, np.full((1, 2, 64), np.inf), np.ones((1, 2, 64)))
+    else:
+        at = at // 16 * 16
+        c.table[0, at // 16] = c.n_pages
+    c.d_pool, c.d_table = dev(c.pool), dev(c.table)
+    got = c.attend()
+    keep = max(at - past, 0)
+    assert torch.equal(got[:keep], clean[:keep])
+    assert bool(got[keep:].isnan().all())
+
+
 @pytest.mark.parametrize("power", [-120, -60, -10, 10, 60])
 def test_queries_of_any_size(power):
     # bf16 queries far outside fp16's range, keys inside: scores tiny or, with
