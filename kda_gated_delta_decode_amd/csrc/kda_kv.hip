@@ -922,8 +922,10 @@ struct ExpRange {
     low = __builtin_elementwise_min(low, static_cast<u16x2>(x - static_cast<uint16_t>(kKvMinExp + 1)));
   }
   __device__ __forceinline__ bool in_half() const {
-    constexpr int least = kHalfMinExp - (kKvMinExp + 1);
-    return top[0] <= kHalfMaxExp && top[1] <= kHalfMaxExp && low[0] >= least && low[1] >= least;
+    constexpr uint16_t least = kHalfMinExp - (kKvMinExp + 1), most = kHalfMaxExp;
+    const u16x2 over = __builtin_elementwise_sub_sat(top, u16x2{most, most});
+    const u16x2 under = __builtin_elementwise_sub_sat(u16x2{least, least}, low);
+    return __builtin_bit_cast(uint32_t, over | under) == 0;
   }
 };
 
@@ -948,11 +950,13 @@ struct ExpRange {
 // row's power of two loses at most 2^-25 of the row's largest channel, and
 // weights, at most 2^15, keep 11 bits down to 2^-21 of the largest.  One product
 // for each operand then does what two or three bf16 pieces do.  The exponents
-// are looked at on the way; a block that meets another one throws its sums
-// away and starts again in bf16 pieces.  (Poisoned keys are NaN in fp16 too.)
+// are looked at before their tiles are added, two tiles at a time: a block that
+// meets another one goes on from there in bf16 pieces, with the sums that it has
+// (8192 bf16 rows with one such token near the front: 720 us, fp16 820; near the
+// end 530).  Poisoned keys are NaN in fp16 too.
 //
 // Bound by the matrix cores and the vector work beside them: 8192 bf16 rows of 32
-// query heads 560 us, 980 TFLOP/s of the 1211 that a large bf16 matrix product
+// query heads 536 us, 1026 TFLOP/s of the 1211 that a large bf16 matrix product
 // reaches (829 us with two bf16 pieces for a weight, one tile after the other).
 template <int DT, int D>
 __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tiles_kernel(KvAttendArgs a) {
@@ -965,9 +969,10 @@ __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tiles_kerne
   constexpr int KBUF = KT * KROW, VBUF = D * VROW;
   __shared__ __attribute__((aligned(16))) char k_sh[2 * KBUF];
   __shared__ __attribute__((aligned(16))) char v_sh[2 * VBUF];
+  // whether a wave met an exponent that fp16 does not hold
+  __shared__ __attribute__((aligned(4))) uint8_t far_sh[4];
 
-  const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
-  const int i32 = lane % 32, half = lane / 32;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   // A sequence's last tiles see the most tokens and go first.  Heads go round
   // the XCDs: with 8 of them each stays on one, and in its L2.
   const int h = blockIdx.x % a.t.H, turn = blockIdx.x / a.t.H;
@@ -984,6 +989,38 @@ __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tiles_kerne
   const uint8_t* head0 = a.t.base + static_cast<int64_t>(h) * block_bytes;
   const_i32* table = (const_i32*)(a.t.page_table + static_cast<int64_t>(s) * a.t.max_pages);
 
+  const int last_row = (row0 + R < all_rows ? row0 + R : all_rows) - 1;
+  const int vis = q.past + last_row / a.group + 1;
+  const int splits = q.bad ? 1 : kv_splits(vis, a);
+  if (sp >= splits) return;
+  const int t0 = q.bad ? 0 : sp * a.chunk;
+  const int t1 = q.bad ? 0 : sp == splits - 1 ? vis : t0 + a.chunk;
+  const int w_first = q.past + (row0 + 32 * wave) / a.group;  // the last token all of the wave's rows see
+
+  // Weights of 16-bit types are taken 2^7 times larger, at most 2^15: fp16 has
+  // room for smaller ones then.
+  constexpr float UP = DT == KDA_F32 ? 0.0f : 7.0f;
+  f16v zero;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) zero[e] = 0.0f;
+  f16v o[CB];
+#pragma unroll
+  for (int c = 0; c < CB; ++c) o[c] = zero;
+  float mx = -INFINITY, sum = 0.0f;
+
+  // Adds the tokens from `from` on; with HALF in fp16, up to a tile that does not
+  // fit.  Returns the first token that is left.
+  auto attend = [&](auto in_half, int from) __attribute__((always_inline)) {
+  constexpr bool HALF = decltype(in_half)::value;
+  constexpr int NQ = HALF ? 1 : q_pieces<DT>(), NP = HALF ? 1 : w_pieces<DT>();
+  // 16-bit types in bf16 keep two pieces of weights (fp16: of queries too), and
+  // have no registers for a second tile's scores
+  constexpr bool PIPED = HALF || DT == KDA_F32;
+  // The lane's places, from an opaque thread id: those of the one form kept over
+  // the other's steps would be spilled.
+  int tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));
+  const int lane = tid % 64, i32 = lane % 32, half = lane / 32;
   // -- a thread's share of a tile's codes: key kt, channels D / 4 kj..; values
   // 4 vt .. 4 vt + 3, channels VC vo..  A wave's 16 tokens lie on one page.
   const int kt = tid / 4, kj = tid % 4, vt = 4 * wave + lane % 4, vo = lane / 4;
@@ -998,25 +1035,10 @@ __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tiles_kerne
   const uint32_t v_off = 4 * (lane % 4) * (D / 2) + vo * (VC / 2);
   const uint32_t ve_off = (vo * VC / kKvGroup) * a.t.P + 4 * (lane % 4);
 
-  const int last_row = (row0 + R < all_rows ? row0 + R : all_rows) - 1;
-  const int vis = q.past + last_row / a.group + 1;
-  const int splits = q.bad ? 1 : kv_splits(vis, a);
-  if (sp >= splits) return;
-  const int t0 = q.bad ? 0 : sp * a.chunk;
-  const int t1 = q.bad ? 0 : sp == splits - 1 ? vis : t0 + a.chunk;
-  const int w_first = q.past + (row0 + 32 * wave) / a.group;  // the last token all of the wave's rows see
-
   const int row = row0 + 32 * wave + i32;
   const int r_in = row <= last_row ? row : last_row;
   const int tok = r_in / a.group, g = r_in - tok * a.group;
   const int limit = row <= last_row ? q.past + tok : -1;
-  // All of the tile; with HALF in fp16, and false if that does not do.
-  auto attend = [&](auto in_half) __attribute__((always_inline)) {
-  constexpr bool HALF = decltype(in_half)::value;
-  constexpr int NQ = HALF ? 1 : q_pieces<DT>(), NP = HALF ? 1 : w_pieces<DT>();
-  // fp16's second try keeps two pieces of queries and weights, and has no
-  // registers for a second tile's scores
-  constexpr bool PIPED = HALF || DT == KDA_F32;
   float scale = a.scale;
   u4 qf[NQ][KS];
   kernel_args args0 = (kernel_args)__builtin_amdgcn_kernarg_segment_ptr();
@@ -1062,14 +1084,17 @@ __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tiles_kerne
   }
   ExpRange seen;
 
-  uint32_t kc[D / 32], ke, vc[4], ve;
+  // The codes in flight; HALF: and the exponents of the next tile's values, from
+  // every second step's key load, whose block they are in.
+  uint32_t kc[D / 32], ke, vc[4], ve, ve_next;
   auto page_of = [&](int tb) __attribute__((always_inline)) {
     const int t = tb + 16 * wave;
     const int page = t < t1 ? table[t >> a.t.log_p] : -1;
     return page < a.t.n_pages ? page : -1;
   };
-  auto load_keys = [&](int tb) __attribute__((always_inline)) {
+  auto load_keys = [&](int tb, auto with_values) __attribute__((always_inline)) {
     const int page = page_of(tb);
+    if constexpr (decltype(with_values)::value) ve_next = 0x7F7F7F7Fu;
     if (page >= 0) {
       const uint8_t* blk = head0 + page * a.t.page_bytes;
       const uint32_t r = (tb + 16 * wave) & (a.t.P - 1);
@@ -1083,14 +1108,17 @@ __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tiles_kerne
         kc[0] = x[0], kc[1] = x[1];
       }
       ke = (blk + kv_key_exps(a.t.P, D) + r * (D / kKvGroup))[k_off / 16];  // 16 bytes of codes an exponent
+      if constexpr (decltype(with_values)::value)
+        ve_next = *reinterpret_cast<const uint32_t*>(blk + kv_value_exps(a.t.P, D) + r + ve_off);
     } else {
       ke = kKvPoison;  // scores NaN, seen only where the mask lets them
 #pragma unroll
       for (int m = 0; m < D / 32; ++m) kc[m] = 0;
     }
   };
-  auto load_values = [&](int tb) __attribute__((always_inline)) {
+  auto load_values = [&](int tb, auto with_exps) __attribute__((always_inline)) {
     const int page = page_of(tb);
+    if constexpr (!decltype(with_exps)::value) ve = ve_next;
     if (page >= 0) {
       const uint8_t* blk = head0 + page * a.t.page_bytes;
       const uint32_t r = (tb + 16 * wave) & (a.t.P - 1);
@@ -1102,9 +1130,10 @@ __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tiles_kerne
         else
           vc[e] = *reinterpret_cast<const uint16_t*>(at + v_off + e * (D / 2));
       }
-      ve = *reinterpret_cast<const uint32_t*>(blk + kv_value_exps(a.t.P, D) + r + ve_off);
+      if constexpr (decltype(with_exps)::value)
+        ve = *reinterpret_cast<const uint32_t*>(blk + kv_value_exps(a.t.P, D) + r + ve_off);
     } else {
-      ve = 0x7F7F7F7Fu;
+      if constexpr (decltype(with_exps)::value) ve = 0x7F7F7F7Fu;
 #pragma unroll
       for (int e = 0; e < 4; ++e) vc[e] = 0;
     }
@@ -1122,23 +1151,27 @@ __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tiles_kerne
     *reinterpret_cast<u4*>(k_sh + buf * KBUF + k_to + 16 * m) = x;
   };
   // values behind the last token may be anything: zeros
-  auto end_values = [&](int tb) __attribute__((always_inline)) {
+  auto end_exps = [&](int tb, uint32_t& exps, auto zero_code) __attribute__((always_inline)) {
     if (tb + KT > t1) {
+      int id = threadIdx.x;  // (as above: kept for this alone, vt was spilled)
+      asm volatile("" : "+v"(id));
+      const int t = tb + 16 * wave + 4 * (id % 4);
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (tb + 4 * vt + e >= t1) {
-          vc[e] = 0;
-          ve = (ve & ~(0xFFu << (8 * e))) | (127u << (8 * e));
+        if (t + e >= t1) {
+          zero_code(e);
+          exps = (exps & ~(0xFFu << (8 * e))) | (127u << (8 * e));
         }
     }
+  };
+  auto end_values = [&](int tb) __attribute__((always_inline)) { end_exps(tb, ve, [&](int e) { vc[e] = 0; }); };
+  auto see = [&](uint32_t exps) __attribute__((always_inline)) {
+    seen.take2(exps & 0x00FF00FFu);
+    seen.take2((exps >> 8) & 0x00FF00FFu);
   };
   // channels 2 c2 and 2 c2 + 1 of the 4 values
   auto stage_value = [&](int buf, auto pick) __attribute__((always_inline)) {
     constexpr int c2 = decltype(pick)::value;
-    if constexpr (HALF && c2 == 0) {
-      seen.take2(ve & 0x00FF00FFu);
-      seen.take2((ve >> 8) & 0x00FF00FFu);
-    }
     uint32_t x[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) x[e] = dequant2_as<HALF, c2>(vc[e], exp_scale((ve >> (8 * e)) & 0xFF));
@@ -1146,9 +1179,6 @@ __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tiles_kerne
     *reinterpret_cast<u2*>(v_sh + buf * VBUF + (32 * c2 + 16) * VROW + v_to) =
         u2{pack_hi(x[0], x[1]), pack_hi(x[2], x[3])};
   };
-  f16v zero;
-#pragma unroll
-  for (int e = 0; e < 16; ++e) zero[e] = 0.0f;
   // product i of a tile's scores: channels 16 (i / 2).., tokens 32 (i % 2)..
   auto key_piece = [&](int buf, int i) __attribute__((always_inline)) {
     const int ks = i / 2, b = i % 2;
@@ -1164,26 +1194,38 @@ __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tiles_kerne
   };
   f16v sc0[2], sc1[2];  // scores of tiles in turn
 
-  f16v o[CB];
+  if constexpr (HALF) far_sh[wave] = 0;
+  constexpr std::true_type yes{};
+  constexpr std::false_type no{};
+  load_keys(from, no);
+  load_values(from, yes);
 #pragma unroll
-  for (int c = 0; c < CB; ++c) o[c] = zero;
-  float mx = -INFINITY, sum = 0.0f;
-  load_keys(t0);
-  load_values(t0);
-#pragma unroll
-  for (int m = 0; m < D / 32; ++m) stage_key(0, m, t0);
-  load_keys(t0 + KT);
-  end_values(t0);
+  for (int m = 0; m < D / 32; ++m) stage_key(0, m, from);
+  load_keys(from + KT, no);
+  end_values(from);
+  if constexpr (HALF) see(ve);
   stage_value(0, std::integral_constant<int, 0>{});
   stage_value(0, std::integral_constant<int, 1>{});
   if constexpr (D == 128) {
     stage_value(0, std::integral_constant<int, 2>{});
     stage_value(0, std::integral_constant<int, 3>{});
   }
-  load_values(t0 + KT);
+  load_values(from + KT, yes);
 #pragma unroll
-  for (int m = 0; m < D / 32; ++m) stage_key(1, m, t0 + KT);
-  load_keys(t0 + 2 * KT);
+  for (int m = 0; m < D / 32; ++m) stage_key(1, m, from + KT);
+  load_keys(from + 2 * KT, no);
+  if constexpr (HALF) {
+    end_values(from + KT);
+    see(ve);
+  }
+  // A wave that met a far exponent says so before an odd step's barrier, and the
+  // block turns away behind it (the even step's barrier lies between that look
+  // and the next odd step's word).
+  auto report = [&]() __attribute__((always_inline)) {
+    if (__ballot(!seen.in_half()) != 0) far_sh[wave] = 1;
+    seen = ExpRange{};
+  };
+  if constexpr (HALF) report();
   __syncthreads();
   if constexpr (PIPED) {
 #pragma unroll
@@ -1197,8 +1239,14 @@ __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tiles_kerne
     return y;
   };
   float best = PIPED ? top_score(sc0) : 0.0f;
+  // Even steps look at what the block has met: their own and the next step's
+  // values, and their next tile's keys (keys of the next step's next tile are
+  // used in the step after that one).  False: nothing is added.
   auto step = [&](int tb, auto which, f16v (&sc)[2], f16v (&next)[2]) __attribute__((always_inline)) {
     constexpr int buf = decltype(which)::value;
+    if constexpr (HALF && buf == 0) {
+      if (__builtin_amdgcn_readfirstlane(*reinterpret_cast<const uint32_t*>(far_sh)) != 0) return false;
+    }
     if constexpr (!PIPED) {
 #pragma unroll
       for (int i = 0; i < 2 * KS; ++i) {
@@ -1226,8 +1274,7 @@ __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tiles_kerne
       for (int c = 0; c < CB; ++c) o[c] *= keep;
     }
     end_values(tb + KT);
-    // weights in fp16 are taken 2^7 times larger, at most 2^15
-    const float base = (mx == -INFINITY ? 0.0f : -mx) + (HALF ? 7.0f : 0.0f);
+    const float base = (mx == -INFINITY ? 0.0f : -mx) + UP;
     // -- this tile's weights, the next one's scores: after each product the
     // vector work that fits beside it, operands read AHEAD products early
     constexpr int AHEAD = 2;
@@ -1277,25 +1324,38 @@ __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tiles_kerne
       __builtin_amdgcn_sched_barrier(0);
     };
     each_of(output, std::make_integer_sequence<int, 4 * CB>{});
-    load_keys(tb + 3 * KT);
-    load_values(tb + 2 * KT);
+    if constexpr (HALF && buf == 1) {
+      see(ve);
+      end_exps(tb + 2 * KT, ve_next, [](int) {});
+      see(ve_next);
+      report();
+    }
+    load_keys(tb + 3 * KT, std::integral_constant<bool, HALF && buf == 0>{});
+    load_values(tb + 2 * KT, std::integral_constant<bool, !HALF || buf == 0>{});
     __syncthreads();
+    return true;
   };
-  for (int tb = t0; tb < t1; tb += 2 * KT) {
-    step(tb, std::integral_constant<int, 0>{}, sc0, sc1);
+  for (int tb = from; tb < t1; tb += 2 * KT) {
+    if (!step(tb, std::integral_constant<int, 0>{}, sc0, sc1)) return tb;
     if (tb + KT >= t1) break;
-    if constexpr (PIPED)
-      step(tb + KT, std::integral_constant<int, 1>{}, sc1, sc0);
-    else
-      step(tb + KT, std::integral_constant<int, 1>{}, sc0, sc1);
+    if constexpr (PIPED) {
+      if (!step(tb + KT, std::integral_constant<int, 1>{}, sc1, sc0)) return tb + KT;
+    } else {
+      if (!step(tb + KT, std::integral_constant<int, 1>{}, sc0, sc1)) return tb + KT;
+    }
   }
-  if constexpr (HALF) {
-    if (!__syncthreads_and(seen.in_half())) return false;
+  return t1;
+  };
+  if constexpr (DT == KDA_F32) {
+    attend(std::false_type{}, t0);
+  } else {
+    const int left = attend(std::true_type{}, t0);
+    if (left < t1) attend(std::false_type{}, left);
   }
 
   // The lane's row and the arguments once more, from an opaque thread id and
   // address: kept from above, they would be spilled over the steps.
-  int again = tid;
+  int again = threadIdx.x;
   kernel_args args = (kernel_args)__builtin_amdgcn_kernarg_segment_ptr();
   asm volatile("" : "+v"(again), "+s"(args));
   // -- rows out: element e of block c is row 8 (e / 4) + 4 half + e % 4 of
@@ -1319,16 +1379,9 @@ __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tiles_kerne
         store_channels<KDA_F32>(args->part, slot * D + c0, x);
     }
     if (splits > 1 && out_half == 0) {
-      args->part_ml[2 * slot] = mx - (HALF ? 7.0f : 0.0f);
+      args->part_ml[2 * slot] = mx - UP;
       args->part_ml[2 * slot + 1] = sum;
     }
-  }
-  return true;
-  };
-  if constexpr (DT == KDA_F32) {
-    attend(std::false_type{});
-  } else {
-    if (!attend(std::true_type{})) attend(std::false_type{});
   }
 }
 

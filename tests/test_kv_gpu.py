@@ -550,6 +550,35 @@ def test_prompts_over_zeros_and_poison(dtype):
     assert (np.abs(got[:110, 2:] - host(clean)[:110, 2:]) <= 2.0 ** -7).all()
 
 
+@pytest.mark.parametrize("dtype,D", [("f16", 64), ("bf16", 128)])
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("past,at", [(0, 0), (0, 63), (0, 64), (0, 127), (100, 140), (100, 192), (100, 220), (100, 299),
+                                     (1500, 0), (1500, 1023), (1500, 1088), (1500, 1540), (1500, 1620), (1500, 1699)])
+def test_one_far_exponent_anywhere_in_a_prompt(dtype, D, which, past, at):
+    # a single group that fp16 does not hold, in any tile of a split: the block
+    # goes on in bf16 pieces from its pair of tiles on, and rows that see nothing
+    # of that keep their bits (scores are too small to move a maximum after a
+    # first tile)
+    rows = 200
+    c = Case([rows], [past], dtype, (2, 2), D, 64, seed=36, joint=False)
+    c.q *= 2.0 ** -6
+    c.hq_np = host(c.q)
+    r, n = c.rng, past + rows
+    k, v = r.standard_normal((n, 2, D)), r.standard_normal((n, 2, D))
+    O.append(c.pool, c.table[0], 0, k, v)
+    c.d_pool = dev(c.pool)
+    clean = c.attend().clone()
+    c.check(clean)
+    (k if which == "k" else v)[at, 1, 32:64] *= 2.0 ** -30
+    O.append(c.pool, c.table[0], 0, k, v)
+    c.d_pool = dev(c.pool)
+    got = c.attend()
+    c.check(got)
+    keep = max(at // 128 * 128 - past, 0)
+    assert torch.equal(got[:keep], clean[:keep])
+    assert torch.equal(got[:, :1], clean[:, :1])        # the other head's
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("rows", [8, 200])
 @pytest.mark.parametrize("how", ["poison", "page"])
