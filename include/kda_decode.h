@@ -614,8 +614,8 @@ int kda_kv_read(const kda_kv_pool* kv, const int32_t* page_table, int32_t max_pa
  *                  the launch has run.  Calls that may overlap need their own.
  * Cached values enter the matrix cores as they are.  So does q, as 3 (fp32), 2
  * (fp16) or 1 bf16 numbers that add up to it; scores, weights, their sums and the
- * output's sums are fp32, and weights lose less than 2^-15 of themselves where
- * outputs have 16 bits.  Prompts of 16-bit types (more than 64 rows of a
+ * output's sums are fp32, and weights are rounded to nearest, by at most 2^-16 of
+ * themselves, where outputs have 16 bits.  Prompts of 16-bit types (more than 64 rows of a
  * sequence and cached head) are multiplied in fp16 where the exponents they meet
  * allow it (104..140, and 2, which zeros have): weights are then rounded to 11
  * bits, and a bf16 query, divided by its row's power of two, is off by at most

@@ -518,8 +518,8 @@ __device__ __forceinline__ TileAt tile_of_slot(const KvAttendArgs& a, int slot) 
 template <int DT>
 constexpr int q_pieces() { return DT == KDA_F32 ? 3 : DT == KDA_F16 ? 2 : 1; }
 // Softmax weights are fp32.  fp32 outputs take all 24 bits of them; for 16-bit
-// outputs two pieces leave less than 2^-15 of one, a sixteenth of fp16's half
-// step.
+// outputs the second of two pieces is rounded to nearest, which is off by at most
+// 2^-16 of a weight, a 32nd of fp16's half step, to either side.
 template <int DT>
 constexpr int w_pieces() { return DT == KDA_F32 ? 3 : 2; }
 
@@ -532,6 +532,19 @@ __device__ __forceinline__ void split_pair(float x, float y, uint32_t (&out)[N])
     out[p] = pack_hi(bits(x), bits(y));
     x -= __uint_as_float(bits(x) & 0xFFFF0000u);
     y -= __uint_as_float(bits(y) & 0xFFFF0000u);
+  }
+}
+
+// two weights as their pieces
+template <int N>
+__device__ __forceinline__ void split_weights(float x, float y, uint32_t (&out)[N]) {
+  if constexpr (N == 2) {
+    out[0] = pack_hi(bits(x), bits(y));
+    x -= __uint_as_float(bits(x) & 0xFFFF0000u);
+    y -= __uint_as_float(bits(y) & 0xFFFF0000u);
+    out[1] = __builtin_bit_cast(uint32_t, bf2{static_cast<__bf16>(x), static_cast<__bf16>(y)});
+  } else {
+    split_pair<N>(x, y, out);
   }
 }
 
@@ -789,7 +802,7 @@ __global__ __launch_bounds__(64 * NW, (kv_rows_waves<NT, NW>())) void kda_kv_row
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           uint32_t t[NP];
-          split_pair<NP>(w[2 * e], w[2 * e + 1], t);
+          split_weights<NP>(w[2 * e], w[2 * e + 1], t);
 #pragma unroll
           for (int p = 0; p < NP; ++p) pf[n][p][e] = t[p];
         }
@@ -1299,7 +1312,7 @@ __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tiles_kerne
         if constexpr (HALF) {
           x[0] = __builtin_bit_cast(uint32_t, h2{static_cast<_Float16>(w0), static_cast<_Float16>(w1)});
         } else {
-          split_pair<NP>(w0, w1, x);
+          split_weights<NP>(w0, w1, x);
         }
 #pragma unroll
         for (int p = 0; p < NP; ++p) pf[2 * b + e / 8][p][(e % 8) / 2] = x[p];

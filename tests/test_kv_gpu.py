@@ -616,6 +616,43 @@ def test_queries_of_any_size(power):
         c.check(c.attend())
 
 
+@pytest.mark.parametrize("rows,far", [(8, False), (100, False), (100, True)])
+def test_errors_lean_to_neither_side(rows, far):
+    # The part of the error that goes with the result, over some 300,000 fp16
+    # outputs.  Each is rounded to half a step, to either side alike, which gives
+    # the slope a variance of sum step^2 want^2 / 12 / (sum want^2)^2, its root some
+    # 1e-6.  Weights cut to 16 bits instead of rounded lean by 2^-17 = 8e-6.
+    # A prompt whose weights p_t are rounded to fp16, by up to 2^-11 of each to either
+    # side, gets sum_t p_t d_t (v_t - out) more: along out, and summed over rows and
+    # heads, a variance of 2^-22 / 3 sum p_t^2 (v_t . out - out . out)^2 / (sum want^2)^2.
+    n = 24 if rows == 8 else 2
+    c = Case([rows] * n, [300] * n, "f16", (12, 12), 128, 16, seed=37, joint=False).fill()
+    if far:  # a group that fp16 does not hold, in the first tile
+        for s in range(n):
+            k, v = O.read(c.pool, c.table[s], 0, 3)
+            O.append(c.pool, c.table[s], 0, k, v * 2.0 ** -30)
+        c.d_pool = dev(c.pool)
+    got, err, want, weights = host(c.attend()), [], [], 0.0
+    for s in range(n):
+        k, v = O.read(c.pool, c.table[s], 0, 300 + rows)
+        q = c.hq_np[s * rows:(s + 1) * rows]
+        want.append(O.attend(k, v, q, 300, 128 ** -0.5)[0])
+        err.append(got[s * rows:(s + 1) * rows] - want[-1])
+        if rows == 100 and not far:
+            p = np.matmul(q.transpose(1, 0, 2), k.transpose(1, 2, 0)) * 128 ** -0.5      # [heads, rows, tokens]
+            p = np.where(np.arange(300 + rows) <= 300 + np.arange(rows)[:, None], p, -np.inf)
+            p = np.exp(p - p.max(-1, keepdims=True))
+            p /= p.sum(-1, keepdims=True)
+            out = want[-1].transpose(1, 0, 2)
+            along = np.matmul(out, v.transpose(1, 2, 0)) - (out ** 2).sum(-1, keepdims=True)
+            weights += (p ** 2 * along ** 2).sum() * 2.0 ** -22 / 3
+    want, err = np.concatenate(want), np.concatenate(err)
+    step = np.exp2(np.maximum(np.floor(np.log2(np.abs(want) + 1e-30)), -14) - 10)
+    sd = np.sqrt((step ** 2 * want ** 2).sum() / 12 + weights) / (want ** 2).sum()
+    assert rows == 100 and not far or 5 * sd < 2.0 ** -17      # else the cut would not show
+    assert abs((err * want).sum() / (want ** 2).sum()) <= 5 * sd
+
+
 @pytest.mark.parametrize("rows,past", [([1, 1, 1], [3000, 10, 555]), ([200, 8], [0, 900])])
 def test_equal_calls_give_equal_bits(rows, past):
     c = Case(rows, past, "bf16", (8, 2), 128, 64, seed=20).fill()
