@@ -618,7 +618,7 @@ int kda_kv_read(const kda_kv_pool* kv, const int32_t* page_table, int32_t max_pa
  * themselves, where outputs have 16 bits.  Prompts of 16-bit types (more than 64 rows of a
  * sequence and cached head) are multiplied in fp16 where the exponents they meet
  * allow it (104..140, and 2, which zeros have): weights are then rounded to 11
- * bits, and a bf16 query, divided by its row's power of two, is off by at most
+ * bits, in both sums alike, and a bf16 query, divided by its row's power of two, is off by at most
  * 2^-25 of the row's largest channel.  From the first other exponent on, a tile's
  * tokens are multiplied as above (up to 1.6 times the time for a whole prompt).
  * The order of the sums depends on the launch's sizes, not on timing: equal calls

@@ -961,7 +961,8 @@ struct ExpRange {
 // 16-bit types take everything in fp16 first: E2M1 times 2^(e - 127) is exact
 // there for e in 104..140, an fp16 query is itself, a bf16 query divided by its
 // row's power of two loses at most 2^-25 of the row's largest channel, and
-// weights, at most 2^15, keep 11 bits down to 2^-21 of the largest.  One product
+// weights, at most 2^15, keep 11 bits down to 2^-21 of the largest (as they are
+// summed, too).  One product
 // for each operand then does what two or three bf16 pieces do.  The exponents
 // are looked at before their tiles are added, two tiles at a time: a block that
 // meets another one goes on from there in bf16 pieces, with the sums that it has
@@ -1307,11 +1308,15 @@ __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tiles_kerne
       for (int k = EACH * i; k < EACH * (i + 1); k += 2) {
         const int b = k / 16, e = k % 16;
         const float w0 = exp2_hw(fmaf(sc[b][e], scale, base)), w1 = exp2_hw(fmaf(sc[b][e + 1], scale, base));
-        sum += w0 + w1;
         uint32_t x[NP];
         if constexpr (HALF) {
-          x[0] = __builtin_bit_cast(uint32_t, h2{static_cast<_Float16>(w0), static_cast<_Float16>(w1)});
+          // the sum takes the weights as they are multiplied: what their
+          // rounding has in common falls out of the quotient
+          const h2 w = {static_cast<_Float16>(w0), static_cast<_Float16>(w1)};
+          sum = __builtin_amdgcn_fdot2(w, h2{1, 1}, sum, false);
+          x[0] = __builtin_bit_cast(uint32_t, w);
         } else {
+          sum += w0 + w1;
           split_weights<NP>(w0, w1, x);
         }
 #pragma unroll

@@ -653,6 +653,29 @@ def test_errors_lean_to_neither_side(rows, far):
     assert abs((err * want).sum() / (want ** 2).sum()) <= 5 * sd
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("rows,past", [(8, 900), (200, 0), (200, 900), (200, 3000)])
+@pytest.mark.parametrize("what", ["equal scores", "random"])
+def test_equal_values_come_out_as_they_are(dtype, rows, past, what):
+    # All values are 1.  Both sums take the same weights (few rows: to 2^-16 of
+    # them), so their quotient is 1 within (T + 64) 2^-24 + 2^-23 + 2^-16, T the tokens:
+    # less than the 2^-12 to fp16's next border below 1 for T < 3500.
+    # Equal scores: behind a first tile of 64 tokens, weights of 2^14 (1 + 0.45 2^-10),
+    # which all lose 0.45 2^-10 when rounded to fp16, nearly a step of the output.
+    c = Case([rows], [past], dtype, (2, 1), 64, 16, seed=38, joint=False).fill()
+    k, _ = O.read(c.pool, c.table[0], 0, past + rows)
+    scale = 0.125
+    if what == "equal scores":
+        c.q.zero_()
+        c.q[:, :, 0] = 1
+        k[:] = 0
+        k[64:, :, 0] = 1
+        scale = (7 + np.log2(1 + 0.45 / 1024)) * np.log(2)
+    O.append(c.pool, c.table[0], 0, k, np.ones_like(k))
+    c.d_pool = dev(c.pool)
+    assert bool((c.attend(scale=scale) == 1).all())
+
+
 @pytest.mark.parametrize("rows,past", [([1, 1, 1], [3000, 10, 555]), ([200, 8], [0, 900])])
 def test_equal_calls_give_equal_bits(rows, past):
     c = Case(rows, past, "bf16", (8, 2), 128, 64, seed=20).fill()
