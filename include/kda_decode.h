@@ -650,7 +650,8 @@ size_t kda_kv_attend_workspace(const kda_kv_pool* kv, int32_t max_pages, int32_t
  * cu_seqlens that descend or leave [0, n_tokens], a negative length or one
  * that max_pages cannot hold; SLOT for a page that is out of range, or one that
  * takes new tokens and appears twice among the pages in use (pages before a
- * sequence's first new token may be shared).  CPU only.
+ * sequence's first new token may be shared).  ARG also when host memory does not
+ * hold a list of the written pages.  CPU only.
  */
 int kda_kv_validate(const kda_kv_pool* kv, const int32_t* page_table_host, int32_t max_pages,
                     const int32_t* cu_seqlens_host, const int32_t* cache_lens_host, int32_t n_seq,

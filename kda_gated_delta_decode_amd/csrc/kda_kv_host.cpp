@@ -2,6 +2,7 @@
 // checks, sizes, table validation and the split of an attention launch.
 // Makes no HIP call, so every refusal can be exercised without a GPU.
 #include <cstdint>
+#include <new>
 #include <unordered_map>
 
 #include "kda_kv.h"
@@ -127,26 +128,30 @@ int kda_kv_validate(const kda_kv_pool* kv, const int32_t* page_table_host, int32
     if (static_cast<int64_t>(cache_lens_host[s]) + cu_seqlens_host[s + 1] - cu_seqlens_host[s] > cover)
       return KDA_ERR_ARG;
   }
-  // pages that hold a sequence's tokens exist; a page that takes new tokens
-  // belongs to that sequence alone (pages before it may be shared)
-  std::unordered_map<int32_t, int64_t> writer;  // page -> s * max_pages + index
-  for (int pass = 0; pass < 2; ++pass)
-    for (int32_t s = 0; s < n_seq; ++s) {
-      const int32_t n = cu_seqlens_host[s + 1] - cu_seqlens_host[s];
-      const int64_t used = (static_cast<int64_t>(cache_lens_host[s]) + n + kv->page_tokens - 1) / kv->page_tokens;
-      const int64_t first_new = cache_lens_host[s] / kv->page_tokens;
-      for (int64_t i = 0; i < used; ++i) {
-        const int64_t at = static_cast<int64_t>(s) * max_pages + i;
-        const int32_t page = page_table_host[at];
-        if (page < 0 || page >= kv->n_pages) return KDA_ERR_SLOT;
-        const bool written = n > 0 && i >= first_new;
-        if (pass == 0 && written && !writer.emplace(page, at).second) return KDA_ERR_SLOT;
-        if (pass == 1) {
-          const auto it = writer.find(page);
-          if (it != writer.end() && it->second != at) return KDA_ERR_SLOT;
+  try {
+    // pages that hold a sequence's tokens exist; a page that takes new tokens
+    // belongs to that sequence alone (pages before it may be shared)
+    std::unordered_map<int32_t, int64_t> writer;  // page -> s * max_pages + index
+    for (int pass = 0; pass < 2; ++pass)
+      for (int32_t s = 0; s < n_seq; ++s) {
+        const int32_t n = cu_seqlens_host[s + 1] - cu_seqlens_host[s];
+        const int64_t used = (static_cast<int64_t>(cache_lens_host[s]) + n + kv->page_tokens - 1) / kv->page_tokens;
+        const int64_t first_new = cache_lens_host[s] / kv->page_tokens;
+        for (int64_t i = 0; i < used; ++i) {
+          const int64_t at = static_cast<int64_t>(s) * max_pages + i;
+          const int32_t page = page_table_host[at];
+          if (page < 0 || page >= kv->n_pages) return KDA_ERR_SLOT;
+          const bool written = n > 0 && i >= first_new;
+          if (pass == 0 && written && !writer.emplace(page, at).second) return KDA_ERR_SLOT;
+          if (pass == 1) {
+            const auto it = writer.find(page);
+            if (it != writer.end() && it->second != at) return KDA_ERR_SLOT;
+          }
         }
       }
-    }
+  } catch (const std::bad_alloc&) {  // `writer` has one entry a written page
+    return KDA_ERR_ARG;
+  }
   return KDA_OK;
 }
 

@@ -354,3 +354,45 @@ int main() {
     assert b.returncode == 0, b.stderr
     r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0 and "kv host checks ok" in r.stdout, r.stdout + r.stderr
+
+
+def test_validate_without_host_memory(tmp_path):
+    """The table check's own memory runs out: an error, and no exception
+    through the C entry."""
+    if shutil.which("g++") is None:
+        pytest.skip("g++ not available")
+    src = tmp_path / "oom.cpp"
+    src.write_text(r'''
+#include <cstdio>
+#include <cstdlib>
+#include <new>
+#include "kda_kv.h"
+static int left = 1 << 30;
+void* operator new(size_t n) {
+  if (left-- <= 0) throw std::bad_alloc();
+  return std::malloc(n);
+}
+void operator delete(void* p) noexcept { std::free(p); }
+void operator delete(void* p, size_t) noexcept { std::free(p); }
+int main() {
+  char dummy[16];
+  kda_kv_pool kv{dummy, 64, 16, 2, 64};
+  int table[64], cu[2] = {0, 64 * 16}, lens[1] = {0};
+  for (int i = 0; i < 64; ++i) table[i] = i;
+  if (kda_kv_validate(&kv, table, 64, cu, lens, 1, 64 * 16) != KDA_OK) return 1;
+  for (int n = 0; n < 40; ++n) {
+    left = n;
+    if (kda_kv_validate(&kv, table, 64, cu, lens, 1, 64 * 16) != KDA_ERR_ARG) return 2;
+  }
+  std::printf("no exception\n");
+  return 0;
+}
+''')
+    exe = tmp_path / "oom"
+    csrc = os.path.join(ROOT, "kda_gated_delta_decode_amd", "csrc")
+    b = subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Wextra", "-Werror", "-I", os.path.join(ROOT, "include"),
+                        "-I", csrc, str(src), os.path.join(csrc, "kda_kv_host.cpp"), "-o", str(exe)],
+                       capture_output=True, text=True)
+    assert b.returncode == 0, b.stderr
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and "no exception" in r.stdout, (r.returncode, r.stdout + r.stderr)
