@@ -88,10 +88,21 @@ struct KvPlan {
   int32_t waves;      // of a workgroup
 };
 
+// Tiles of rows of a plan, over sequences and cached heads: a workgroup for each
+// and every split.
+inline int64_t kv_tiles(const KvPlan& p, int32_t n_seq, int32_t H) {
+  return (p.slots > 0 ? p.slots : static_cast<int64_t>(n_seq) * p.row_tiles) * H;
+}
+
 KvPlan kv_plan(int32_t H, int32_t D, int32_t n_seq, int64_t n_tokens, int32_t max_rows,
                int64_t max_kv_len, int32_t q_heads, kda_dtype dtype);
 
 // Checks shared by the entry points, in the documented order.
 int kv_check(const kda_kv_pool* kv, int32_t max_pages, int32_t n_seq, int64_t n_tokens);
+
+// What the attention asks of its numbers, and the bytes of an element (0: no type).
+int kv_type_bytes(kda_dtype dtype);
+int kv_check_attend(const kda_kv_pool* kv, int64_t n_tokens, int32_t max_rows, int64_t max_kv_len, int32_t q_heads,
+                    kda_dtype dtype);
 
 }  // namespace kda

@@ -1501,8 +1501,6 @@ __global__ __launch_bounds__(256) void kda_kv_join_kernel(KvAttendArgs a, int ti
 
 bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-int type_bytes(kda_dtype d) { return d == KDA_F32 ? 4 : d == KDA_F16 || d == KDA_BF16 ? 2 : 0; }
-
 KvTables make_tables(const kda_kv_pool* kv, const int32_t* page_table, int32_t max_pages, const int32_t* cu,
                      const int32_t* past, int32_t n_seq, int64_t n_tokens) {
   KvTables t;
@@ -1557,7 +1555,7 @@ extern "C" int kda_kv_append(const kda_kv_pool* kv, const int32_t* page_table, i
                              kda_dtype dtype, void* stream) {
   const int rc = kv_check(kv, max_pages, n_seq, n_tokens);
   if (rc != KDA_OK) return rc;
-  const int size = type_bytes(dtype);
+  const int size = kv_type_bytes(dtype);
   if (size == 0) return KDA_ERR_DTYPE_REFUSED;
   if (q_heads < 0 || q_heads > 65535 || n_positions < 0 || (interleaved != 0 && interleaved != 1)) return KDA_ERR_ARG;
   if (rot_dim < 0 || rot_dim > kv->D || rot_dim % 16 != 0) return KDA_ERR_SHAPE;
@@ -1614,7 +1612,7 @@ extern "C" int kda_kv_read(const kda_kv_pool* kv, const int32_t* page_table, int
                            void* stream) {
   const int rc = kv_check(kv, max_pages, n_seq, n_tokens);
   if (rc != KDA_OK) return rc;
-  const int size = type_bytes(dtype);
+  const int size = kv_type_bytes(dtype);
   if (size == 0) return KDA_ERR_DTYPE_REFUSED;
   if (n_seq == 0 || n_tokens == 0) return KDA_OK;
   if (page_table == nullptr || cu_seqlens == nullptr || first == nullptr || (k_out == nullptr && v_out == nullptr))
@@ -1649,14 +1647,11 @@ extern "C" int kda_kv_attend(const kda_kv_pool* kv, const int32_t* page_table, i
                              int64_t q_stride, void* out, int32_t n_seq, int64_t n_tokens, int32_t max_rows,
                              int64_t max_kv_len, int32_t q_heads, kda_dtype dtype, float scale, void* workspace,
                              size_t workspace_bytes, void* stream) {
-  const int rc = kv_check(kv, max_pages, n_seq, n_tokens);
+  int rc = kv_check(kv, max_pages, n_seq, n_tokens);
+  if (rc == KDA_OK) rc = kv_check_attend(kv, n_tokens, max_rows, max_kv_len, q_heads, dtype);
   if (rc != KDA_OK) return rc;
-  const int size = type_bytes(dtype);
-  if (size == 0) return KDA_ERR_DTYPE_REFUSED;
-  if (q_heads < 1 || q_heads > 65535 || q_heads % kv->H != 0) return KDA_ERR_SHAPE;
-  if (max_rows < 0 || max_kv_len < 0 || !std::isfinite(scale)) return KDA_ERR_ARG;
-  // a row index is token * group + head within the group
-  if (n_tokens * (q_heads / kv->H) > INT32_MAX / 4) return KDA_ERR_ARG;
+  if (!std::isfinite(scale)) return KDA_ERR_ARG;
+  const int size = kv_type_bytes(dtype);
   if (n_seq == 0 || n_tokens == 0) return KDA_OK;
   if (page_table == nullptr || cu_seqlens == nullptr || cache_lens == nullptr || q == nullptr || out == nullptr)
     return KDA_ERR_NULL;
@@ -1688,7 +1683,7 @@ extern "C" int kda_kv_attend(const kda_kv_pool* kv, const int32_t* page_table, i
   a.sign = scale < 0.0f ? -1.0f : 1.0f;
   a.part = static_cast<float*>(workspace);
   a.part_ml = a.part == nullptr ? nullptr : a.part + static_cast<int64_t>(p.n_splits) * n_tokens * q_heads * kv->D;
-  const int64_t tiles = (p.slots > 0 ? p.slots : static_cast<int64_t>(n_seq) * p.row_tiles) * kv->H;
+  const int64_t tiles = kv_tiles(p, n_seq, kv->H);
   if (tiles * p.n_splits > kKvMaxBlocks) return KDA_ERR_ARG;  // (many splits: few tiles, so the join's blocks fit too)
   hipStream_t st = static_cast<hipStream_t>(stream);
   return status(by_type(dtype, kv->D, [&](auto t, auto d) {

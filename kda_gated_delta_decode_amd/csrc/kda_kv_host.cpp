@@ -21,6 +21,20 @@ int kv_check(const kda_kv_pool* kv, int32_t max_pages, int32_t n_seq, int64_t n_
   return KDA_OK;
 }
 
+int kv_type_bytes(kda_dtype dtype) {
+  return dtype == KDA_F32 ? 4 : dtype == KDA_F16 || dtype == KDA_BF16 ? 2 : 0;
+}
+
+int kv_check_attend(const kda_kv_pool* kv, int64_t n_tokens, int32_t max_rows, int64_t max_kv_len, int32_t q_heads,
+                    kda_dtype dtype) {
+  if (kv_type_bytes(dtype) == 0) return KDA_ERR_DTYPE_REFUSED;
+  if (q_heads < 1 || q_heads > 65535 || q_heads % kv->H != 0) return KDA_ERR_SHAPE;
+  if (max_rows < 0 || max_kv_len < 0) return KDA_ERR_ARG;
+  // a row index is token * group + head within the group
+  if (n_tokens * (q_heads / kv->H) > INT32_MAX / 4) return KDA_ERR_ARG;
+  return KDA_OK;
+}
+
 KvPlan kv_plan(int32_t H, int32_t D, int32_t n_seq, int64_t n_tokens, int32_t max_rows,
                int64_t max_kv_len, int32_t q_heads, kda_dtype dtype) {
   (void)D;
@@ -104,11 +118,12 @@ size_t kda_kv_pool_bytes(int32_t n_pages, int32_t page_tokens, int32_t H, int32_
 size_t kda_kv_attend_workspace(const kda_kv_pool* kv, int32_t max_pages, int32_t n_seq, int64_t n_tokens,
                                int32_t max_rows, int64_t max_kv_len, int32_t q_heads, kda_dtype dtype) {
   if (kv_check(kv, max_pages, n_seq, n_tokens) != KDA_OK) return 0;
-  if (q_heads < 1 || q_heads % kv->H != 0 || max_rows < 0 || max_kv_len < 0) return 0;
+  if (kv_check_attend(kv, n_tokens, max_rows, max_kv_len, q_heads, dtype) != KDA_OK) return 0;
+  if (n_seq == 0 || n_tokens == 0) return 0;
   const int64_t cover = static_cast<int64_t>(max_pages) * kv->page_tokens;
   const KvPlan p = kv_plan(kv->H, kv->D, n_seq, n_tokens, max_rows,
                            max_kv_len > 0 && max_kv_len < cover ? max_kv_len : cover, q_heads, dtype);
-  if (p.n_splits == 1) return 0;
+  if (p.n_splits == 1 || kv_tiles(p, n_seq, kv->H) * p.n_splits > kKvMaxBlocks) return 0;
   return static_cast<size_t>(p.n_splits) * n_tokens * q_heads * (kv->D + 2) * sizeof(float);
 }
 

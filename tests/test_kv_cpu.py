@@ -220,6 +220,21 @@ def test_workspace_sizes():
     assert size(n_seq=4096, n_tokens=4096, kv=4096) == 0      # enough sequences fill the chip by themselves
 
 
+def test_no_workspace_for_what_the_attention_refuses():
+    # by type, heads, rows or workgroups; and a size for what it takes
+    for over in (dict(dtype=3), dict(dtype=-1), dict(heads=65536), dict(heads=65536 * 2), dict(n_tokens=1 << 28),
+                 dict(n_tokens=0), dict(n_seq=0), dict(n_seq=1 << 22, n_tokens=1 << 22, H=1)):
+        C = cache(H=over.get("H", 2))
+        kw = dict(max_pages=1000, max_kv=16000, heads=4, dtype=B.KDA_F32, n_seq=1, n_tokens=3, max_rows=3)
+        kw.update({k: v for k, v in over.items() if k != "H"})
+        need = B.library().kda_kv_attend_workspace(ctypes.byref(C), kw["max_pages"], kw["n_seq"], kw["n_tokens"],
+                                                   kw["max_rows"], kw["max_kv"], kw["heads"], kw["dtype"])
+        assert need == 0, over
+        rc = attend(C, qs=65536 * 2 * 128, ws=None, ws_bytes=0, **kw)
+        assert (rc == B.KDA_OK) == (kw["n_seq"] * kw["n_tokens"] == 0), over
+    assert B.library().kda_kv_attend_workspace(ctypes.byref(cache()), 1000, 1, 3, 3, 16000, 4, B.KDA_F32) > 0
+
+
 # -- host tables ------------------------------------------------------------
 
 def valid(table, cu, lens, n_tokens, **pool):
