@@ -9,13 +9,14 @@
 
 namespace kda {
 
-static bool page_tokens_ok(int32_t p) { return p == 16 || p == 32 || p == 64 || p == 128 || p == 256; }
+static bool kv_shape_ok(int32_t n_pages, int32_t P, int32_t H, int32_t D) {
+  return (D == 64 || D == 128) && (P == 16 || P == 32 || P == 64 || P == 128 || P == 256) && H >= 1 &&
+         H <= kKvMaxHeads && n_pages >= 1;
+}
 
 int kv_check(const kda_kv_pool* kv, int32_t max_pages, int32_t n_seq, int64_t n_tokens) {
   if (kv == nullptr || kv->base == nullptr) return KDA_ERR_NULL;
-  if ((kv->D != 64 && kv->D != 128) || !page_tokens_ok(kv->page_tokens) || kv->H < 1 ||
-      kv->H > kKvMaxHeads || kv->n_pages < 1)
-    return KDA_ERR_SHAPE;
+  if (!kv_shape_ok(kv->n_pages, kv->page_tokens, kv->H, kv->D)) return KDA_ERR_SHAPE;
   if (n_seq < 0 || n_tokens < 0 || n_tokens > INT32_MAX || max_pages < 1) return KDA_ERR_ARG;
   if (static_cast<int64_t>(max_pages) * kv->page_tokens > kKvMaxPositions) return KDA_ERR_ARG;
   return KDA_OK;
@@ -111,7 +112,7 @@ using namespace kda;
 extern "C" {
 
 size_t kda_kv_pool_bytes(int32_t n_pages, int32_t page_tokens, int32_t H, int32_t D) {
-  if ((D != 64 && D != 128) || !page_tokens_ok(page_tokens) || n_pages < 0 || H < 0) return 0;
+  if (!kv_shape_ok(n_pages, page_tokens, H, D)) return 0;
   return static_cast<size_t>(n_pages) * H * kv_block_bytes(page_tokens, D);
 }
 

@@ -267,6 +267,12 @@ def test_pool_sizes():
     assert np.prod(K.kv_pool_shape(7, 8, 128, 64)) == B.kda_kv_pool_bytes(7, 128, 8, 64)
 
 
+def test_no_size_for_shapes_that_are_refused():
+    for shape in ((7, 128, 4097, 128), (7, 128, 0, 128), (0, 128, 8, 128), (7, 128, 1 << 30, 64)):
+        assert B.kda_kv_pool_bytes(*shape) == 0, shape
+    assert B.kda_kv_pool_bytes((1 << 31) - 1, 256, 4096, 128) == ((1 << 31) - 1) * 256 * 4096 * 136
+
+
 def test_the_binding_refuses_what_is_not_on_a_gpu():
     torch = pytest.importorskip("torch")
     pool = torch.zeros(K.kv_pool_shape(2, 1, 16, 64), dtype=torch.uint8)
