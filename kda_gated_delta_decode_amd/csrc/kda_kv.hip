@@ -1096,7 +1096,7 @@ __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tiles_kerne
                       static_cast<_Float16>(__uint_as_float(w & 0xFFFF0000u) * down)};
         qf[0][ks][k] = __builtin_bit_cast(uint32_t, y);
       }
-    scale = fminf(fmaxf(scale * exp_scale(ex), 0x1p-126f), FLT_MAX);  // as a.scale
+    scale = fminf(fmaxf(scale * exp_scale(ex), 0x1p-149f), FLT_MAX);  // as a.scale
   }
   ExpRange seen;
 
@@ -1677,9 +1677,9 @@ extern "C" int kda_kv_attend(const kda_kv_pool* kv, const int32_t* page_table, i
   a.row_tiles = p.row_tiles;
   a.slots = p.slots;
   // Above zero, so that a masked score (-infinity) times it is what it was
-  // (2^-126 times any score leaves its weight 1), and finite, so that a score of
+  // (2^-149 times any score leaves its weight 1), and finite, so that a score of
   // zero is.
-  a.scale = std::fmin(std::fmax(std::fabs(scale) * 1.44269504088896340736f, 0x1p-126f), FLT_MAX);
+  a.scale = std::fmin(std::fmax(std::fabs(scale) * 1.44269504088896340736f, 0x1p-149f), FLT_MAX);
   a.sign = scale < 0.0f ? -1.0f : 1.0f;
   a.part = static_cast<float*>(workspace);
   a.part_ml = a.part == nullptr ? nullptr : a.part + static_cast<int64_t>(p.n_splits) * n_tokens * q_heads * kv->D;

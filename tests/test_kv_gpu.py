@@ -412,6 +412,22 @@ def test_a_scale_near_the_largest_number(dtype, rows):
     c.check(c.attend(scale=3.3e38), scale=0.0)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows", [2, 80])
+@pytest.mark.parametrize("scale", [0.0, 1e-43])
+def test_a_scale_of_nothing_over_the_largest_scores(dtype, rows, scale):
+    # scores of up to 3 * 2^125: times 0 they are 0, times 1e-43 below 2^-15
+    c = Case([rows], [50], dtype, (2, 1), 64, 16, seed=39, joint=False)
+    k = np.zeros((50 + rows, 1, 64))
+    k[:, 0, 0] = np.arange(50 + rows) % 7 - 3
+    O.append(c.pool, c.table[0], 0, k, c.rng.standard_normal(k.shape))
+    c.d_pool = dev(c.pool)
+    c.q.zero_()
+    c.q[:, :, 0] = 2.0 ** 125
+    c.hq_np = host(c.q)
+    c.check(c.attend(scale=scale), scale=scale)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("rows,past", [(2, 50), (80, 50), (2, 3000), (80, 3000)])
 @pytest.mark.parametrize("what", ["largest", "all", "query"])
