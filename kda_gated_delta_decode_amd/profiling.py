@@ -34,16 +34,22 @@ COPY_KERNEL = "kda_copy_probe_kernel"
 DECODE_KERNEL = "kda_decode_tile"
 
 
-# headers a kernel's code and launch shapes also come from
+# files a kernel's code and launch shapes also come from
 KERNEL_HEADERS = ("kda_launch.h", "kda_device.h", "kda_internal.h")
+MORE_SOURCES = {"kda_kv.hip": ("kda_kv.h", "kda_kv_host.cpp")}
+
+
+def kernel_sources(src: str) -> tuple:
+    """The csrc files beside a kernel source file that decide what it runs."""
+    return KERNEL_HEADERS + MORE_SOURCES.get(os.path.basename(src), ())
 
 
 def kernel_hash(src: str = KERNEL_SRC) -> str:
-    """sha256[:16] of a kernel source file and the csrc headers it is built
-    with (device helpers, launch-shape defaults): a summary taken on other
-    sources no longer describes the kernel that runs."""
+    """sha256[:16] of a kernel source file and the csrc files it is built and
+    launched with (device helpers, launch-shape defaults and plans): a summary
+    taken on other sources no longer describes the kernel that runs."""
     h = hashlib.sha256()
-    for path in [src] + [os.path.join(HERE, "csrc", n) for n in KERNEL_HEADERS]:
+    for path in [src] + [os.path.join(HERE, "csrc", n) for n in kernel_sources(src)]:
         with open(path, "rb") as f:
             h.update(f.read())
     return h.hexdigest()[:16]
@@ -178,7 +184,7 @@ def trace(args):
     lines += args.command + ["```", "", "Summary written by (from the repository root):", "", "```",
                              self_command(), "```", "",
                              "Kernel sources (%s with %s) sha256[:16] at the time: `%s`." % (
-                                 args.source, ", ".join(KERNEL_HEADERS),
+                                 args.source, ", ".join(kernel_sources(args.source)),
                                  kernel_hash(os.path.join(HERE, "csrc", args.source))), "",
                              "## rocprofv3 kernel stats (all dispatches of the run)", "",
                              "| Kernel | Calls | Average µs | Min µs | Max µs |", "|---|---|---|---|---|"]

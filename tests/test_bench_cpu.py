@@ -59,3 +59,18 @@ def test_cpu_baseline_reports_the_oracle_on_a_bounded_sample():
     other = res["other_configs"]
     assert set(other) == {"batched_f32", "batched_f16", "spec_verify_f16", "layers69_f32_one_pass"}
     assert all(v["us_per_step"] > 0 and v["state_GB/s"] > 0 for v in other.values())
+
+
+def test_kernel_hash_covers_the_launch_plan_of_the_cache(tmp_path, monkeypatch):
+    # the 4-bit cache's block layout and split plan lie outside its kernel file
+    import shutil
+    from kda_gated_delta_decode_amd import profiling
+    shutil.copytree(os.path.join(profiling.HERE, "csrc"), str(tmp_path / "csrc"))
+    monkeypatch.setattr(profiling, "HERE", str(tmp_path))
+    src = str(tmp_path / "csrc" / "kda_kv.hip")
+    seen = {profiling.kernel_hash(src)}
+    for name in ("kda_kv.h", "kda_kv_host.cpp"):
+        with open(str(tmp_path / "csrc" / name), "a") as f:
+            f.write("// another plan\n")
+        seen.add(profiling.kernel_hash(src))
+    assert len(seen) == 3
