@@ -48,7 +48,7 @@
 extern "C" {
 #endif
 
-#define KDA_ABI_VERSION 11  /* 11: kda_launch_opts.g_raw; 10: kda_rows_probe tile shapes; 9: kda_decode_step_conv_noalloc; 8: kda_decode_step_conv_ws; 7: kda_rows_probe; 6: kda_bw_probe and kda_tile_probe; 5: KDA_ROWS_MATRIX */
+#define KDA_ABI_VERSION 11  /* 11: kda_launch_opts.g_raw, later the kda_kv_* functions (new symbols only); 10: kda_rows_probe tile shapes; 9: kda_decode_step_conv_noalloc; 8: kda_decode_step_conv_ws; 7: kda_rows_probe; 6: kda_bw_probe and kda_tile_probe; 5: KDA_ROWS_MATRIX */
 
 /* Head dimensions this build supports (the Kimi-K3 KDA layer shape). */
 #define KDA_HEAD_K 128
@@ -483,9 +483,9 @@ int kda_prefill_validate(const kda_pool* pool, const int32_t* init_slot_ids_host
 
 /* ------------------------------------------------------------------------
  * The paged 4-bit key/value cache: what the softmax-attention layers of a
- * hybrid model keep beside the KDA layers' states.  Its memory is what a
- * narrower state pool is traded for (ROCm/ATOM PR #2945, Performance: an
- * fp16 state pool leaves room for 45% more cache blocks).
+ * hybrid model keep beside the KDA layers' states, for grouped or single query
+ * heads.  (The blocks that an fp16 state pool makes room for in ROCm/ATOM
+ * PR #2945, Performance, are a latent cache's, another kind.)
  *
  * Format: OCP microscaling MXFP4.  A value is an E2M1 number (0, 0.5, 1, 1.5,
  * 2, 3, 4, 6 and their negatives; the code's high bit is the sign) times

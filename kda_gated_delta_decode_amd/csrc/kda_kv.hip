@@ -956,7 +956,10 @@ struct ExpRange {
 // A wave's matrix and vector work overlap: the scores of the next tile are
 // multiplied while this one's weights are formed, and the codes of later
 // tiles are turned while the values are multiplied.  Keys are therefore
-// staged one tile further ahead than values; one barrier a tile.
+// staged one tile further ahead than values; one barrier a tile.  Step i reads
+// key buffer (i + 1) % 2 and value buffer i % 2 and writes the two others, which
+// were last read before the barrier that ends step i - 1; the first tile's scores
+// have a barrier of their own.
 //
 // 16-bit types take everything in fp16 first: E2M1 times 2^(e - 127) is exact
 // there for e in 104..140, an fp16 query is itself, a bf16 query divided by its

@@ -38,7 +38,7 @@ int kv_check_attend(const kda_kv_pool* kv, int64_t n_tokens, int32_t max_rows, i
 
 KvPlan kv_plan(int32_t H, int32_t D, int32_t n_seq, int64_t n_tokens, int32_t max_rows,
                int64_t max_kv_len, int32_t q_heads, kda_dtype dtype) {
-  (void)D;
+  (void)D;  // one plan for both: its figures are of D = 128, those of four prompt chunks of D = 64
   KvPlan p;
   const int64_t rows = static_cast<int64_t>(max_rows < n_tokens ? max_rows : n_tokens) * (q_heads / H);
   // 128-row tiles share a tile's turned codes through LDS; below that every
