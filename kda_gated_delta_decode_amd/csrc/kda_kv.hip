@@ -974,9 +974,11 @@ struct ExpRange {
 // (8192 bf16 rows with one such token near the front: 720 us, fp16 820; near the
 // end 530).  Poisoned keys are NaN in fp16 too.
 //
-// Bound by the matrix cores and the vector work beside them: 8192 bf16 rows of 32
-// query heads 536 us, 1026 TFLOP/s of the 1211 that a large bf16 matrix product
-// reaches (829 us with two bf16 pieces for a weight, one tile after the other).
+// Bound by how much of the vector work two waves a SIMD hide behind the products
+// (the matrix cores are busy 48% of the cycles, waves wait 25% of theirs): 8192 bf16
+// rows of 32 query heads 536 us, 1026 TFLOP/s of the 1211 that a large bf16 matrix
+// product reaches (829 us with two bf16 pieces for a weight, one tile after the
+// other).
 template <int DT, int D>
 __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tiles_kernel(KvAttendArgs a) {
   constexpr int KT = 64;            // tokens of a tile
