@@ -692,6 +692,30 @@ def test_equal_values_come_out_as_they_are(dtype, rows, past, what):
     assert bool((c.attend(scale=scale) == 1).all())
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("rows", [4, 80])
+@pytest.mark.parametrize("first", [0.0, 1.0])
+def test_many_weights_far_below_the_largest(dtype, rows, first):
+    # One token, and 60,000 of 2^-22.5 of its weight in the same split (a prompt's
+    # fp16 holds them as subnormals, 362 of 2^-24 for 362.04).  With values 1 but for
+    # the first, which is 0 or 1, the result is S / (1 + S), S = 0.0101 (T 2^-22.5), or
+    # 1: off by 2^-13 of S, half a step of the output (2^-8 at most) and, of sums over
+    # T equal terms in fp32, T 2^-24 of S or of 1 at most.
+    past = 60000
+    c = Case([rows], [past], dtype, (2, 1), 64, 256, seed=40, joint=False)
+    pool, one = c.d_pool, torch.zeros((past + rows, 1, 64), dtype=torch.float32, device="cuda")
+    k, v = one.clone(), one + 1
+    k[0, 0, 0], v[0] = 1, first
+    B.kda_kv_append(pool, c.d_table, i32([0, past + rows]), i32([0]), k, v)
+    c.q.zero_()
+    c.q[:, :, 0] = 1
+    got = host(c.attend(max_kv_len=64, scale=22.5 * np.log(2)))
+    s = (past + np.arange(rows))[:, None, None] * 2.0 ** -22.5
+    want = (first + s) / (1 + s)
+    off = 2.0 ** -13 + 60100 * 2.0 ** -24
+    assert (np.abs(got - want) <= (off * s if first == 0 else off) + HALF_STEP[dtype] * want).all()
+
+
 @pytest.mark.parametrize("rows,past", [([1, 1, 1], [3000, 10, 555]), ([200, 8], [0, 900])])
 def test_equal_calls_give_equal_bits(rows, past):
     c = Case(rows, past, "bf16", (8, 2), 128, 64, seed=20).fill()
