@@ -48,7 +48,7 @@
 extern "C" {
 #endif
 
-#define KDA_ABI_VERSION 11  /* 11: kda_launch_opts.g_raw, later the kda_kv_* functions (new symbols only); 10: kda_rows_probe tile shapes; 9: kda_decode_step_conv_noalloc; 8: kda_decode_step_conv_ws; 7: kda_rows_probe; 6: kda_bw_probe and kda_tile_probe; 5: KDA_ROWS_MATRIX */
+#define KDA_ABI_VERSION 11  /* 11: kda_launch_opts.g_raw, later the kda_kv_* functions and those for trees of drafted tokens (new symbols only); 10: kda_rows_probe tile shapes; 9: kda_decode_step_conv_noalloc; 8: kda_decode_step_conv_ws; 7: kda_rows_probe; 6: kda_bw_probe and kda_tile_probe; 5: KDA_ROWS_MATRIX */
 
 /* Head dimensions this build supports (the Kimi-K3 KDA layer shape). */
 #define KDA_HEAD_K 128
@@ -56,11 +56,15 @@ extern "C" {
 /* Rows (tokens) one request may chain in one launch: 1 + up to 7 drafts. */
 #define KDA_MAX_ROWS 8
 
+/* Nodes of one request's tree of drafted tokens. */
+#define KDA_MAX_NODES 64
+
 /* Element type of a state pool (or of the tensors of the kda_kv_* functions). */
 typedef enum kda_dtype {
   KDA_F32 = 0,
   KDA_F16 = 1,
-  KDA_BF16 = 2 /* refused for state pools; a type of the kda_kv_* functions' tensors */
+  KDA_BF16 = 2 /* refused for state pools; a type of the kda_kv_* functions' tensors
+                  and of kda_verify_drafts' probabilities */
 } kda_dtype;
 
 typedef enum kda_status {
@@ -70,7 +74,8 @@ typedef enum kda_status {
   KDA_ERR_DTYPE_MISMATCH = 3, /* state_dtype differs from the pool's dtype */
   KDA_ERR_SHAPE = 4,          /* K or V != 128, H outside [1, 65535], n_slots < 1;
                                  or a key/value cache's shape */
-  KDA_ERR_ROWS = 5,           /* rows per request outside [1, KDA_MAX_ROWS] */
+  KDA_ERR_ROWS = 5,           /* rows per request outside [1, KDA_MAX_ROWS], or a
+                                 tree's outside [0, KDA_MAX_NODES] */
   KDA_ERR_SLOT = 6,           /* slot id out of range or repeated, or more
                                  rows than slots */
   KDA_ERR_ALIGN = 7,          /* a device pointer is not 16-byte aligned */
@@ -656,6 +661,188 @@ size_t kda_kv_attend_workspace(const kda_kv_pool* kv, int32_t max_pages, int32_t
 int kda_kv_validate(const kda_kv_pool* kv, const int32_t* page_table_host, int32_t max_pages,
                     const int32_t* cu_seqlens_host, const int32_t* cache_lens_host, int32_t n_seq,
                     int64_t n_tokens);
+
+/* ------------------------------------------------------------------------
+ * Trees of drafted tokens.  A speculative step may offer a target model more
+ * than one continuation: the drafted tokens of a request form a tree, each
+ * node a token that follows its parent's.  (The pages' own drafts are chains,
+ * 1 + 7 rows a request, ROCm/ATOM PR #2945, Method; kda_decode_step takes
+ * those, with a snapshot for each row.)  One step over a tree is
+ *   kda_kv_append_at, kda_kv_attend_tree   in every softmax-attention layer
+ *   kda_decode_tree                        in every KDA layer
+ *   kda_verify_drafts                      once, on the target's probabilities
+ *   kda_kv_keep, kda_decode_path           the accepted path enters the caches
+ *                                          and the states
+ *
+ * The tables (device int32):
+ *  cu_seqlens  [n_req + 1], non-decreasing: request r owns nodes
+ *              cu_seqlens[r] .. cu_seqlens[r + 1] - 1 of the launch, up to
+ *              KDA_MAX_NODES of them (none: nothing is done for it).  A request
+ *              whose entries are out of range is skipped.
+ *  parents     [n_tokens]: the parent of the request's node i, counted from the
+ *              request's first node: -1 (the node follows the context) or a
+ *              node before it, 0 .. i - 1.  Node 0 has -1.  (A chain: i - 1.)
+ *  path        [n_req, max_path], path_lens [n_req]: the accepted nodes, from
+ *              the root down, as kda_verify_drafts writes them; entries behind
+ *              a path's length may hold anything.  max_path in
+ *              [1, KDA_MAX_NODES].
+ * Rows of nodes before the first or behind the last request are left as they
+ * were.  Nothing is allocated or synchronised; launches are captured into
+ * graphs as they are.  Calls on different streams may overlap as long as none
+ * writes what another one reads or writes.
+ */
+
+/*
+ * kda_tree_validate -- host-side check of a step's tables (host copies): ARG
+ * for cu_seqlens that descend or leave [0, n_tokens], and for a parent that is
+ * neither -1 nor before its node; ROWS for a request of more than
+ * KDA_MAX_NODES nodes.  CPU only.
+ */
+int kda_tree_validate(const int32_t* cu_seqlens_host, const int32_t* parents_host, int32_t n_req,
+                      int64_t n_tokens);
+
+/*
+ * kda_kv_append_at -- kda_kv_append with the positions that keys and queries are
+ * turned by given apart from their places.  positions: NULL (then exactly
+ * kda_kv_append), or device int32 [n_tokens], 4-byte aligned: token t is turned
+ * by row positions[t] of cos and sin and stored at cache_lens[s] + i as ever.
+ * A tree's node stands at the context's length plus its depth.  A position
+ * outside [0, n_positions) is treated like a token without a page: not stored,
+ * its q_out rows NaN.  With rot_dim 0 positions are not read.
+ */
+int kda_kv_append_at(const kda_kv_pool* kv, const int32_t* page_table, int32_t max_pages,
+                     const int32_t* cu_seqlens, const int32_t* cache_lens, const void* k, const void* v,
+                     int64_t k_stride, int64_t v_stride, const void* q, int64_t q_stride, void* q_out,
+                     const float* cos, const float* sin, const int32_t* positions, int32_t n_positions,
+                     int32_t rot_dim, int32_t interleaved, int32_t n_seq, int64_t n_tokens, int32_t q_heads,
+                     kda_dtype dtype, void* stream);
+
+/*
+ * kda_kv_attend_tree -- kda_kv_attend for a tree's nodes: node i of sequence s,
+ * cached at position cache_lens[s] + i, sees the cache_lens[s] tokens of the
+ * context, the nodes on its path and itself.  Everything else is
+ * kda_kv_attend's, workspace and precision included (a chain's results are the
+ * same bits); workspace: kda_kv_attend_workspace() bytes for the same
+ * arguments.
+ *  parents   device int32 [n_tokens], 4-byte aligned (see above).
+ *  max_rows  at most KDA_MAX_NODES (else KDA_ERR_ROWS, checked with the counts).
+ * The rows of a sequence of more than KDA_MAX_NODES nodes, or with a parent
+ * that does not lie before its node, are NaN.
+ */
+int kda_kv_attend_tree(const kda_kv_pool* kv, const int32_t* page_table, int32_t max_pages,
+                       const int32_t* cu_seqlens, const int32_t* cache_lens, const int32_t* parents,
+                       const void* q, int64_t q_stride, void* out, int32_t n_seq, int64_t n_tokens,
+                       int32_t max_rows, int64_t max_kv_len, int32_t q_heads, kda_dtype dtype, float scale,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * kda_kv_keep -- moves the cache entries of accepted nodes together: node
+ * path[s][e], cached at position cache_lens[s] + path[s][e], to position
+ * cache_lens[s] + e, for every e < path_lens[s], bytes as they are.  The caller
+ * then counts path_lens[s] more tokens in cache_lens[s].
+ *  path must ascend (a path from the root down does); a path that does not,
+ *  that names a node the sequence does not have, or whose length is outside
+ *  [0, max_path], leaves its sequence as it was.
+ * A token whose source has no page becomes a poisoned one (it reads back as
+ * NaN); one whose destination has none is not moved.  Checks as kda_kv_read's,
+ * with ROWS (max_path) behind the counts.
+ */
+int kda_kv_keep(const kda_kv_pool* kv, const int32_t* page_table, int32_t max_pages,
+                const int32_t* cu_seqlens, const int32_t* cache_lens, const int32_t* path, int32_t max_path,
+                const int32_t* path_lens, int32_t n_seq, int64_t n_tokens, void* stream);
+
+/*
+ * kda_decode_tree -- the recurrence of kda_decode_step over trees: a node starts
+ * from its parent's state (the roots from slot init_slot_ids[r], widened
+ * exactly), is updated by its own q, k, v, g, b, and out receives its read-out.
+ * All states between are fp32 and none is stored: the pool is only read, so a
+ * rejected branch leaves nothing to undo.
+ *  init_slot_ids  device int32 [n_req], may repeat; a request whose slot is
+ *                 out of range has NaN rows.
+ *  q, k, g, v     device fp32 [n_tokens, H, 128]; b device fp32 [n_tokens, H];
+ *  out            device fp32 [n_tokens, H, 128].
+ *  max_nodes      the most nodes of a request, in [0, KDA_MAX_NODES]: it chooses
+ *                 the kernel.  A request with more nodes has NaN rows, as has one
+ *                 with a parent that does not lie before its node.
+ * g <= 0 as everywhere: decays multiply along a path, from the node up.
+ * Checks run in the order: pool NULL, DTYPE_REFUSED, DTYPE_MISMATCH, SHAPE (also
+ * H > 16384), ARG (counts), ROWS (max_nodes), then, for n_req and n_tokens > 0
+ * (either 0 is a valid no-op), NULL, ARG (scale, launch size), ALIGN.
+ */
+int kda_decode_tree(const kda_pool* pool, const int32_t* init_slot_ids, const int32_t* cu_seqlens,
+                    const int32_t* parents, const float* q, const float* k, const float* v,
+                    const float* g, const float* b, float* out, int32_t n_req, int64_t n_tokens,
+                    int32_t max_nodes, kda_dtype state_dtype, float scale, void* stream);
+
+/*
+ * kda_decode_path -- the accepted nodes' updates applied in turn: the state of
+ * slot init_slot_ids[r] takes the k, v, g, b rows of nodes path[r][0],
+ * path[r][1], .. and is stored to slot dst_slot_ids[r] (NULL: back to
+ * init_slot_ids[r]; fp16 pools round to nearest even, once).  A path of length
+ * 0 copies the state.  dst_slot_ids: distinct, and none is another request's
+ * initial slot (kda_prefill_validate checks host copies).  A request with a slot
+ * out of range, a length outside [0, max_path], or a path entry that is not one
+ * of its nodes, is skipped: nothing is stored for it.
+ * Checks as kda_decode_tree's (ROWS: max_path outside [1, KDA_MAX_NODES]; SLOT:
+ * n_req > n_slots, behind it), but only n_req 0 is a no-op; k, v, g and b may be
+ * NULL with n_tokens 0.
+ */
+int kda_decode_path(const kda_pool* pool, const int32_t* init_slot_ids, const int32_t* dst_slot_ids,
+                    const int32_t* cu_seqlens, const int32_t* path, int32_t max_path,
+                    const int32_t* path_lens, const float* k, const float* v, const float* g,
+                    const float* b, int32_t n_req, int64_t n_tokens, kda_dtype state_dtype, void* stream);
+
+/*
+ * kda_verify_drafts -- which drafted tokens are kept, and the token that follows
+ * them, so that every token is distributed as the target's probabilities say
+ * (rejection sampling from given random numbers).
+ *
+ * A request's walk starts at node 0, which is certain, with weights f = the
+ * target's row of node 0 and M = 1.  Its nodes 1, 2, .. are looked at in turn;
+ * node i is tried if its parent is the last accepted node.  With x =
+ * tokens[i], u = accept_rand[i] and q the draft's row of that parent:
+ *   accepted if u q(x) M < f(x): then f = target's row of node i, M = 1;
+ *   else f <- max(f - M q, 0), M <- sum f.
+ * (q: the distribution that each child of that node was drawn from.)  Without
+ * a draft, for children that are chosen and not drawn (the draft's likeliest):
+ *   accepted if u M < f(x); else M <- M - f(x), f(x) <- 0.
+ * Last, the following token is the smallest x with f(x) > 0 and f(0) + .. + f(x)
+ * > sample_rand[r] * (sum f); the last with f(x) > 0 if rounding leaves none;
+ * drawn from the target's row itself if sum f is 0.
+ * All of it in fp64 on the stored probabilities, so that a draw next to a
+ * border is the definition's; an entry that is not above 0 (NaN among them)
+ * counts as 0, and a token outside [0, vocab) has probability 0.
+ *
+ *  target       device [n_tokens, vocab] of dtype (KDA_F32, KDA_F16 or KDA_BF16),
+ *               target_stride (>= vocab) elements from row to row: row i is the
+ *               distribution behind node i.  Not rescaled: acceptance takes the
+ *               rows as normalised.
+ *  draft        NULL, or the same of the draft (draft_stride not read with NULL).
+ *  tokens       device int32 [n_tokens]; node 0's is not read.
+ *  accept_rand  device fp32 [n_tokens], in [0, 1); sample_rand fp32 [n_req].
+ *  path         int32 [n_req, max_path], out: node 0 and the accepted nodes, then
+ *               -1.  A path that fills max_path ends there, and its last node's
+ *               children are not tried.
+ *  path_lens    int32 [n_req], out: at least 1; 0 for a request without nodes,
+ *               or one that is skipped (its path -1), whose tree is bad, or which
+ *               has more than KDA_MAX_NODES nodes.
+ *  next_tokens  int32 [n_req], out: the following token; -1 for a request of
+ *               length 0, and where the last row has no weight or an infinite one.
+ *  workspace    kda_verify_workspace() bytes (may be NULL for 0), 8-byte aligned,
+ *               free for use again once the launch has run.
+ * Probabilities and rows may have any alignment of their type.  Equal calls give
+ * equal results.  Checks run in the order: DTYPE_REFUSED, ARG (counts, vocab < 1),
+ * ROWS (max_path), then, for n_req > 0 (0 is a valid no-op; n_tokens 0 leaves
+ * lengths of 0), NULL, ARG (strides), ALIGN, the workspace (NULL, ARG).
+ */
+int kda_verify_drafts(const void* target, int64_t target_stride, const void* draft, int64_t draft_stride,
+                      const int32_t* cu_seqlens, const int32_t* parents, const int32_t* tokens,
+                      const float* accept_rand, const float* sample_rand, int32_t* path, int32_t max_path,
+                      int32_t* path_lens, int32_t* next_tokens, int32_t n_req, int64_t n_tokens,
+                      int32_t vocab, kda_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace kda_verify_drafts needs (0: none, or arguments it refuses). */
+size_t kda_verify_workspace(int32_t n_req, int64_t n_tokens, int32_t vocab, int32_t max_path, kda_dtype dtype);
 
 /* Launch shape kda_decode_step uses for a given problem (host only). */
 typedef struct kda_launch_desc {

@@ -39,6 +39,7 @@ KDA_ERR_LAUNCH = 9
 KDA_HEAD_K = 128
 KDA_HEAD_V = 128
 KDA_MAX_ROWS = 8
+KDA_MAX_NODES = 64  # of one request's tree of drafted tokens
 KDA_ROWS_DEFAULT = 0
 KDA_ROWS_K_SPLIT = 1
 KDA_ROWS_WAVE_K = 2
@@ -135,6 +136,21 @@ SIGNATURES = {
                                      _P]),
     "kda_kv_attend_workspace": (ctypes.c_size_t, [ctypes.POINTER(kda_kv_pool), _I32, _I32, _I64, _I32, _I64,
                                                   _I32, ctypes.c_int]),
+    "kda_kv_append_at": (ctypes.c_int, [ctypes.POINTER(kda_kv_pool), _P, _I32, _P, _P, _P, _P, _I64, _I64, _P,
+                                        _I64, _P, _P, _P, _P, _I32, _I32, _I32, _I32, _I64, _I32, ctypes.c_int,
+                                        _P]),
+    "kda_kv_attend_tree": (ctypes.c_int, [ctypes.POINTER(kda_kv_pool), _P, _I32, _P, _P, _P, _P, _I64, _P, _I32,
+                                          _I64, _I32, _I64, _I32, ctypes.c_int, ctypes.c_float, _P,
+                                          ctypes.c_size_t, _P]),
+    "kda_kv_keep": (ctypes.c_int, [ctypes.POINTER(kda_kv_pool), _P, _I32, _P, _P, _P, _I32, _P, _I32, _I64, _P]),
+    "kda_decode_tree": (ctypes.c_int, [ctypes.POINTER(kda_pool), _P, _P, _P, _P, _P, _P, _P, _P, _P, _I32, _I64,
+                                       _I32, ctypes.c_int, ctypes.c_float, _P]),
+    "kda_decode_path": (ctypes.c_int, [ctypes.POINTER(kda_pool), _P, _P, _P, _P, _I32, _P, _P, _P, _P, _P, _I32,
+                                       _I64, ctypes.c_int, _P]),
+    "kda_verify_drafts": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _I32, _P, _P, _I32, _I64, _I32,
+                                         ctypes.c_int, _P, ctypes.c_size_t, _P]),
+    "kda_verify_workspace": (ctypes.c_size_t, [_I32, _I64, _I32, _I32, ctypes.c_int]),
+    "kda_tree_validate": (ctypes.c_int, [_P, _P, _I32, _I64]),
     "kda_kv_validate": (ctypes.c_int, [ctypes.POINTER(kda_kv_pool), _P, _I32, _P, _P, _I32, _I64]),
     "kda_strerror": (ctypes.c_char_p, [ctypes.c_int]),
     "kda_abi_version": (ctypes.c_int, []),
@@ -650,7 +666,7 @@ def _kv_call(torch, name, device, *args):
 
 
 def kda_kv_append(pool, page_table, cu_seqlens, cache_lens, k, v, q=None, q_out=None, cos=None, sin=None,
-                  interleaved: bool = False, stream=None) -> None:
+                  interleaved: bool = False, stream=None, positions=None) -> None:
     """Stores a step's keys and values in the cache, turned by their positions
     (see kda_kv_append in include/kda_decode.h).
 
@@ -658,7 +674,10 @@ def kda_kv_append(pool, page_table, cu_seqlens, cache_lens, k, v, q=None, q_out=
     cu_seqlens: int32 [n_seq + 1]; cache_lens: int32 [n_seq]; k, v: [T, H, D] of
     float32, float16 or bfloat16, slices of a joint projection allowed; q: None
     or [T, q_heads, D] of the same type, turned into q_out (contiguous); cos,
-    sin: None, or float32 [n_positions, rot_dim / 2]."""
+    sin: None, or float32 [n_positions, rot_dim / 2]; positions: None, or int32
+    [T], the rows of cos and sin where they are not the tokens' places
+    (kda_kv_append_at: a tree's nodes stand at the context's length plus their
+    depth)."""
     import torch
     P, dev = make_kv_pool(pool), pool.get_device()
     tables, n_seq = _kv_tables(dev, torch.int32, page_table, cu_seqlens, cache_lens)
@@ -672,7 +691,7 @@ def kda_kv_append(pool, page_table, cu_seqlens, cache_lens, k, v, q=None, q_out=
         heads = q.shape[1] if q.dim() == 3 else -1
         qp, qs = _kv_rows(q, "q", dev, dtype, T, heads, D)
         qo, _ = _kv_rows(q_out, "q_out", dev, dtype, T, heads, D, gaps=False)
-    cp = sp = positions = half = 0
+    cp = sp = n_positions = half = 0
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin go together")
     if cos is not None:
@@ -681,10 +700,14 @@ def kda_kv_append(pool, page_table, cu_seqlens, cache_lens, k, v, q=None, q_out=
                 _kv_refuse(t, name, dev, torch.float32)
         if cos.dim() != 2 or cos.shape != sin.shape or not (cos.is_contiguous() and sin.is_contiguous()):
             raise ValueError("cos and sin must be contiguous [n_positions, rot_dim / 2], both")
-        positions, half = cos.shape
+        n_positions, half = cos.shape
         cp, sp = cos.data_ptr(), sin.data_ptr()
-    _kv_call(torch, "kda_kv_append", dev, ctypes.byref(P), *tables, kp, vp, ks, vs, qp, qs, qo, cp, sp, positions, 2 * half,
-             int(interleaved), n_seq, T, heads, dtype_code(dtype), _kv_stream(torch, dev, stream))
+    last = (n_positions, 2 * half, int(interleaved), n_seq, T, heads, dtype_code(dtype), _kv_stream(torch, dev, stream))
+    if positions is None:
+        _kv_call(torch, "kda_kv_append", dev, ctypes.byref(P), *tables, kp, vp, ks, vs, qp, qs, qo, cp, sp, *last)
+    else:
+        at = _tree_table(positions, "positions", dev, torch.int32, (T,))
+        _kv_call(torch, "kda_kv_append_at", dev, ctypes.byref(P), *tables, kp, vp, ks, vs, qp, qs, qo, cp, sp, at, *last)
 
 
 def kda_kv_read(pool, page_table, cu_seqlens, first, k_out=None, v_out=None, stream=None) -> None:
@@ -713,6 +736,45 @@ def kda_kv_attend_workspace(pool, page_table, n_tokens: int, q_heads: int, max_r
                                                  _dtype_arg(dtype)))
 
 
+def _workspace(torch, pool, dev, workspace, bytes_needed, st):
+    """(tensor, bytes): the caller's workspace, checked, or one of bytes_needed()
+    from torch's allocator, as memory of the launch's stream."""
+    if workspace is None:
+        wn = bytes_needed()
+        if wn == 0 or st == torch._C._cuda_getCurrentRawStream(dev):
+            return torch.empty(wn, dtype=torch.uint8, device=pool.device), wn
+        # memory of that stream: the allocator hands it on in its order
+        on = torch.cuda.ExternalStream(st, device=pool.device) if st else torch.cuda.default_stream(pool.device)
+        with torch.cuda.stream(on):
+            return torch.empty(wn, dtype=torch.uint8, device=pool.device), wn
+    if not _kv_is(workspace, dev, torch.uint8):
+        _kv_refuse(workspace, "workspace", dev, torch.uint8)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace, workspace.numel()
+
+
+def _attend(name, pool, page_table, cu_seqlens, cache_lens, parents, q, out, max_rows, max_kv_len, scale, workspace,
+            stream):
+    import torch
+    P, dev = make_kv_pool(pool), pool.get_device()
+    tables, n_seq = _kv_tables(dev, torch.int32, page_table, cu_seqlens, cache_lens)
+    if q.dim() != 3:
+        raise ValueError("q must be [T, q_heads, D], got %s" % list(q.shape))
+    (T, heads, _), dtype, D = q.shape, q.dtype, P.D
+    qp, qs = _kv_rows(q, "q", dev, dtype, T, heads, D)
+    op, _ = _kv_rows(out, "out", dev, dtype, T, heads, D, gaps=False)
+    rows = int(max_rows) if max_rows is not None else T if parents is None else min(T, KDA_MAX_NODES)
+    kv, code, st = int(max_kv_len), dtype_code(dtype), _kv_stream(torch, dev, stream)
+    pool_ref = ctypes.byref(P)
+    workspace, wn = _workspace(torch, pool, dev, workspace, lambda: (_lib or library()).kda_kv_attend_workspace(
+        pool_ref, tables[1], n_seq, T, rows, kv, heads, code), st)
+    if parents is not None:
+        tables += (_tree_table(parents, "parents", dev, torch.int32, (T,)),)
+    _kv_call(torch, name, dev, pool_ref, *tables, qp, qs, op, n_seq, T, rows, kv, heads, code,
+             1.0 / math.sqrt(D) if scale is None else float(scale), workspace.data_ptr(), wn, st)
+
+
 def kda_kv_attend(pool, page_table, cu_seqlens, cache_lens, q, out, max_rows: int | None = None,
                   max_kv_len: int = 0, scale: float | None = None, workspace=None, stream=None) -> None:
     """Causal attention of a step's rows over the cache (see kda_kv_attend in
@@ -724,33 +786,178 @@ def kda_kv_attend(pool, page_table, cu_seqlens, cache_lens, q, out, max_rows: in
     page_table covers): they lay out the launch, results hold for any.
     workspace: a contiguous uint8 tensor of kda_kv_attend_workspace bytes, or
     None to take one from torch's allocator on the launch's stream."""
+    _attend("kda_kv_attend", pool, page_table, cu_seqlens, cache_lens, None, q, out, max_rows, max_kv_len, scale,
+            workspace, stream)
+
+
+def kda_kv_attend_tree(pool, page_table, cu_seqlens, cache_lens, parents, q, out, max_rows: int | None = None,
+                       max_kv_len: int = 0, scale: float | None = None, workspace=None, stream=None) -> None:
+    """kda_kv_attend for the nodes of trees of drafted tokens: a node sees the
+    context, its path and itself (see kda_kv_attend_tree in
+    include/kda_decode.h).  parents: int32 [T], each node's parent within its
+    request, -1 for none; max_rows: the most nodes of a request (default: T, at
+    most KDA_MAX_NODES); the rest as kda_kv_attend's."""
+    if parents is None:
+        raise ValueError("a tree needs its parents")
+    _attend("kda_kv_attend_tree", pool, page_table, cu_seqlens, cache_lens, parents, q, out, max_rows, max_kv_len, scale,
+            workspace, stream)
+
+
+# ---------------------------------------------------------------------------
+# trees of drafted tokens
+# ---------------------------------------------------------------------------
+
+def _tree_table(t, name, device, dtype, shape):
+    """Address of a contiguous tensor of this type, shape and GPU."""
+    if not _kv_is(t, device, dtype):
+        _kv_refuse(t, name, device, dtype)
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError("%s must be contiguous %s, got %s" % (name, list(shape), list(t.shape)))
+    return t.data_ptr()
+
+
+def _tree_path(path, dev, i32, n_req):
+    """Address and width of a table of paths."""
+    if not _kv_is(path, dev, i32):
+        _kv_refuse(path, "path", dev, i32)
+    if path.dim() != 2:
+        raise ValueError("path must be [n_req, max_path], got %s" % list(path.shape))
+    return _tree_table(path, "path", dev, i32, (n_req, path.shape[1])), path.shape[1]
+
+
+def kda_kv_keep(pool, page_table, cu_seqlens, cache_lens, path, path_lens, n_tokens: int | None = None,
+                stream=None) -> None:
+    """Moves the cache entries of accepted nodes together, behind the context
+    (see kda_kv_keep in include/kda_decode.h).  path: int32 [n_seq, max_path],
+    path_lens: int32 [n_seq], as kda_verify_drafts writes them; n_tokens: nodes
+    of the launch (default: no bound but cu_seqlens' own)."""
     import torch
-    P, dev = make_kv_pool(pool), pool.get_device()
-    tables, n_seq = _kv_tables(dev, torch.int32, page_table, cu_seqlens, cache_lens)
-    if q.dim() != 3:
-        raise ValueError("q must be [T, q_heads, D], got %s" % list(q.shape))
-    (T, heads, _), dtype, D = q.shape, q.dtype, P.D
-    qp, qs = _kv_rows(q, "q", dev, dtype, T, heads, D)
-    op, _ = _kv_rows(out, "out", dev, dtype, T, heads, D, gaps=False)
-    rows, kv, code, st = T if max_rows is None else int(max_rows), int(max_kv_len), dtype_code(dtype), _kv_stream(torch, dev, stream)
-    pool_ref = ctypes.byref(P)
-    if workspace is None:
-        wn = (_lib or library()).kda_kv_attend_workspace(pool_ref, tables[1], n_seq, T, rows, kv, heads, code)
-        if wn == 0 or st == torch._C._cuda_getCurrentRawStream(dev):
-            workspace = torch.empty(wn, dtype=torch.uint8, device=pool.device)
-        else:
-            # memory of that stream: the allocator hands it on in its order
-            on = torch.cuda.ExternalStream(st, device=pool.device) if st else torch.cuda.default_stream(pool.device)
-            with torch.cuda.stream(on):
-                workspace = torch.empty(wn, dtype=torch.uint8, device=pool.device)
-    else:
-        if not _kv_is(workspace, dev, torch.uint8):
-            _kv_refuse(workspace, "workspace", dev, torch.uint8)
-        if not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous")
-        wn = workspace.numel()
-    _kv_call(torch, "kda_kv_attend", dev, pool_ref, *tables, qp, qs, op, n_seq, T, rows, kv, heads, code,
-             1.0 / math.sqrt(D) if scale is None else float(scale), workspace.data_ptr(), wn, st)
+    P, dev, i32 = make_kv_pool(pool), pool.get_device(), torch.int32
+    tables, n_seq = _kv_tables(dev, i32, page_table, cu_seqlens, cache_lens)
+    pp, wide = _tree_path(path, dev, i32, n_seq)
+    lp = _tree_table(path_lens, "path_lens", dev, i32, (n_seq,))
+    T = 2 ** 31 - 1 if n_tokens is None else int(n_tokens)
+    _kv_call(torch, "kda_kv_keep", dev, ctypes.byref(P), *tables, pp, wide, lp, n_seq, T, _kv_stream(torch, dev, stream))
+
+
+def _tree_rows(dev, T, H, **rows):
+    """Addresses of the nodes' rows: [T, H, 128] ([T, H] for b), contiguous float32."""
+    import torch
+    return [_tree_table(t, name, dev, torch.float32, (T, H) if name == "b" else (T, H, 128)) for name, t in rows.items()]
+
+
+def _tree_pool(pool, cu_seqlens, init_slot_ids, pool_dtype, state_dtype):
+    """The checked pool, its GPU, the requests and the tables' addresses."""
+    import torch
+    P = make_pool(pool, pool_dtype)
+    dev = pool.get_device()
+    n_req = init_slot_ids.shape[0] if isinstance(init_slot_ids, torch.Tensor) and init_slot_ids.dim() == 1 else -1
+    ip = _tree_table(init_slot_ids, "init_slot_ids", dev, torch.int32, (n_req,))
+    cp = _tree_table(cu_seqlens, "cu_seqlens", dev, torch.int32, (n_req + 1,))
+    return P, dev, n_req, ip, cp, P.dtype if state_dtype is None else _dtype_arg(state_dtype)
+
+
+def kda_decode_tree(pool, init_slot_ids, cu_seqlens, parents, q, k, v, g, b, out, max_nodes: int | None = None,
+                    state_dtype=None, scale: float | None = None, stream=None, pool_dtype=None) -> None:
+    """The recurrence over trees of drafted tokens: every node's read-out from its
+    path's state; the pool is only read (see kda_decode_tree in
+    include/kda_decode.h).
+
+    pool: [n_slots, H, 128, 128], float32 or float16; init_slot_ids: int32
+    [n_req]; cu_seqlens: int32 [n_req + 1]; parents: int32 [T]; q, k, v, g, out:
+    float32 [T, H, 128]; b: [T, H]; max_nodes: the most nodes of a request
+    (default: T, at most KDA_MAX_NODES)."""
+    import torch
+    P, dev, n_req, ip, cp, sd = _tree_pool(pool, cu_seqlens, init_slot_ids, pool_dtype, state_dtype)
+    T = parents.shape[0] if isinstance(parents, torch.Tensor) and parents.dim() == 1 else -1
+    pp = _tree_table(parents, "parents", dev, torch.int32, (T,))
+    rows = _tree_rows(dev, T, P.H, q=q, k=k, v=v, g=g, b=b, out=out)
+    most = min(T, KDA_MAX_NODES) if max_nodes is None else int(max_nodes)
+    _kv_call(torch, "kda_decode_tree", dev, ctypes.byref(P), ip, cp, pp, *rows, n_req, T, most, sd,
+             1.0 / math.sqrt(KDA_HEAD_K) if scale is None else float(scale), _kv_stream(torch, dev, stream))
+
+
+def kda_decode_path(pool, init_slot_ids, cu_seqlens, path, path_lens, k, v, g, b, dst_slot_ids=None, state_dtype=None,
+                    stream=None, pool_dtype=None) -> None:
+    """Applies the accepted nodes' updates in turn and stores the state (see
+    kda_decode_path in include/kda_decode.h).  path: int32 [n_req, max_path],
+    path_lens: int32 [n_req]; k, v, g: float32 [T, H, 128]; b: [T, H];
+    dst_slot_ids: int32 [n_req], or None to store back."""
+    import torch
+    P, dev, n_req, ip, cp, sd = _tree_pool(pool, cu_seqlens, init_slot_ids, pool_dtype, state_dtype)
+    dp = 0 if dst_slot_ids is None else _tree_table(dst_slot_ids, "dst_slot_ids", dev, torch.int32, (n_req,))
+    pp, wide = _tree_path(path, dev, torch.int32, n_req)
+    lp = _tree_table(path_lens, "path_lens", dev, torch.int32, (n_req,))
+    T = k.shape[0] if isinstance(k, torch.Tensor) and k.dim() == 3 else -1
+    rows = _tree_rows(dev, T, P.H, k=k, v=v, g=g, b=b)
+    _kv_call(torch, "kda_decode_path", dev, ctypes.byref(P), ip, dp, cp, pp, wide, lp, *rows, n_req, T, sd,
+             _kv_stream(torch, dev, stream))
+
+
+def _verify_rows(t, name, dev, dtype, n, vocab):
+    """Address and row stride of probabilities [n, vocab] whose rows have no gaps."""
+    if not _kv_is(t, dev, dtype):
+        _kv_refuse(t, name, dev, dtype)
+    if t.shape != (n, vocab):
+        raise ValueError("%s must be [%d, %d], got %s" % (name, n, vocab, list(t.shape)))
+    row, entry = t.stride()
+    if n < 2:
+        row = vocab
+    if (entry != 1 and vocab > 1) or row < vocab:
+        raise ValueError("%s must be contiguous within its rows" % name)
+    return t.data_ptr(), row
+
+
+def kda_verify_workspace(n_req: int, n_tokens: int, vocab: int, max_path: int, dtype="f32") -> int:
+    """Bytes of workspace kda_verify_drafts needs for a launch of these sizes."""
+    return int(library().kda_verify_workspace(int(n_req), int(n_tokens), int(vocab), int(max_path), _dtype_arg(dtype)))
+
+
+def kda_verify_drafts(target, cu_seqlens, parents, tokens, accept_rand, sample_rand, path, path_lens, next_tokens,
+                      draft=None, workspace=None, stream=None) -> None:
+    """Which drafted tokens are kept, and the token that follows them (see
+    kda_verify_drafts in include/kda_decode.h).
+
+    target: [T, vocab] probabilities of float32, float16 or bfloat16 (row stride
+    free); draft: None, or the same; cu_seqlens: int32 [n_req + 1]; parents,
+    tokens: int32 [T]; accept_rand: float32 [T]; sample_rand: float32 [n_req].
+    Written: path: int32 [n_req, max_path]; path_lens, next_tokens: int32 [n_req].
+    workspace: a contiguous uint8 tensor of kda_verify_workspace bytes, or None to
+    take one from torch's allocator on the launch's stream."""
+    import torch
+    if not isinstance(target, torch.Tensor) or not target.is_cuda:
+        _on_gpu(target, "target")
+    if target.dim() != 2:
+        raise ValueError("target must be [T, vocab], got %s" % list(target.shape))
+    dev, dtype, i32, f32 = target.get_device(), target.dtype, torch.int32, torch.float32
+    T, vocab = target.shape
+    tp, ts = _verify_rows(target, "target", dev, dtype, T, vocab)
+    qp, qs = (0, 0) if draft is None else _verify_rows(draft, "draft", dev, dtype, T, vocab)
+    n_req = sample_rand.shape[0] if isinstance(sample_rand, torch.Tensor) and sample_rand.dim() == 1 else -1
+    sp = _tree_table(sample_rand, "sample_rand", dev, f32, (n_req,))
+    cp = _tree_table(cu_seqlens, "cu_seqlens", dev, i32, (n_req + 1,))
+    pp, xp = _tree_table(parents, "parents", dev, i32, (T,)), _tree_table(tokens, "tokens", dev, i32, (T,))
+    ap = _tree_table(accept_rand, "accept_rand", dev, f32, (T,))
+    op, wide = _tree_path(path, dev, i32, n_req)
+    lp = _tree_table(path_lens, "path_lens", dev, i32, (n_req,))
+    np_ = _tree_table(next_tokens, "next_tokens", dev, i32, (n_req,))
+    code, st = dtype_code(dtype), _kv_stream(torch, dev, stream)
+    workspace, wn = _workspace(torch, target, dev, workspace, lambda: (_lib or library()).kda_verify_workspace(
+        n_req, T, vocab, wide, code), st)
+    _kv_call(torch, "kda_verify_drafts", dev, tp, ts, qp, qs, cp, pp, xp, ap, sp, op, wide, lp, np_, n_req, T, vocab,
+             code, workspace.data_ptr(), wn, st)
+
+
+def kda_tree_validate(cu_seqlens_host, parents_host, n_tokens: int | None = None) -> int:
+    """Host-side check of a step's trees; returns the kda_status code."""
+    cu = np.ascontiguousarray(cu_seqlens_host, dtype=np.int32)
+    up = np.ascontiguousarray(parents_host, dtype=np.int32)
+    if cu.ndim != 1 or cu.size < 1 or up.ndim != 1:
+        raise ValueError("cu_seqlens [n_req + 1], parents [n_tokens]")
+    n = up.size if n_tokens is None else int(n_tokens)
+    if n > up.size:
+        raise ValueError("parents holds %d nodes, the launch addresses %d" % (up.size, n))
+    return int(library().kda_tree_validate(cu.ctypes.data, up.ctypes.data, cu.size - 1, n))
 
 
 def kda_kv_validate(pool_desc: kda_kv_pool, page_table_host, cu_seqlens_host, cache_lens_host, n_tokens: int) -> int:

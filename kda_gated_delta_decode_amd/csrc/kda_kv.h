@@ -51,6 +51,7 @@ struct KvAppendArgs {
   const float* cos;
   const float* sin;
   int64_t q_stride, k_stride, v_stride;  // elements between tokens
+  const int32_t* positions;  // nullable: the rows of cos and sin, apart from the places
   int32_t n_positions, half, interleaved, q_heads;
   int32_t units, units_per_block, unit_blocks;  // units: cached heads, then query heads
 };
@@ -61,6 +62,13 @@ struct KvReadArgs {
   void* v_out;
   int64_t k_stride, v_stride;
   int32_t heads_per_block, head_blocks;
+};
+
+struct KvKeepArgs {
+  KvTables t;
+  const int32_t* path;  // [n_seq][max_path]
+  const int32_t* lens;  // [n_seq]
+  int32_t max_path;
 };
 
 struct KvAttendArgs {
@@ -76,6 +84,8 @@ struct KvAttendArgs {
   int32_t slots;                // 128-row tiles: places for all sequences' tiles
   float scale;                  // |scale| * log2(e)
   float sign;                   // of scale: queries are multiplied by it
+  const int32_t* parents;       // trees: [n_tokens]
+  int32_t most_rows;            // trees: KDA_MAX_NODES; else no bound
 };
 
 // How kda_kv_attend takes a launch.

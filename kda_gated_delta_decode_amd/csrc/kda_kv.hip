@@ -19,6 +19,7 @@
 #include "kda_decode.h"
 #include "kda_device.h"
 #include "kda_kv.h"
+#include "kda_tree_device.h"
 
 namespace kda {
 namespace {
@@ -287,8 +288,15 @@ __global__ __launch_bounds__(256) void kda_kv_append_kernel(KvAppendArgs a) {
   const int64_t token = tile * (256 / W) + threadIdx.x / W;
   const int u0 = ub * a.units_per_block;
   const int u1 = u0 + a.units_per_block < a.units ? u0 + a.units_per_block : a.units;
-  const TokenPlace at = find_token<W>(a.t, token, a.n_positions);
+  // (given positions are asked for before the sequence is known)
+  const bool given = a.positions != nullptr;
+  const int32_t turn = given && token < a.t.n_tokens ? a.positions[token] : 0;
+  TokenPlace at = find_token<W>(a.t, token, given ? INT32_MAX : a.n_positions);
   if (at.what == kOutside) return;
+  if (given) {
+    if (turn < 0 || turn >= a.n_positions) at.what = kBad;
+    at.pos = turn;
+  }
 
   // out[e] = x[e] * cs[e] + partner[e] * sn[e]
   const int c0 = 8 * li, lane = threadIdx.x % 64;
@@ -484,6 +492,22 @@ __device__ __forceinline__ Seq seq_of(const KvTables& t, int s) {
   return q;
 }
 
+// Trees: lane i gets node i's path, as bits of nodes; *broken: a node's parent
+// does not lie before it.
+__device__ __forceinline__ uint64_t path_of_lane(const KvAttendArgs& a, const Seq& q, bool* broken) {
+  const int lane = threadIdx.x % 64, n = q.bad ? 0 : q.rows;
+  return tree_paths(lane < n ? a.parents[q.n0 + lane] : -1, n, broken);
+}
+
+// The tokens tb + x that a node sees, as bits x < 64; `nodes`: its path, whose
+// first bit is token `past`.
+__device__ __forceinline__ uint64_t seen_from(int tb, int past, uint64_t nodes) {
+  const int before = past - tb;  // tokens of the context from tb on
+  if (before >= 64) return ~0ull;
+  if (before >= 0) return nodes << before | ((1ull << before) - 1);
+  return before > -64 ? nodes >> -before : 0;
+}
+
 // Splits of a tile whose last row sees `vis` tokens; the last split takes what
 // the launch had no blocks for.
 __device__ __forceinline__ int kv_splits(int vis, const KvAttendArgs& a) {
@@ -606,8 +630,10 @@ constexpr int kv_rows_waves() { return NT == 1 && NW == 4 ? 3 : 2; }
 // one set of registers keeps loads in flight all the time.  64 requests of 4096
 // tokens, 12 cached heads in bf16: 427 MB in 81 us, 5.2 TB/s of the 6.5 that a
 // streaming copy reaches; 8 requests of 8 rows: 53 MB in 15 us.
-template <int DT, int D, int NT, int NW>
-__global__ __launch_bounds__(64 * NW, (kv_rows_waves<NT, NW>())) void kda_kv_rows_kernel(KvAttendArgs a) {
+// TREE: a node sees the context and its path, a word of 64 bits in LDS that only
+// the steps with nodes look at.
+template <int DT, int D, int NT, int NW, bool TREE>
+__device__ __forceinline__ void rows_body(const KvAttendArgs& a) {
   constexpr int NQ = q_pieces<DT>(), NP = w_pieces<DT>();
   constexpr int M = D / 32;   // products over the channels
   constexpr int C = D / 16;   // channels of a lane in the second product, and its row tiles
@@ -615,6 +641,8 @@ __global__ __launch_bounds__(64 * NW, (kv_rows_waves<NT, NW>())) void kda_kv_row
   constexpr int LD = D + 4;
   __shared__ float o_sh[NW][R][LD];
   __shared__ float ml_sh[NW][R][2];
+  // nodes' paths behind the context: 32 bits of it, 64 of nodes, 32 of nothing
+  __shared__ u4 path_sh[TREE ? NW : 1][TREE ? 64 : 1];
 
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int i16 = lane % 16, j = lane / 16;
@@ -635,9 +663,18 @@ __global__ __launch_bounds__(64 * NW, (kv_rows_waves<NT, NW>())) void kda_kv_row
     return at < a.t.max_pages ? table[at] : -1;
   };
   const int pages0 = load_pages(t0 + 32 * wave);
-  const Seq q = seq_of(a.t, s);
+  Seq q = seq_of(a.t, s);
   if (q.skip) return;
   const int all_rows = q.rows * a.group;
+  bool broken = false;  // a tree that is none
+  if constexpr (TREE) {
+    q.bad |= q.rows > a.most_rows;
+    // Only the splits that reach the nodes wait for the parents.  (Between the
+    // first loads and the steps the paths' registers would be spilled.)
+    const bool reaches = static_cast<int64_t>(t0) + a.chunk > q.past || sp == a.n_splits - 1;
+    const uint64_t nodes = reaches ? path_of_lane(a, q, &broken) : 0;
+    path_sh[wave][lane] = u4{~0u, static_cast<uint32_t>(nodes), static_cast<uint32_t>(nodes >> 32), 0};
+  }
 
   const int block_bytes = kv_block_bytes(a.t.P, D);
   const uint8_t* head0 = a.t.base + static_cast<int64_t>(h) * block_bytes;
@@ -653,9 +690,9 @@ __global__ __launch_bounds__(64 * NW, (kv_rows_waves<NT, NW>())) void kda_kv_row
     const int splits = q.bad ? 1 : kv_splits(vis, a);
     if (sp >= splits) continue;
     const int t1 = q.bad ? 0 : sp == splits - 1 ? vis : t0 + a.chunk;
-    const int first_limit = q.past + row0 / a.group;  // the last token every row sees
+    const int first_limit = TREE ? q.past - 1 : q.past + row0 / a.group;  // the last token every row sees
 
-    // this lane's query row of each tile, and the last token it sees
+    // this lane's query row of each tile, and the last token it sees (TREE: its node)
     u4 qf[NT][NQ][M];
     int limit[NT];
 #pragma unroll
@@ -663,7 +700,7 @@ __global__ __launch_bounds__(64 * NW, (kv_rows_waves<NT, NW>())) void kda_kv_row
       const int row = row0 + 16 * n + i16;
       const int r = row <= last_row ? row : last_row;
       const int tok = r / a.group, g = r - tok * a.group;
-      limit[n] = row <= last_row ? q.past + tok : -1;
+      limit[n] = TREE ? tok : row <= last_row ? q.past + tok : -1;
       const int64_t at = (q.n0 + tok) * a.q_stride + (static_cast<int64_t>(h) * a.group + g) * D + j * (D / 4);
 #pragma unroll
       for (int m = 0; m < M; ++m) {
@@ -765,13 +802,24 @@ __global__ __launch_bounds__(64 * NW, (kv_rows_waves<NT, NW>())) void kda_kv_row
 #pragma unroll
         for (int b = 0; b < 2; ++b) sc[n][b] *= a.scale;
       if (tail) {
+        uint32_t seen[NT];  // TREE: from the lane's first token on
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          if constexpr (TREE) {
+            const int x = tb - q.past < -32 ? 0 : tb - q.past + 32;  // of the 128 bits, below 96
+            const uint32_t* word = reinterpret_cast<const uint32_t*>(&path_sh[wave][limit[n]]) + x / 32;
+            seen[n] = __builtin_amdgcn_alignbit(word[1], word[0], x % 32) >> (4 * j);
+          }
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const int t = tb + 16 * b + 4 * j + r;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) sc[n][b][r] = t > limit[n] ? -INFINITY : sc[n][b][r];
+            for (int n = 0; n < NT; ++n) {
+              const bool hidden = TREE ? (seen[n] & (1u << (16 * b + r))) == 0 : t > limit[n];
+              sc[n][b][r] = hidden ? -INFINITY : sc[n][b][r];
+            }
             const bool none = t >= t1 || vp[b] < 0;
             vc[4 * b + r] = none ? 0 : vc[4 * b + r];
             ve[b] = none ? (ve[b] & ~(0xFFu << (8 * r))) | (127u << (8 * r)) : ve[b];
@@ -878,7 +926,7 @@ __global__ __launch_bounds__(64 * NW, (kv_rows_waves<NT, NW>())) void kda_kv_row
       if (splits == 1) {
         // every row sees its own token: a sum of zero means that its largest
         // score is infinite, and 0 / 0 makes the row NaN, as a bad sequence's are
-        const float inv = q.bad ? __builtin_nanf("") : 1.0f / total;
+        const float inv = q.bad || broken ? __builtin_nanf("") : 1.0f / total;
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] *= inv;
         store8<DT>(a.out, at * D + c, acc);
@@ -887,11 +935,90 @@ __global__ __launch_bounds__(64 * NW, (kv_rows_waves<NT, NW>())) void kda_kv_row
         store8<KDA_F32>(a.part, slot * D + c, acc);
         if (c == 0) {
           a.part_ml[2 * slot] = top;
-          a.part_ml[2 * slot + 1] = total;
+          a.part_ml[2 * slot + 1] = broken ? __builtin_nanf("") : total;
         }
       }
     }
     __syncthreads();
+  }
+}
+
+template <int DT, int D, int NT, int NW>
+__global__ __launch_bounds__(64 * NW, (kv_rows_waves<NT, NW>())) void kda_kv_rows_kernel(KvAttendArgs a) {
+  rows_body<DT, D, NT, NW, false>(a);
+}
+template <int DT, int D, int NT, int NW>
+__global__ __launch_bounds__(64 * NW, (kv_rows_waves<NT, NW>())) void kda_kv_tree_rows_kernel(KvAttendArgs a) {
+  rows_body<DT, D, NT, NW, true>(a);
+}
+
+// ---------------------------------------------------------------------------
+// Keeping accepted nodes
+// ---------------------------------------------------------------------------
+
+// A wave for a sequence and cached head, 16 lanes a token: four of them with 16
+// bytes (D = 64: 8) of key codes each, four with the value codes, one with the key
+// exponents, one with the value exponents.  Four tokens are read, then written; a
+// path ascends, so every source lies at or behind its destination and behind
+// the destinations of all tokens before it.  Bound by latency: path and pages,
+// then the tokens.
+template <int D>
+__global__ __launch_bounds__(256) void kda_kv_keep_kernel(KvKeepArgs a) {
+  using Codes = std::conditional_t<D == 128, u4, u2>;
+  using Exps = std::conditional_t<D == 128, uint32_t, uint16_t>;
+  constexpr int kExps = D / kKvGroup;
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / 64;
+  const int64_t s = unit / a.t.H;
+  const int h = static_cast<int>(unit % a.t.H);
+  if (s >= a.t.n_seq) return;
+  const int lane = threadIdx.x % 64, sub = lane / 16, li = lane % 16;
+  const int len = a.lens[s];
+  const Seq q = seq_of(a.t, static_cast<int>(s));
+  if (len < 1 || len > a.max_path || q.skip || q.past < 0) return;
+  const int node = lane < len ? a.path[s * a.max_path + lane] : INT32_MAX;
+  const int before = __shfl_up(node, 1);
+  const bool ok = lane >= len || (node >= 0 && node < q.rows && (lane == 0 || node > before));
+  if (__ballot(!ok) != 0) return;
+  const int block_bytes = kv_block_bytes(a.t.P, D);
+  const int32_t* table = a.t.page_table + s * a.t.max_pages;
+  auto place = [&](int64_t pos) __attribute__((always_inline)) {
+    const int64_t i = pos >> a.t.log_p;
+    const int page = i < a.t.max_pages ? table[i] : -1;
+    return page >= 0 && page < a.t.n_pages ? a.t.base + page * a.t.page_bytes + static_cast<int64_t>(h) * block_bytes : nullptr;
+  };
+  for (int e0 = 0; e0 < len; e0 += 4) {
+    const int e = e0 + sub;
+    const int from = __shfl(node, e % 64);
+    const int64_t a0 = static_cast<int64_t>(q.past) + from, b0 = static_cast<int64_t>(q.past) + e;
+    const bool moves = e < len && from != e;
+    const uint8_t* src = moves ? place(a0) : nullptr;
+    uint8_t* dst = moves ? place(b0) : nullptr;
+    const int ra = static_cast<int>(a0) & (a.t.P - 1), rb = static_cast<int>(b0) & (a.t.P - 1);
+    // codes: keys' quarters in lanes 0..3, values' in 4..7
+    const int part = (li < 4 ? 0 : kv_value_codes(a.t.P, D)) + li % 4 * (D / 8);
+    Codes codes{};
+    Exps exps{};
+    if (dst != nullptr && src != nullptr) {
+      if (li < 8) codes = *reinterpret_cast<const Codes*>(src + part + ra * (D / 2));
+      if (li == 8) exps = *reinterpret_cast<const Exps*>(src + kv_key_exps(a.t.P, D) + ra * kExps);
+      if (li == 9)
+#pragma unroll
+        for (int g = 0; g < kExps; ++g)
+          exps |= static_cast<Exps>(static_cast<uint32_t>(src[kv_value_exps(a.t.P, D) + g * a.t.P + ra]) << (8 * g));
+    } else if (li == 8) {
+      exps = static_cast<Exps>(~0u);  // no page: poisoned, with values of zero
+    } else if (li == 9) {
+      exps = static_cast<Exps>(kKvMinExp * 0x01010101u);
+    }
+    // (every lane's load above is waited for before the first store below)
+    if (dst != nullptr) {
+      if (li < 8) *reinterpret_cast<Codes*>(dst + part + rb * (D / 2)) = codes;
+      if (li == 8) *reinterpret_cast<Exps*>(dst + kv_key_exps(a.t.P, D) + rb * kExps) = exps;
+      if (li == 9)
+#pragma unroll
+        for (int g = 0; g < kExps; ++g)
+          dst[kv_value_exps(a.t.P, D) + g * a.t.P + rb] = static_cast<uint8_t>(exps >> (8 * g));
+    }
   }
 }
 
@@ -979,8 +1106,9 @@ struct ExpRange {
 // rows of 32 query heads 536 us, 1026 TFLOP/s of the 1211 that a large bf16 matrix
 // product reaches (829 us with two bf16 pieces for a weight, one tile after the
 // other).
-template <int DT, int D>
-__global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tiles_kernel(KvAttendArgs a) {
+// TREE: as in the rows kernel.
+template <int DT, int D, bool TREE>
+__device__ __forceinline__ void tiles_body(const KvAttendArgs& a) {
   constexpr int KT = 64;            // tokens of a tile
   constexpr int KS = D / 16;        // products over the channels
   constexpr int CB = D / 32;        // 32-channel blocks
@@ -992,6 +1120,7 @@ __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tiles_kerne
   __shared__ __attribute__((aligned(16))) char v_sh[2 * VBUF];
   // whether a wave met an exponent that fp16 does not hold
   __shared__ __attribute__((aligned(4))) uint8_t far_sh[4];
+  __shared__ uint64_t path_sh[TREE ? 4 : 1][TREE ? 64 : 1];
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   // A sequence's last tiles see the most tokens and go first.  Heads go round
@@ -1001,8 +1130,9 @@ __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tiles_kerne
   const TileAt mine = tile_of_slot(a, a.slots - 1 - turn / a.n_splits);
   if (mine.tile < 0) return;
   const int s = mine.s;
-  const Seq q = seq_of(a.t, s);
+  Seq q = seq_of(a.t, s);
   if (q.skip) return;
+  if constexpr (TREE) q.bad |= q.rows > a.most_rows;
   const int all_rows = q.rows * a.group;
   if (mine.tile >= (all_rows + R - 1) / R) return;
   const int row0 = mine.tile * R;
@@ -1016,7 +1146,12 @@ __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tiles_kerne
   if (sp >= splits) return;
   const int t0 = q.bad ? 0 : sp * a.chunk;
   const int t1 = q.bad ? 0 : sp == splits - 1 ? vis : t0 + a.chunk;
-  const int w_first = q.past + (row0 + 32 * wave) / a.group;  // the last token all of the wave's rows see
+  // the last token all of the wave's rows see
+  const int w_first = TREE ? q.past - 1 : q.past + (row0 + 32 * wave) / a.group;
+  bool broken = false;  // a tree that is none
+  if constexpr (TREE) {
+    if (t1 > q.past) path_sh[wave][threadIdx.x % 64] = path_of_lane(a, q, &broken);
+  }
 
   // Weights of 16-bit types are taken 2^7 times larger, at most 2^15: fp16 has
   // room for smaller ones then.
@@ -1059,7 +1194,7 @@ __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tiles_kerne
   const int row = row0 + 32 * wave + i32;
   const int r_in = row <= last_row ? row : last_row;
   const int tok = r_in / a.group, g = r_in - tok * a.group;
-  const int limit = row <= last_row ? q.past + tok : -1;
+  const int limit = TREE ? tok : row <= last_row ? q.past + tok : -1;  // TREE: the row's node
   float scale = a.scale;
   u4 qf[NQ][KS];
   kernel_args args0 = (kernel_args)__builtin_amdgcn_kernarg_segment_ptr();
@@ -1279,10 +1414,15 @@ __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tiles_kerne
     }
     if (tb + KT - 1 > w_first) {
       const int left = limit - tb - 4 * half;  // the last of the lane's tokens its row sees
+      const uint64_t seen = TREE ? seen_from(tb, q.past, path_sh[wave][limit]) >> (4 * half) : 0;
 #pragma unroll
       for (int b = 0; b < 2; ++b)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) sc[b][e] = 32 * b + 8 * (e / 4) + e % 4 > left ? -INFINITY : sc[b][e];
+        for (int e = 0; e < 16; ++e) {
+          const int x = 32 * b + 8 * (e / 4) + e % 4;
+          const bool hidden = TREE ? (static_cast<uint32_t>(seen >> (32 * b)) & (1u << (x % 32))) == 0 : x > left;
+          sc[b][e] = hidden ? -INFINITY : sc[b][e];
+        }
       best = top_score(sc);
     }
     // the running maximum moves only when a score passes it by 8
@@ -1391,7 +1531,7 @@ __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tiles_kerne
     const int ot = out_row / args->group, og = out_row - ot * args->group;
     const int64_t at = (q.n0 + ot) * args->q_heads + static_cast<int64_t>(h) * args->group + og;
     const int64_t slot = static_cast<int64_t>(sp) * args->t.n_tokens * args->q_heads + at;
-    const float inv = splits > 1 ? 1.0f : q.bad ? __builtin_nanf("") : 1.0f / sum;  // sum 0: NaN, as above
+    const float inv = splits > 1 ? 1.0f : q.bad || broken ? __builtin_nanf("") : 1.0f / sum;  // sum 0: NaN, as above
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int64_t c0 = VC * (8 * (e / 4) + 4 * out_half + e % 4);
@@ -1405,9 +1545,18 @@ __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tiles_kerne
     }
     if (splits > 1 && out_half == 0) {
       args->part_ml[2 * slot] = mx - UP;
-      args->part_ml[2 * slot + 1] = sum;
+      args->part_ml[2 * slot + 1] = broken ? __builtin_nanf("") : sum;
     }
   }
+}
+
+template <int DT, int D>
+__global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tiles_kernel(KvAttendArgs a) {
+  tiles_body<DT, D, false>(a);
+}
+template <int DT, int D>
+__global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tree_tiles_kernel(KvAttendArgs a) {
+  tiles_body<DT, D, true>(a);
 }
 
 // Joins the splits of rows, D / 8 lanes across a row's channels.  Few splits:
@@ -1437,7 +1586,7 @@ __global__ __launch_bounds__(256) void kda_kv_join_kernel(KvAttendArgs a, int ti
     rt0 = mine.tile, s = mine.s;
   }
   const Seq q = seq_of(a.t, s);
-  if (q.skip || q.bad || r >= tile_rows) return;
+  if (q.skip || q.bad || q.rows > a.most_rows || r >= tile_rows) return;
   const int all_rows = q.rows * a.group;
   const int64_t stride = a.t.n_tokens * a.q_heads;
   for (int64_t row0 = static_cast<int64_t>(rt0) * tile_rows + r; row0 < all_rows;
@@ -1552,12 +1701,12 @@ int heads_a_block(int64_t token_tiles, int heads) {
 
 using namespace kda;
 
-extern "C" int kda_kv_append(const kda_kv_pool* kv, const int32_t* page_table, int32_t max_pages,
-                             const int32_t* cu_seqlens, const int32_t* cache_lens, const void* k, const void* v,
-                             int64_t k_stride, int64_t v_stride, const void* q, int64_t q_stride, void* q_out,
-                             const float* cos, const float* sin, int32_t n_positions, int32_t rot_dim,
-                             int32_t interleaved, int32_t n_seq, int64_t n_tokens, int32_t q_heads,
-                             kda_dtype dtype, void* stream) {
+extern "C" int kda_kv_append_at(const kda_kv_pool* kv, const int32_t* page_table, int32_t max_pages,
+                                const int32_t* cu_seqlens, const int32_t* cache_lens, const void* k, const void* v,
+                                int64_t k_stride, int64_t v_stride, const void* q, int64_t q_stride, void* q_out,
+                                const float* cos, const float* sin, const int32_t* positions, int32_t n_positions,
+                                int32_t rot_dim, int32_t interleaved, int32_t n_seq, int64_t n_tokens,
+                                int32_t q_heads, kda_dtype dtype, void* stream) {
   const int rc = kv_check(kv, max_pages, n_seq, n_tokens);
   if (rc != KDA_OK) return rc;
   const int size = kv_type_bytes(dtype);
@@ -1573,7 +1722,7 @@ extern "C" int kda_kv_append(const kda_kv_pool* kv, const int32_t* page_table, i
   if (k_stride < kv_row || v_stride < kv_row || (q_heads > 0 && q_stride < q_row)) return KDA_ERR_ARG;
   if (!aligned(kv->base, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q, 16) || !aligned(q_out, 16) ||
       !aligned(cos, 16) || !aligned(sin, 16) || !aligned(page_table, 4) || !aligned(cu_seqlens, 4) ||
-      !aligned(cache_lens, 4) || k_stride * size % 16 != 0 || v_stride * size % 16 != 0 ||
+      !aligned(cache_lens, 4) || !aligned(positions, 4) || k_stride * size % 16 != 0 || v_stride * size % 16 != 0 ||
       (q_heads > 0 && q_stride * size % 16 != 0))
     return KDA_ERR_ALIGN;
   KvAppendArgs a;
@@ -1587,6 +1736,7 @@ extern "C" int kda_kv_append(const kda_kv_pool* kv, const int32_t* page_table, i
   a.q_stride = q_stride;
   a.k_stride = k_stride;
   a.v_stride = v_stride;
+  a.positions = rot_dim > 0 ? positions : nullptr;
   a.n_positions = rot_dim > 0 ? n_positions : INT32_MAX;
   a.half = rot_dim / 2;
   a.interleaved = interleaved;
@@ -1609,6 +1759,17 @@ extern "C" int kda_kv_append(const kda_kv_pool* kv, const int32_t* page_table, i
       hipLaunchKernelGGL((kda_kv_append_kernel<DT, D, false>), grid, dim3(256), 0, st, a);
     return hipGetLastError();
   }));
+}
+
+extern "C" int kda_kv_append(const kda_kv_pool* kv, const int32_t* page_table, int32_t max_pages,
+                             const int32_t* cu_seqlens, const int32_t* cache_lens, const void* k, const void* v,
+                             int64_t k_stride, int64_t v_stride, const void* q, int64_t q_stride, void* q_out,
+                             const float* cos, const float* sin, int32_t n_positions, int32_t rot_dim,
+                             int32_t interleaved, int32_t n_seq, int64_t n_tokens, int32_t q_heads,
+                             kda_dtype dtype, void* stream) {
+  return kda_kv_append_at(kv, page_table, max_pages, cu_seqlens, cache_lens, k, v, k_stride, v_stride, q, q_stride,
+                          q_out, cos, sin, nullptr, n_positions, rot_dim, interleaved, n_seq, n_tokens, q_heads,
+                          dtype, stream);
 }
 
 extern "C" int kda_kv_read(const kda_kv_pool* kv, const int32_t* page_table, int32_t max_pages,
@@ -1647,22 +1808,29 @@ extern "C" int kda_kv_read(const kda_kv_pool* kv, const int32_t* page_table, int
   }));
 }
 
-extern "C" int kda_kv_attend(const kda_kv_pool* kv, const int32_t* page_table, int32_t max_pages,
-                             const int32_t* cu_seqlens, const int32_t* cache_lens, const void* q,
-                             int64_t q_stride, void* out, int32_t n_seq, int64_t n_tokens, int32_t max_rows,
-                             int64_t max_kv_len, int32_t q_heads, kda_dtype dtype, float scale, void* workspace,
-                             size_t workspace_bytes, void* stream) {
+namespace kda {
+namespace {
+
+// TREE: with a table of parents
+template <bool TREE>
+int attend(const kda_kv_pool* kv, const int32_t* page_table, int32_t max_pages, const int32_t* cu_seqlens,
+           const int32_t* cache_lens, const int32_t* parents, const void* q, int64_t q_stride, void* out,
+           int32_t n_seq, int64_t n_tokens, int32_t max_rows, int64_t max_kv_len, int32_t q_heads, kda_dtype dtype,
+           float scale, void* workspace, size_t workspace_bytes, void* stream) {
   int rc = kv_check(kv, max_pages, n_seq, n_tokens);
   if (rc == KDA_OK) rc = kv_check_attend(kv, n_tokens, max_rows, max_kv_len, q_heads, dtype);
   if (rc != KDA_OK) return rc;
+  if (TREE && max_rows > kMaxNodes) return KDA_ERR_ROWS;
   if (!std::isfinite(scale)) return KDA_ERR_ARG;
   const int size = kv_type_bytes(dtype);
   if (n_seq == 0 || n_tokens == 0) return KDA_OK;
-  if (page_table == nullptr || cu_seqlens == nullptr || cache_lens == nullptr || q == nullptr || out == nullptr)
+  if (page_table == nullptr || cu_seqlens == nullptr || cache_lens == nullptr || q == nullptr || out == nullptr ||
+      (TREE && parents == nullptr))
     return KDA_ERR_NULL;
   if (q_stride < static_cast<int64_t>(q_heads) * kv->D) return KDA_ERR_ARG;
   if (!aligned(kv->base, 16) || !aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 16) ||
-      !aligned(page_table, 4) || !aligned(cu_seqlens, 4) || !aligned(cache_lens, 4) || q_stride * size % 16 != 0)
+      !aligned(page_table, 4) || !aligned(cu_seqlens, 4) || !aligned(cache_lens, 4) || !aligned(parents, 4) ||
+      q_stride * size % 16 != 0)
     return KDA_ERR_ALIGN;
   const size_t need = kda_kv_attend_workspace(kv, max_pages, n_seq, n_tokens, max_rows, max_kv_len, q_heads, dtype);
   if (need > 0 && workspace == nullptr) return KDA_ERR_NULL;
@@ -1686,6 +1854,8 @@ extern "C" int kda_kv_attend(const kda_kv_pool* kv, const int32_t* page_table, i
   // zero is.
   a.scale = std::fmin(std::fmax(std::fabs(scale) * 1.44269504088896340736f, 0x1p-149f), FLT_MAX);
   a.sign = scale < 0.0f ? -1.0f : 1.0f;
+  a.parents = parents;
+  a.most_rows = TREE ? kMaxNodes : INT32_MAX;
   a.part = static_cast<float*>(workspace);
   a.part_ml = a.part == nullptr ? nullptr : a.part + static_cast<int64_t>(p.n_splits) * n_tokens * q_heads * kv->D;
   const int64_t tiles = kv_tiles(p, n_seq, kv->H);
@@ -1694,14 +1864,25 @@ extern "C" int kda_kv_attend(const kda_kv_pool* kv, const int32_t* page_table, i
   return status(by_type(dtype, kv->D, [&](auto t, auto d) {
     constexpr int DT = decltype(t)::value, D = decltype(d)::value;
     const dim3 grid(static_cast<uint32_t>(tiles * p.n_splits));
-    if (p.tile_rows == kTileRows)
-      hipLaunchKernelGGL((kda_kv_tiles_kernel<DT, D>), grid, dim3(256), 0, st, a);
-    else if (p.waves == 8)
-      hipLaunchKernelGGL((kda_kv_rows_kernel<DT, D, 1, 8>), grid, dim3(512), 0, st, a);
-    else if (DT == KDA_F32 || p.tile_rows == 16)
-      hipLaunchKernelGGL((kda_kv_rows_kernel<DT, D, 1, 4>), grid, dim3(256), 0, st, a);
-    else if constexpr (DT != KDA_F32)
-      hipLaunchKernelGGL((kda_kv_rows_kernel<DT, D, 2, 4>), grid, dim3(256), 0, st, a);
+    if constexpr (TREE) {
+      if (p.tile_rows == kTileRows)
+        hipLaunchKernelGGL((kda_kv_tree_tiles_kernel<DT, D>), grid, dim3(256), 0, st, a);
+      else if (p.waves == 8)
+        hipLaunchKernelGGL((kda_kv_tree_rows_kernel<DT, D, 1, 8>), grid, dim3(512), 0, st, a);
+      else if (DT == KDA_F32 || p.tile_rows == 16)
+        hipLaunchKernelGGL((kda_kv_tree_rows_kernel<DT, D, 1, 4>), grid, dim3(256), 0, st, a);
+      else if constexpr (DT != KDA_F32)
+        hipLaunchKernelGGL((kda_kv_tree_rows_kernel<DT, D, 2, 4>), grid, dim3(256), 0, st, a);
+    } else {
+      if (p.tile_rows == kTileRows)
+        hipLaunchKernelGGL((kda_kv_tiles_kernel<DT, D>), grid, dim3(256), 0, st, a);
+      else if (p.waves == 8)
+        hipLaunchKernelGGL((kda_kv_rows_kernel<DT, D, 1, 8>), grid, dim3(512), 0, st, a);
+      else if (DT == KDA_F32 || p.tile_rows == 16)
+        hipLaunchKernelGGL((kda_kv_rows_kernel<DT, D, 1, 4>), grid, dim3(256), 0, st, a);
+      else if constexpr (DT != KDA_F32)
+        hipLaunchKernelGGL((kda_kv_rows_kernel<DT, D, 2, 4>), grid, dim3(256), 0, st, a);
+    }
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && p.n_splits > 1) {
       // up to 8 splits a row in two rounds of loads, more side by side
@@ -1720,4 +1901,55 @@ extern "C" int kda_kv_attend(const kda_kv_pool* kv, const int32_t* page_table, i
     }
     return e;
   }));
+}
+
+}  // namespace
+}  // namespace kda
+
+extern "C" int kda_kv_attend(const kda_kv_pool* kv, const int32_t* page_table, int32_t max_pages,
+                             const int32_t* cu_seqlens, const int32_t* cache_lens, const void* q,
+                             int64_t q_stride, void* out, int32_t n_seq, int64_t n_tokens, int32_t max_rows,
+                             int64_t max_kv_len, int32_t q_heads, kda_dtype dtype, float scale, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  return attend<false>(kv, page_table, max_pages, cu_seqlens, cache_lens, nullptr, q, q_stride, out, n_seq, n_tokens,
+                       max_rows, max_kv_len, q_heads, dtype, scale, workspace, workspace_bytes, stream);
+}
+
+extern "C" int kda_kv_attend_tree(const kda_kv_pool* kv, const int32_t* page_table, int32_t max_pages,
+                                  const int32_t* cu_seqlens, const int32_t* cache_lens, const int32_t* parents,
+                                  const void* q, int64_t q_stride, void* out, int32_t n_seq, int64_t n_tokens,
+                                  int32_t max_rows, int64_t max_kv_len, int32_t q_heads, kda_dtype dtype, float scale,
+                                  void* workspace, size_t workspace_bytes, void* stream) {
+  return attend<true>(kv, page_table, max_pages, cu_seqlens, cache_lens, parents, q, q_stride, out, n_seq, n_tokens,
+                      max_rows, max_kv_len, q_heads, dtype, scale, workspace, workspace_bytes, stream);
+}
+
+extern "C" int kda_kv_keep(const kda_kv_pool* kv, const int32_t* page_table, int32_t max_pages,
+                           const int32_t* cu_seqlens, const int32_t* cache_lens, const int32_t* path,
+                           int32_t max_path, const int32_t* path_lens, int32_t n_seq, int64_t n_tokens,
+                           void* stream) {
+  const int rc = kv_check(kv, max_pages, n_seq, n_tokens);
+  if (rc != KDA_OK) return rc;
+  if (max_path < 1 || max_path > kMaxNodes) return KDA_ERR_ROWS;
+  if (n_seq == 0 || n_tokens == 0) return KDA_OK;
+  if (page_table == nullptr || cu_seqlens == nullptr || cache_lens == nullptr || path == nullptr ||
+      path_lens == nullptr)
+    return KDA_ERR_NULL;
+  if (!aligned(kv->base, 16) || !aligned(page_table, 4) || !aligned(cu_seqlens, 4) || !aligned(cache_lens, 4) ||
+      !aligned(path, 4) || !aligned(path_lens, 4))
+    return KDA_ERR_ALIGN;
+  KvKeepArgs a;
+  a.t = make_tables(kv, page_table, max_pages, cu_seqlens, cache_lens, n_seq, n_tokens);
+  a.path = path;
+  a.lens = path_lens;
+  a.max_path = max_path;
+  const int64_t blocks = (static_cast<int64_t>(n_seq) * kv->H + 3) / 4;
+  if (blocks > kKvMaxBlocks) return KDA_ERR_ARG;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const dim3 grid(static_cast<uint32_t>(blocks));
+  if (kv->D == 128)
+    hipLaunchKernelGGL((kda_kv_keep_kernel<128>), grid, dim3(256), 0, st, a);
+  else
+    hipLaunchKernelGGL((kda_kv_keep_kernel<64>), grid, dim3(256), 0, st, a);
+  return status(hipGetLastError());
 }
