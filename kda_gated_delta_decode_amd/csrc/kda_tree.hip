@@ -22,10 +22,16 @@
 namespace kda {
 namespace {
 
-using f16v = float __attribute__((ext_vector_type(16)));
-
 // sum over 16 lanes, in each of them
 __device__ __forceinline__ float sum16(float x) { return sum_xor8(sum_xor4(sum_xor2(sum_xor1(x)))); }
+
+// the larger of 16 lanes' x >= 0, in each of them
+__device__ __forceinline__ float max16(float x) {
+  x = fmaxf(x, dpp<kDppQuadXor1>(x));
+  x = fmaxf(x, dpp<kDppQuadXor2>(x));
+  x = fmaxf(x, dpp<kDppQuadXor3>(dpp<kDppRowHalfMirror>(x)));
+  return fmaxf(x, dpp<kDppRowRor8>(x));
+}
 
 template <int DT>
 using Stored = std::conditional_t<DT == KDA_F32, float, _Float16>;
@@ -36,224 +42,323 @@ constexpr int kLd = 132;  // floats between rows in LDS: neighbouring rows start
 // Trees
 // ---------------------------------------------------------------------------
 
-// What node i takes from a node on its path.
-struct Pair {
-  float c, d;  // a k_i . k_j and a q_i . k_j
-  int row;     // j's place in LDS
-  int pad;
-};
+// A row of the left operand, its 128 numbers held by 16 lanes (channels 4 l16.. and
+// 64 + 4 l16..).  HALF: in two fp16 pieces of 11 bits, after division by the row's
+// power of two, the second one 2^11 times larger so that it is no subnormal: 22
+// bits of every number down to 2^-14 of the row's largest, 2^-36 of that below;
+// what the pieces miss is less than the products' own fp32 sums round away.
+template <bool HALF>
+__device__ __forceinline__ void put_row(float* row, float* size, const float (&w)[8], bool some) {
+  const int l16 = threadIdx.x % 16;
+  if constexpr (HALF) {
+    float most = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(w[e]));
+    most = max16(most);
+    int ex = __float_as_int(most) >> 23;
+    ex = ex < 1 ? 1 : ex > 253 ? 253 : ex;
+    const float down = __int_as_float((254 - ex) << 23);
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      h4 hi, lo;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x = some ? w[4 * p + e] * down : 0.0f;
+        hi[e] = static_cast<_Float16>(x);
+        lo[e] = static_cast<_Float16>((x - static_cast<float>(hi[e])) * 2048.0f);
+      }
+      *reinterpret_cast<h4*>(reinterpret_cast<_Float16*>(row) + 64 * p + 4 * l16) = hi;
+      *reinterpret_cast<h4*>(reinterpret_cast<_Float16*>(row) + 128 + 64 * p + 4 * l16) = lo;
+    }
+    if (l16 == 0) *size = __int_as_float(ex << 23);
+  } else {
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      f4 x;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = some ? w[4 * p + e] : 0.0f;
+      *reinterpret_cast<f4*>(row + 64 * p + 4 * l16) = x;
+    }
+  }
+}
 
-template <int NB>
-constexpr int tree_threads() { return NB == 64 ? 512 : 256; }
+// 16 rows of the left operand times the wave's 16 columns of the state; a lane gets
+// rows 4 (lane / 16) + e of column lane % 16.
+template <bool HALF, typename T, int N, int RUN>
+__device__ __forceinline__ f4 product(const float* rows, const float* sizes, const T (&S)[N][RUN]) {
+  const int lane = threadIdx.x % 64, quarter = lane / 16;
+  f4 hi = {0, 0, 0, 0};
+  if constexpr (HALF) {
+    f4 lo = {0, 0, 0, 0};
+    const _Float16* from = reinterpret_cast<const _Float16*>(rows + (lane % 16) * kLd) + 8 * quarter;
+#pragma unroll
+    for (int kk = 0; kk < N; ++kk) {
+      h8 s;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[j] = S[kk][j];
+      hi = __builtin_amdgcn_mfma_f32_16x16x32_f16(*reinterpret_cast<const h8*>(from + 32 * kk), s, hi, 0, 0, 0);
+      lo = __builtin_amdgcn_mfma_f32_16x16x32_f16(*reinterpret_cast<const h8*>(from + 128 + 32 * kk), s, lo, 0, 0, 0);
+    }
+    const f4 size = *reinterpret_cast<const f4*>(sizes + 4 * quarter);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) hi[e] = fmaf(lo[e], 0x1p-11f, hi[e]) * size[e];
+  } else {
+    const float* from = rows + (lane % 16) * kLd + 4 * quarter;
+#pragma unroll
+    for (int kk = 0; kk < N; ++kk) {
+      const f4 x = *reinterpret_cast<const f4*>(from + 16 * kk);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) hi = __builtin_amdgcn_mfma_f32_16x16x4f32(x[e], S[kk][e], hi, 0, 0, 0);
+    }
+  }
+  return hi;
+}
 
-// A workgroup for a request and head, up to NB nodes.
-template <int DT, int NB>
-__global__ __launch_bounds__(tree_threads<NB>()) void kda_tree_kernel(TreeArgs a) {
-  constexpr int NT = tree_threads<NB>(), NW = NT / 64;
-  constexpr int GROUPS = NT / 16, PER = NB / GROUPS;  // 16 lanes a node, PER nodes each
-  constexpr int SETS = NW / 4;                        // waves that share 32 columns
-  constexpr int TILES = NB / 16 / SETS;               // 16-node tiles of a wave
-  constexpr int SOLVE = NT / 128;                     // lanes of a column in the solve
-  constexpr int PAIRS = NB * (NB + 1) / 2;
-  // first the keys (rows 0..NB) and decays; then the 2 NB decayed vectors; then
-  // a row of right-hand sides for each node, which become beta u
-  __shared__ __attribute__((aligned(16))) float x_sh[2 * NB * kLd];
-  __shared__ __attribute__((aligned(16))) Pair pair_sh[PAIRS];
-  __shared__ int parent_sh[64];
+// What a node takes from a node above it: a k_i . k_j and a q_i . k_j.
+using Pair = f2;
+
+constexpr int kTreeThreads = 512;
+
+// Node i's pairs start at a multiple of 4, behind those of the nodes before it, of
+// which node m has at most m.
+KDA_HD constexpr int first_pair(int i) {
+  const int c = (i - 1) / 4, r = (i - 1) % 4;
+  return i < 1 ? 0 : 4 * (2 * c * (c + 1) + r * (c + 1));
+}
+// LDS for nb nodes: keys and decays, then the decayed vectors as operands, then
+// right-hand sides (which become beta u) and the queries' products; pairs, and
+// their j.
+constexpr int tree_rows_bytes(int nb) { return 2 * nb * kLd * 4; }
+constexpr int tree_lds_bytes(int nb) { return tree_rows_bytes(nb) + 9 * first_pair(nb + 1); }
+
+// A workgroup for a request and head; nb: its places for nodes, a multiple of 16.
+// Sixteen lanes a node up to the product, 32 PER nodes in all; from there a wave has
+// 16 value columns of its own, and no other needs what it writes.
+template <int DT, int PER>
+__global__ __launch_bounds__(kTreeThreads, 4) void kda_tree_kernel(TreeArgs a, int nb) {
+  constexpr int GROUPS = kTreeThreads / 16;
+  constexpr int TILES = 2 * PER;  // of 16 nodes
+  constexpr bool HALF = DT == KDA_F16;
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  float* x_sh = reinterpret_cast<float*>(lds);
+  Pair* pair_sh = reinterpret_cast<Pair*>(lds + tree_rows_bytes(nb));
+  uint8_t* from_sh = reinterpret_cast<uint8_t*>(pair_sh + first_pair(nb + 1));
+  __shared__ uint64_t path_sh[64];
+  __shared__ __attribute__((aligned(16))) float size_sh[128];  // HALF: the operand's rows' powers of two
+  __shared__ float self_sh[64], beta_sh[64];                   // q_i . k_i; beta
 
   const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
   const int h = blockIdx.x % a.H, r = blockIdx.x / a.H;
+  const int slot = a.init_ids[r];
   const Nodes t = nodes_of(a.cu, r, a.n_tokens);
   if (t.n == 0) return;
-  const int slot = a.init_ids[r];
-  const int64_t step = static_cast<int64_t>(a.H) * 128;           // between nodes
+  const int64_t step = static_cast<int64_t>(a.H) * 128;              // between nodes
   const int64_t row0 = t.n0 * step + static_cast<int64_t>(h) * 128;  // node 0's
-  const bool fits = t.n <= NB && t.n <= a.max_nodes;
+  const bool fits = t.n <= a.max_nodes, placed = slot >= 0 && slot < a.n_slots;
   const int n = fits ? t.n : 0;
+
+  // -- everything is asked for before anything is waited for: parents, gates,
+  // nodes (channels 4 l16.. and 64 + 4 l16.. of a lane), the state
   const int parent = lane < n ? a.parents[t.n0 + lane] : -1;
-  bool bad;
-  const uint64_t above = tree_paths(parent, n, &bad);
-  if (!fits || bad || slot < 0 || slot >= a.n_slots) {
-    for (int64_t i = tid; i < static_cast<int64_t>(t.n) * 128; i += NT)
-      a.out[row0 + i / 128 * step + i % 128] = __builtin_nanf("");
-    return;
-  }
-  // places of the nodes' pairs: lane i has node i's first, and their number
-  const int count = lane < n ? __popcll(above) : 0;
-  int first = count;
-#pragma unroll
-  for (int m = 1; m < 64; m *= 2) {
-    const int y = __shfl_up(first, m);
-    first = lane >= m ? first + y : first;
-  }
-  first -= count;
-  if (wave == 0) parent_sh[lane] = parent;
-  const float beta = lane < n ? 1.0f / (1.0f + expf(-a.b[(t.n0 + lane) * a.H + h])) : 0.0f;
-
-  // -- the state's columns 32 (wave % 4).., one a lane: rows 8 kk + 4 half + j
-  const int half = lane / 32, col = 32 * (wave % 4) + lane % 32;
-  const Stored<DT>* S0 = static_cast<const Stored<DT>*>(a.pool) + (static_cast<int64_t>(slot) * a.H + h) * 128 * 128;
-  float S[64];
-#pragma unroll
-  for (int i = 0; i < 64; ++i) S[i] = static_cast<float>(S0[(8 * (i / 4) + 4 * half + i % 4) * 128 + col]);
-
-  // -- nodes: 16 lanes each, channels 4 l16.. and 64 + 4 l16..
+  const float gate = lane < n ? a.b[(t.n0 + lane) * a.H + h] : 0.0f;
   const int l16 = tid % 16;
-  float wk[PER][8], wq[PER][8];
+  f4 x[PER][2], y[PER][2], z[PER][2];
 #pragma unroll
   for (int m = 0; m < PER; ++m) {
     const int i = tid / 16 + GROUPS * m;
     const int64_t at = row0 + (i < n ? i : 0) * step + 4 * l16;
-    f4 x[2], y[2], z[2];
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
-      x[p] = *reinterpret_cast<const f4*>(a.k + at + 64 * p);
-      y[p] = *reinterpret_cast<const f4*>(a.q + at + 64 * p);
-      z[p] = *reinterpret_cast<const f4*>(a.g + at + 64 * p);
+      x[m][p] = *reinterpret_cast<const f4*>(a.k + at + 64 * p);
+      y[m][p] = *reinterpret_cast<const f4*>(a.q + at + 64 * p);
+      z[m][p] = *reinterpret_cast<const f4*>(a.g + at + 64 * p);
     }
+  }
+  // the wave's 16 columns, one a lane: as they go into the products, rows 16 kk + 4
+  // quarter + j of fp32, 32 kk + 8 quarter + j of fp16
+  const int quarter = lane / 16, col = 16 * wave + lane % 16;
+  const Stored<DT>* S0 =
+      static_cast<const Stored<DT>*>(a.pool) + (static_cast<int64_t>(placed ? slot : 0) * a.H + h) * 128 * 128 + col;
+  constexpr int RUN = HALF ? 8 : 4;
+  Stored<DT> S[128 / (4 * RUN)][RUN];
+#pragma unroll
+  for (int kk = 0; kk < 128 / (4 * RUN); ++kk)
+#pragma unroll
+    for (int j = 0; j < RUN; ++j) S[kk][j] = S0[(4 * RUN * kk + RUN * quarter + j) * 128];
+  __builtin_amdgcn_sched_barrier(0);
+
+  bool bad;
+  const uint64_t above = tree_paths(parent, n, &bad);
+  if (!fits || bad || !placed) {
+    for (int64_t i = tid; i < static_cast<int64_t>(t.n) * 128; i += kTreeThreads)
+      a.out[row0 + i / 128 * step + i % 128] = __builtin_nanf("");
+    return;
+  }
+  const int depth_of = __popcll(above) - 1;
+  if (wave == 0) {
+    path_sh[lane] = above;
+    beta_sh[lane] = 1.0f / (1.0f + expf(-gate));
+  }
+
+  // -- lengths, decays
+  float wk[PER][8], wq[PER][8];
+#pragma unroll
+  for (int m = 0; m < PER; ++m) {
+    const int i = tid / 16 + GROUPS * m;
     float kk = 0.0f, qq = 0.0f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      kk = fmaf(x[e / 4][e % 4], x[e / 4][e % 4], kk);
-      qq = fmaf(y[e / 4][e % 4], y[e / 4][e % 4], qq);
+      kk = fmaf(x[m][e / 4][e % 4], x[m][e / 4][e % 4], kk);
+      qq = fmaf(y[m][e / 4][e % 4], y[m][e / 4][e % 4], qq);
     }
     const float kn = 1.0f / sqrtf(sum16(kk) + 1e-6f), qn = 1.0f / sqrtf(sum16(qq) + 1e-6f);
     float dot = 0.0f;
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      f4 dec;
+    for (int p = 0; p < 2; ++p)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        x[p][e] *= kn;
-        y[p][e] *= qn;
-        dec[e] = expf(z[p][e]);
-        dot = fmaf(x[p][e], y[p][e], dot);
-        wk[m][4 * p + e] = x[p][e] * dec[e];
-        wq[m][4 * p + e] = y[p][e] * dec[e];
+        x[m][p][e] *= kn;
+        y[m][p][e] *= qn;
+        z[m][p][e] = expf(z[m][p][e]);
+        dot = fmaf(x[m][p][e], y[m][p][e], dot);
+        wk[m][4 * p + e] = x[m][p][e] * z[m][p][e];
+        wq[m][4 * p + e] = y[m][p][e] * z[m][p][e];
       }
-      *reinterpret_cast<f4*>(x_sh + i * kLd + 64 * p + 4 * l16) = x[p];
-      *reinterpret_cast<f4*>(x_sh + (NB + i) * kLd + 64 * p + 4 * l16) = dec;
-    }
     dot = sum16(dot);
-    const int at_pair = __shfl(first, i % 64);
-    if (l16 == 0 && i < n) pair_sh[at_pair] = Pair{0.0f, dot, i * kLd, 0};
+    if (i < n) {
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        *reinterpret_cast<f4*>(x_sh + i * kLd + 64 * p + 4 * l16) = x[m][p];
+        *reinterpret_cast<f4*>(x_sh + (nb + i) * kLd + 64 * p + 4 * l16) = z[m][p];
+      }
+      if (l16 == 0) self_sh[i] = dot;
+    }
   }
   __syncthreads();
 
-  // -- up the tree: at each node above, the products with its key, then its decay
+  // -- up the tree: at each node above, the products with its key, then its decay.
+  // A path's nodes are the bits of a word, the lowest node the highest bit.
 #pragma unroll
   for (int m = 0; m < PER; ++m) {
     const int i = tid / 16 + GROUPS * m;
-    int at_pair = __shfl(first, i % 64) + 1;
-    int j = i < n ? parent_sh[i] : -1;
-    while (__ballot(j >= 0) != 0) {
-      const int from = j < 0 ? 0 : j;
-      float c = 0.0f, d = 0.0f;
+    uint64_t way = i < n ? path_sh[i] & ~(1ull << i) : 0;
+    int at = first_pair(i);
+    while (__ballot(way != 0) != 0) {
+      const int j = way == 0 ? 0 : 63 - __builtin_clzll(way);
       f4 key[2], dec[2];
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
-        key[p] = *reinterpret_cast<const f4*>(x_sh + from * kLd + 64 * p + 4 * l16);
-        dec[p] = *reinterpret_cast<const f4*>(x_sh + (NB + from) * kLd + 64 * p + 4 * l16);
+        key[p] = *reinterpret_cast<const f4*>(x_sh + j * kLd + 64 * p + 4 * l16);
+        dec[p] = *reinterpret_cast<const f4*>(x_sh + (nb + j) * kLd + 64 * p + 4 * l16);
       }
-      const int next = parent_sh[from];
+      f2 c = {0.0f, 0.0f}, d = {0.0f, 0.0f};
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        c = fmaf(wk[m][e], key[e / 4][e % 4], c);
-        d = fmaf(wq[m][e], key[e / 4][e % 4], d);
+        c[e % 2] = fmaf(wk[m][e], key[e / 4][e % 4], c[e % 2]);
+        d[e % 2] = fmaf(wq[m][e], key[e / 4][e % 4], d[e % 2]);
       }
-      c = sum16(c);
-      d = sum16(d);
-      if (j >= 0) {
-        if (l16 == 0) pair_sh[at_pair] = Pair{c, d, j * kLd, 0};
+      const float cs = sum16(c[0] + c[1]), ds = sum16(d[0] + d[1]);
+      if (way != 0) {
+        if (l16 == 0) {
+          pair_sh[at] = Pair{cs, ds};
+          from_sh[at] = static_cast<uint8_t>(j);
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           wk[m][e] *= dec[e / 4][e % 4];
           wq[m][e] *= dec[e / 4][e % 4];
         }
+        way &= ~(1ull << j);
       }
-      ++at_pair;
-      j = j < 0 ? -1 : next;
+      ++at;
     }
   }
   __syncthreads();
-  // -- the decayed vectors as rows of the left operand: 32 of a tile, 16 nodes'
-  // keys, then their queries
+  // -- the decayed vectors as rows of the left operand: 16 nodes' keys, then their
+  // queries
+  const int tiles = (n + 15) / 16;
 #pragma unroll
   for (int m = 0; m < PER; ++m) {
     const int i = tid / 16 + GROUPS * m;
-    float* to = x_sh + (32 * (i / 16) + i % 16) * kLd + 4 * l16;
-#pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      const bool some = i < n;
-      f4 x, y;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = some ? wk[m][4 * p + e] : 0.0f, y[e] = some ? wq[m][4 * p + e] : 0.0f;
-      *reinterpret_cast<f4*>(to + 64 * p) = x;
-      *reinterpret_cast<f4*>(to + 16 * kLd + 64 * p) = y;
+    if (i < 16 * tiles) {
+      const int to = 32 * (i / 16) + i % 16;
+      put_row<HALF>(x_sh + to * kLd, size_sh + to, wk[m], i < n);
+      put_row<HALF>(x_sh + (to + 16) * kLd, size_sh + to + 16, wq[m], i < n);
     }
   }
-  __syncthreads();
-
-  // -- products with the state.  Result e of a lane: row 8 (e / 4) + 4 half + e % 4
-  // of the tile, so e < 8 is a node's key and e + 8 its query.
-  const int set = wave / 4;
-  f16v acc[TILES];
-#pragma unroll
-  for (int m = 0; m < TILES; ++m) {
-    const int tile = SETS * m + set;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) acc[m][e] = 0.0f;
-    if (16 * tile < n) {
-      const float* from = x_sh + (32 * tile + lane % 32) * kLd + 4 * half;
-#pragma unroll
-      for (int kk = 0; kk < 16; ++kk) {
-        const f4 w = *reinterpret_cast<const f4*>(from + 8 * kk);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          acc[m] = __builtin_amdgcn_mfma_f32_32x32x2f32(w[e], S[4 * kk + e], acc[m], 0, 0, 0);
-      }
-    }
-  }
-  __syncthreads();
+  // (the values are on their way while the products run)
+  float v[TILES][4];
 #pragma unroll
   for (int m = 0; m < TILES; ++m)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int i = 16 * (SETS * m + set) + 8 * (e / 4) + 4 * half + e % 4;
-      if (i < n) x_sh[i * kLd + col] = a.v[row0 + i * step + col] - acc[m][e];
+    for (int e = 0; e < 4; ++e) {
+      const int i = 16 * m + 4 * quarter + e;
+      v[m][e] = a.v[row0 + (i < n ? i : 0) * step + col];
     }
   __syncthreads();
 
-  // -- the solve: SOLVE lanes a column share a node's sum, node after node
-  {
-    constexpr int COLS = 64 / SOLVE;
-    const int mine = COLS * wave + lane % COLS, part = lane / COLS;
-    for (int i = 0; i < n; ++i) {
-      const int at = __builtin_amdgcn_readlane(first, i), end = at + __builtin_amdgcn_readlane(count, i);
-      float s = 0.0f;
-      for (int e = at + 1 + part; e < end; e += SOLVE) s = fmaf(pair_sh[e].c, x_sh[pair_sh[e].row + mine], s);
-      if constexpr (SOLVE == 4) s = sum_xor16(s);
-      s = sum_xor32(s);
-      const float b = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(beta), i));
-      const float u = b * (x_sh[i * kLd + mine] - s);
-      if (part == 0) x_sh[i * kLd + mine] = u;
-    }
-  }
-  __syncthreads();
-
-  // -- read-outs
+  // -- products with the state: a lane gets its column of nodes 4 quarter + e of a tile
+  f4 pk[TILES], pq[TILES];
 #pragma unroll
   for (int m = 0; m < TILES; ++m)
+    if (m < tiles) {
+      pk[m] = product<HALF>(x_sh + 32 * m * kLd, size_sh + 32 * m, S);
+      pq[m] = product<HALF>(x_sh + (32 * m + 16) * kLd, size_sh + 32 * m + 16, S);
+    }
+  __syncthreads();
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int i = 16 * (SETS * m + set) + 8 * (e / 4) + 4 * half + e % 4;
-      const int at = __shfl(first, i % 64), end = at + __shfl(count, i % 64);
-      if (i < n) {
-        float s = acc[m][8 + e];
-        for (int p = at; p < end; ++p) s = fmaf(pair_sh[p].d, x_sh[pair_sh[p].row + col], s);
-        a.out[row0 + i * step + col] = a.scale * s;
+  for (int m = 0; m < TILES; ++m)
+    if (m < tiles)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = 16 * m + 4 * quarter + e;
+        x_sh[i * kLd + col] = v[m][e] - pk[m][e];
+        x_sh[(nb + i) * kLd + col] = pq[m][e];
+      }
+
+  // -- the solve, level after level (level's nodes have as many above them): four
+  // nodes at a time; below level 4 one or two share the four lanes of a column
+  for (int level = 0;; ++level) {
+    uint64_t rest = __ballot(lane < n && depth_of == level);
+    if (rest == 0) break;
+    while (rest != 0) {
+      const int left = __popcll(rest), parts = level <= 4 || left >= 3 ? 1 : left == 2 ? 2 : 4;
+      int node = -1;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int b = rest != 0 ? __builtin_ctzll(rest) : -1;
+        if (g < 4 / parts) {
+          node = quarter / parts == g ? b : node;
+          rest &= rest - 1;  // (0 stays 0)
+        }
+      }
+      const int i = node < 0 ? 0 : node, part = quarter % parts, at = first_pair(i);
+      float* row = x_sh + i * kLd + col;
+      const float b = beta_sh[i], self = self_sh[i], rhs = row[0], pq_i = row[nb * kLd];
+      f2 s = {0.0f, 0.0f};
+      for (int e = 4 * part; e < level; e += 4 * parts) {
+        const uint32_t from = *reinterpret_cast<const uint32_t*>(from_sh + at + e);
+        f4 p[2];
+        p[0] = *reinterpret_cast<const f4*>(pair_sh + at + e);
+        p[1] = *reinterpret_cast<const f4*>(pair_sh + at + e + 2);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const bool some = e + q < level;
+          const float u = x_sh[(some ? (from >> (8 * q)) & 0xFF : 0) * kLd + col];
+          const float c = p[q / 2][2 * (q % 2)], d = p[q / 2][2 * (q % 2) + 1];
+          s[0] = some ? fmaf(c, u, s[0]) : s[0];
+          s[1] = some ? fmaf(d, u, s[1]) : s[1];
+        }
+      }
+      if (parts > 1) s = f2{sum_xor16(s[0]), sum_xor16(s[1])};
+      if (parts > 2) s = f2{sum_xor32(s[0]), sum_xor32(s[1])};
+      const float u = b * (rhs - s[0]);
+      if (node >= 0 && part == 0) {
+        row[0] = u;
+        a.out[row0 + i * step + col] = a.scale * (pq_i + fmaf(self, u, s[1]));
       }
     }
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -381,13 +486,18 @@ bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p)
 template <int DT>
 hipError_t launch_tree(const TreeArgs& a, hipStream_t st) {
   const dim3 grid(static_cast<uint32_t>(a.n_req) * a.H);
-  if (a.max_nodes <= 16)
-    hipLaunchKernelGGL((kda_tree_kernel<DT, 16>), grid, dim3(tree_threads<16>()), 0, st, a);
-  else if (a.max_nodes <= 32)
-    hipLaunchKernelGGL((kda_tree_kernel<DT, 32>), grid, dim3(tree_threads<32>()), 0, st, a);
-  else
-    hipLaunchKernelGGL((kda_tree_kernel<DT, 64>), grid, dim3(tree_threads<64>()), 0, st, a);
-  return hipGetLastError();
+  const int nb = a.max_nodes < 1 ? 16 : (a.max_nodes + 15) / 16 * 16;
+  const auto launch = [&](auto kernel) {
+    // (more than 64 KiB of LDS has to be asked for)
+    hipError_t e = hipSuccess;
+    if (tree_lds_bytes(nb) > 65536)
+      e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
+                              tree_lds_bytes(nb));
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(kernel, grid, dim3(kTreeThreads), tree_lds_bytes(nb), st, a, nb);
+    return hipGetLastError();
+  };
+  return nb <= 32 ? launch(kda_tree_kernel<DT, 1>) : launch(kda_tree_kernel<DT, 2>);
 }
 
 // threads of a launch stay below 2^32 for the widest workgroup
