@@ -33,6 +33,15 @@ __device__ __forceinline__ float max16(float x) {
   return fmaxf(x, dpp<kDppRowRor8>(x));
 }
 
+// e^x for x below 88, within 2 units of the last place (0 below 2^-126): 2^t, with
+// what rounding x log2(e) to t lost put back.
+__device__ __forceinline__ float exp_near(float x) {
+  const float t = x * 1.44269504f;
+  const float lost = fmaf(x, 1.44269504f, -t) + x * 1.92596299e-8f;
+  const float y = __builtin_amdgcn_exp2f(t);
+  return fmaf(y, lost * 0.693147181f, y);
+}
+
 template <int DT>
 using Stored = std::conditional_t<DT == KDA_F32, float, _Float16>;
 
@@ -57,15 +66,14 @@ __device__ __forceinline__ void put_row(float* row, float* size, const float (&w
     most = max16(most);
     int ex = __float_as_int(most) >> 23;
     ex = ex < 1 ? 1 : ex > 253 ? 253 : ex;
-    const float down = __int_as_float((254 - ex) << 23);
+    const float down = some ? __int_as_float((254 - ex) << 23) : 0.0f, up = 2048.0f * down;
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
       h4 hi, lo;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float x = some ? w[4 * p + e] * down : 0.0f;
-        hi[e] = static_cast<_Float16>(x);
-        lo[e] = static_cast<_Float16>((x - static_cast<float>(hi[e])) * 2048.0f);
+        hi[e] = static_cast<_Float16>(w[4 * p + e] * down);
+        lo[e] = static_cast<_Float16>(fmaf(static_cast<float>(hi[e]), -2048.0f, w[4 * p + e] * up));
       }
       *reinterpret_cast<h4*>(reinterpret_cast<_Float16*>(row) + 64 * p + 4 * l16) = hi;
       *reinterpret_cast<h4*>(reinterpret_cast<_Float16*>(row) + 128 + 64 * p + 4 * l16) = lo;
@@ -122,8 +130,7 @@ constexpr int kTreeThreads = 512;
 // Node i's pairs start at a multiple of 4, behind those of the nodes before it, of
 // which node m has at most m.
 KDA_HD constexpr int first_pair(int i) {
-  const int c = (i - 1) / 4, r = (i - 1) % 4;
-  return i < 1 ? 0 : 4 * (2 * c * (c + 1) + r * (c + 1));
+  return i < 1 ? 0 : 4 * ((i - 1) / 4 + 1) * (2 * ((i - 1) / 4) + (i - 1) % 4);
 }
 // LDS for nb nodes: keys and decays, then the decayed vectors as operands, then
 // right-hand sides (which become beta u) and the queries' products; pairs, and
@@ -132,8 +139,8 @@ constexpr int tree_rows_bytes(int nb) { return 2 * nb * kLd * 4; }
 constexpr int tree_lds_bytes(int nb) { return tree_rows_bytes(nb) + 9 * first_pair(nb + 1); }
 
 // A workgroup for a request and head; nb: its places for nodes, a multiple of 16.
-// Sixteen lanes a node up to the product, 32 PER nodes in all; from there a wave has
-// 16 value columns of its own, and no other needs what it writes.
+// Sixteen lanes a node up to the products, 32 PER nodes in all; there a wave has 16
+// value columns, in the solve 64 and four nodes.
 template <int DT, int PER>
 __global__ __launch_bounds__(kTreeThreads, 4) void kda_tree_kernel(TreeArgs a, int nb) {
   constexpr int GROUPS = kTreeThreads / 16;
@@ -145,7 +152,9 @@ __global__ __launch_bounds__(kTreeThreads, 4) void kda_tree_kernel(TreeArgs a, i
   uint8_t* from_sh = reinterpret_cast<uint8_t*>(pair_sh + first_pair(nb + 1));
   __shared__ uint64_t path_sh[64];
   __shared__ __attribute__((aligned(16))) float size_sh[128];  // HALF: the operand's rows' powers of two
-  __shared__ float self_sh[64], beta_sh[64];                   // q_i . k_i; beta
+  // nodes level by level (those with as many above them): beta, q_i . k_i, i, the
+  // place of its pairs
+  __shared__ f4 node_sh[64];
 
   const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
   const int h = blockIdx.x % a.H, r = blockIdx.x / a.H;
@@ -163,8 +172,11 @@ __global__ __launch_bounds__(kTreeThreads, 4) void kda_tree_kernel(TreeArgs a, i
   const float gate = lane < n ? a.b[(t.n0 + lane) * a.H + h] : 0.0f;
   const int l16 = tid % 16;
   f4 x[PER][2], y[PER][2], z[PER][2];
+  // a wave's four nodes of a share; without one of the tree it passes it by
+  const auto has = [&](int m) __attribute__((always_inline)) { return 4 * wave + GROUPS * m < n; };
 #pragma unroll
   for (int m = 0; m < PER; ++m) {
+    if (!has(m)) break;
     const int i = tid / 16 + GROUPS * m;
     const int64_t at = row0 + (i < n ? i : 0) * step + 4 * l16;
 #pragma unroll
@@ -194,16 +206,21 @@ __global__ __launch_bounds__(kTreeThreads, 4) void kda_tree_kernel(TreeArgs a, i
       a.out[row0 + i / 128 * step + i % 128] = __builtin_nanf("");
     return;
   }
-  const int depth_of = __popcll(above) - 1;
-  if (wave == 0) {
-    path_sh[lane] = above;
-    beta_sh[lane] = 1.0f / (1.0f + expf(-gate));
+  const int depth_of = lane < n ? __popcll(above) - 1 : -1;
+  const float beta = 1.0f / (1.0f + expf(-gate));
+  if (wave == 0) path_sh[lane] = above;
+  int rank = 0;  // of lane's node, among the levels
+  for (int level = 0, before = 0; before < n; ++level) {
+    const uint64_t same = __ballot(depth_of == level);
+    if (depth_of == level) rank = before + __builtin_amdgcn_mbcnt_hi(same >> 32, __builtin_amdgcn_mbcnt_lo(same, 0));
+    before += __popcll(same);
   }
 
   // -- lengths, decays
   float wk[PER][8], wq[PER][8];
 #pragma unroll
   for (int m = 0; m < PER; ++m) {
+    if (!has(m)) break;
     const int i = tid / 16 + GROUPS * m;
     float kk = 0.0f, qq = 0.0f;
 #pragma unroll
@@ -211,7 +228,7 @@ __global__ __launch_bounds__(kTreeThreads, 4) void kda_tree_kernel(TreeArgs a, i
       kk = fmaf(x[m][e / 4][e % 4], x[m][e / 4][e % 4], kk);
       qq = fmaf(y[m][e / 4][e % 4], y[m][e / 4][e % 4], qq);
     }
-    const float kn = 1.0f / sqrtf(sum16(kk) + 1e-6f), qn = 1.0f / sqrtf(sum16(qq) + 1e-6f);
+    const float kn = __builtin_amdgcn_rsqf(sum16(kk) + 1e-6f), qn = __builtin_amdgcn_rsqf(sum16(qq) + 1e-6f);
     float dot = 0.0f;
 #pragma unroll
     for (int p = 0; p < 2; ++p)
@@ -219,32 +236,44 @@ __global__ __launch_bounds__(kTreeThreads, 4) void kda_tree_kernel(TreeArgs a, i
       for (int e = 0; e < 4; ++e) {
         x[m][p][e] *= kn;
         y[m][p][e] *= qn;
-        z[m][p][e] = expf(z[m][p][e]);
+        z[m][p][e] = exp_near(z[m][p][e]);
         dot = fmaf(x[m][p][e], y[m][p][e], dot);
         wk[m][4 * p + e] = x[m][p][e] * z[m][p][e];
         wq[m][4 * p + e] = y[m][p][e] * z[m][p][e];
       }
     dot = sum16(dot);
+    const int place = __shfl(rank, i % 64);
+    const float mine = __shfl(beta, i % 64);
     if (i < n) {
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
         *reinterpret_cast<f4*>(x_sh + i * kLd + 64 * p + 4 * l16) = x[m][p];
         *reinterpret_cast<f4*>(x_sh + (nb + i) * kLd + 64 * p + 4 * l16) = z[m][p];
       }
-      if (l16 == 0) self_sh[i] = dot;
+      if (l16 == 0) node_sh[place] = f4{mine, dot, __int_as_float(i), __int_as_float(first_pair(i))};
     }
   }
   __syncthreads();
 
   // -- up the tree: at each node above, the products with its key, then its decay.
   // A path's nodes are the bits of a word, the lowest node the highest bit.
+  uint64_t way[PER];
+  int at[PER];
 #pragma unroll
   for (int m = 0; m < PER; ++m) {
     const int i = tid / 16 + GROUPS * m;
-    uint64_t way = i < n ? path_sh[i] & ~(1ull << i) : 0;
-    int at = first_pair(i);
-    while (__ballot(way != 0) != 0) {
-      const int j = way == 0 ? 0 : 63 - __builtin_clzll(way);
+    way[m] = i < n ? path_sh[i] & ~(1ull << i) : 0;
+    at[m] = first_pair(i);
+  }
+  for (;;) {
+    uint64_t any = 0;
+#pragma unroll
+    for (int m = 0; m < PER; ++m) any |= way[m];
+    if (__ballot(any != 0) == 0) break;
+#pragma unroll
+    for (int m = 0; m < PER; ++m) {
+      if (!has(m)) break;
+      const int j = way[m] == 0 ? 0 : 63 - __builtin_clzll(way[m]);
       f4 key[2], dec[2];
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
@@ -258,19 +287,28 @@ __global__ __launch_bounds__(kTreeThreads, 4) void kda_tree_kernel(TreeArgs a, i
         d[e % 2] = fmaf(wq[m][e], key[e / 4][e % 4], d[e % 2]);
       }
       const float cs = sum16(c[0] + c[1]), ds = sum16(d[0] + d[1]);
-      if (way != 0) {
+      if (way[m] != 0) {
         if (l16 == 0) {
-          pair_sh[at] = Pair{cs, ds};
-          from_sh[at] = static_cast<uint8_t>(j);
+          pair_sh[at[m]] = Pair{cs, ds};
+          from_sh[at[m]] = static_cast<uint8_t>(j);
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           wk[m][e] *= dec[e / 4][e % 4];
           wq[m][e] *= dec[e / 4][e % 4];
         }
-        way &= ~(1ull << j);
+        way[m] &= ~(1ull << j);
+        ++at[m];
       }
-      ++at;
+    }
+  }
+  // (pairs come in fours: nothing of the node's own row behind the last)
+#pragma unroll
+  for (int m = 0; m < PER; ++m) {
+    const int i = tid / 16 + GROUPS * m, none = -at[m] & 3;
+    if (i < n && l16 < none) {
+      pair_sh[at[m] + l16] = Pair{0.0f, 0.0f};
+      from_sh[at[m] + l16] = static_cast<uint8_t>(i);
     }
   }
   __syncthreads();
@@ -280,7 +318,7 @@ __global__ __launch_bounds__(kTreeThreads, 4) void kda_tree_kernel(TreeArgs a, i
 #pragma unroll
   for (int m = 0; m < PER; ++m) {
     const int i = tid / 16 + GROUPS * m;
-    if (i < 16 * tiles) {
+    if (4 * wave + GROUPS * m < 16 * tiles) {
       const int to = 32 * (i / 16) + i % 16;
       put_row<HALF>(x_sh + to * kLd, size_sh + to, wk[m], i < n);
       put_row<HALF>(x_sh + (to + 16) * kLd, size_sh + to + 16, wq[m], i < n);
@@ -316,48 +354,68 @@ __global__ __launch_bounds__(kTreeThreads, 4) void kda_tree_kernel(TreeArgs a, i
         x_sh[(nb + i) * kLd + col] = pq[m][e];
       }
 
-  // -- the solve, level after level (level's nodes have as many above them): four
-  // nodes at a time; below level 4 one or two share the four lanes of a column
-  for (int level = 0;; ++level) {
-    uint64_t rest = __ballot(lane < n && depth_of == level);
-    if (rest == 0) break;
-    while (rest != 0) {
-      const int left = __popcll(rest), parts = level <= 4 || left >= 3 ? 1 : left == 2 ? 2 : 4;
-      int node = -1;
+  // -- the solve and the read-outs, level after level.  A wave takes 64 columns, four a
+  // lane, and each quarter of it a node, so eight waves take 16 nodes of a level at
+  // once; up to four nodes below level 4 have a wave's quarters share each one's sum.
+  __syncthreads();
+  const int c4 = 64 * (wave % 2) + 4 * (lane % 16);
+  char* const out = reinterpret_cast<char*>(a.out + row0 + c4);
+  const uint32_t out_step = static_cast<uint32_t>(4 * step);  // (64 of them are less than 2^30)
+  float* const x_col = x_sh + c4;
+  const auto solve = [&](int level, int at, bool some, int part, auto share) __attribute__((always_inline)) {
+    constexpr bool SHARE = decltype(share)::value;
+    const f4 node = node_sh[at];
+    float* row = x_col + __float_as_int(node[2]) * kLd;
+    int pairs = __float_as_int(node[3]) + 4 * part;
+    f4 u = *reinterpret_cast<const f4*>(row), o = *reinterpret_cast<const f4*>(row + nb * kLd);
+    if (SHARE && part > 0) u = o = f4{0, 0, 0, 0};
+    const auto quad = [&]() __attribute__((always_inline)) {
+      const uint32_t from = *reinterpret_cast<const uint32_t*>(from_sh + pairs);
+      const f4 p0 = *reinterpret_cast<const f4*>(pair_sh + pairs), p1 = *reinterpret_cast<const f4*>(pair_sh + pairs + 2);
+      f4 y[4];
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int b = rest != 0 ? __builtin_ctzll(rest) : -1;
-        if (g < 4 / parts) {
-          node = quarter / parts == g ? b : node;
-          rest &= rest - 1;  // (0 stays 0)
-        }
-      }
-      const int i = node < 0 ? 0 : node, part = quarter % parts, at = first_pair(i);
-      float* row = x_sh + i * kLd + col;
-      const float b = beta_sh[i], self = self_sh[i], rhs = row[0], pq_i = row[nb * kLd];
-      f2 s = {0.0f, 0.0f};
-      for (int e = 4 * part; e < level; e += 4 * parts) {
-        const uint32_t from = *reinterpret_cast<const uint32_t*>(from_sh + at + e);
-        f4 p[2];
-        p[0] = *reinterpret_cast<const f4*>(pair_sh + at + e);
-        p[1] = *reinterpret_cast<const f4*>(pair_sh + at + e + 2);
+      for (int q = 0; q < 4; ++q) y[q] = *reinterpret_cast<const f4*>(x_col + ((from >> (8 * q)) & 0xFF) * kLd);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const bool some = e + q < level;
-          const float u = x_sh[(some ? (from >> (8 * q)) & 0xFF : 0) * kLd + col];
-          const float c = p[q / 2][2 * (q % 2)], d = p[q / 2][2 * (q % 2) + 1];
-          s[0] = some ? fmaf(c, u, s[0]) : s[0];
-          s[1] = some ? fmaf(d, u, s[1]) : s[1];
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float c = q < 2 ? p0[2 * (q % 2)] : p1[2 * (q % 2)], d = q < 2 ? p0[2 * (q % 2) + 1] : p1[2 * (q % 2) + 1];
+          u[k] = fmaf(-c, y[q][k], u[k]);
+          o[k] = fmaf(d, y[q][k], o[k]);
         }
+    };
+    if constexpr (SHARE) {
+      for (int e = 4 * part; e < level; e += 16, pairs += 16) quad();
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        u[k] = sum_xor32(sum_xor16(u[k]));
+        o[k] = sum_xor32(sum_xor16(o[k]));
       }
-      if (parts > 1) s = f2{sum_xor16(s[0]), sum_xor16(s[1])};
-      if (parts > 2) s = f2{sum_xor32(s[0]), sum_xor32(s[1])};
-      const float u = b * (rhs - s[0]);
-      if (node >= 0 && part == 0) {
-        row[0] = u;
-        a.out[row0 + i * step + col] = a.scale * (pq_i + fmaf(self, u, s[1]));
+    } else {
+      for (int e = 0; e < level; e += 4, pairs += 4) quad();
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      u[k] *= node[0];
+      o[k] = a.scale * fmaf(node[1], u[k], o[k]);
+    }
+    if (some) {
+      *reinterpret_cast<f4*>(row) = u;
+      *reinterpret_cast<f4*>(out + __float_as_int(node[2]) * out_step) = o;
+    }
+  };
+  for (int level = 0, place = 0; place < n; ++level) {
+    if (level > 0) __syncthreads();
+    const int end = place + __popcll(__ballot(depth_of == level));
+    if (level > 4 && end - place <= 4) {
+      if (place + wave / 2 < end) solve(level, place + wave / 2, quarter == 0, quarter, std::true_type{});
+    } else {
+      for (int at = place + 4 * (wave / 2); at < end; at += 16) {
+        const bool some = at + quarter < end;
+        solve(level, some ? at + quarter : at, some, 0, std::false_type{});
       }
     }
+    place = end;
   }
 }
 
