@@ -57,7 +57,7 @@ constexpr int kLd = 132;  // floats between rows in LDS: neighbouring rows start
 // bits of every number down to 2^-14 of the row's largest, 2^-36 of that below;
 // what the pieces miss is less than the products' own fp32 sums round away.
 template <bool HALF>
-__device__ __forceinline__ void put_row(float* row, float* size, const float (&w)[8], bool some) {
+__device__ __forceinline__ void put_row(float* row, float* size, const float (&w)[8]) {
   const int l16 = threadIdx.x % 16;
   if constexpr (HALF) {
     float most = 0.0f;
@@ -66,7 +66,7 @@ __device__ __forceinline__ void put_row(float* row, float* size, const float (&w
     most = max16(most);
     int ex = __float_as_int(most) >> 23;
     ex = ex < 1 ? 1 : ex > 253 ? 253 : ex;
-    const float down = some ? __int_as_float((254 - ex) << 23) : 0.0f, up = 2048.0f * down;
+    const float down = __int_as_float((254 - ex) << 23), up = 2048.0f * down;
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
       h4 hi, lo;
@@ -81,12 +81,8 @@ __device__ __forceinline__ void put_row(float* row, float* size, const float (&w
     if (l16 == 0) *size = __int_as_float(ex << 23);
   } else {
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      f4 x;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = some ? w[4 * p + e] : 0.0f;
-      *reinterpret_cast<f4*>(row + 64 * p + 4 * l16) = x;
-    }
+    for (int p = 0; p < 2; ++p)
+      *reinterpret_cast<f4*>(row + 64 * p + 4 * l16) = f4{w[4 * p], w[4 * p + 1], w[4 * p + 2], w[4 * p + 3]};
   }
 }
 
@@ -140,8 +136,9 @@ constexpr int tree_lds_bytes(int nb) { return tree_rows_bytes(nb) + 9 * first_pa
 
 // A workgroup for a request and head; nb: its places for nodes, a multiple of 16.
 // Sixteen lanes a node up to the products, 32 PER nodes in all; there a wave has 16
-// value columns, in the solve 64 and four nodes.
-template <int DT, int PER>
+// value columns, in the solve 64 and four nodes.  COLS 64: a workgroup has half a
+// head's columns, and half its waves the keys' products, half the queries'.
+template <int DT, int PER, int COLS>
 __global__ __launch_bounds__(kTreeThreads, 4) void kda_tree_kernel(TreeArgs a, int nb) {
   constexpr int GROUPS = kTreeThreads / 16;
   constexpr int TILES = 2 * PER;  // of 16 nodes
@@ -157,7 +154,8 @@ __global__ __launch_bounds__(kTreeThreads, 4) void kda_tree_kernel(TreeArgs a, i
   __shared__ f4 node_sh[64];
 
   const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
-  const int h = blockIdx.x % a.H, r = blockIdx.x / a.H;
+  constexpr int PARTS = 128 / COLS;
+  const int c0 = blockIdx.x % PARTS * COLS, h = blockIdx.x / PARTS % a.H, r = blockIdx.x / PARTS / a.H;
   const int slot = a.init_ids[r];
   const Nodes t = nodes_of(a.cu, r, a.n_tokens);
   if (t.n == 0) return;
@@ -188,9 +186,10 @@ __global__ __launch_bounds__(kTreeThreads, 4) void kda_tree_kernel(TreeArgs a, i
   }
   // the wave's 16 columns, one a lane: as they go into the products, rows 16 kk + 4
   // quarter + j of fp32, 32 kk + 8 quarter + j of fp16
-  const int quarter = lane / 16, col = 16 * wave + lane % 16;
+  const int quarter = lane / 16, col = 16 * (wave % (COLS / 16)) + lane % 16;
+  const bool keys = COLS == 128 || wave < 4, queries = COLS == 128 || wave >= 4;  // this wave's products
   const Stored<DT>* S0 =
-      static_cast<const Stored<DT>*>(a.pool) + (static_cast<int64_t>(placed ? slot : 0) * a.H + h) * 128 * 128 + col;
+      static_cast<const Stored<DT>*>(a.pool) + (static_cast<int64_t>(placed ? slot : 0) * a.H + h) * 128 * 128 + c0 + col;
   constexpr int RUN = HALF ? 8 : 4;
   Stored<DT> S[128 / (4 * RUN)][RUN];
 #pragma unroll
@@ -202,8 +201,8 @@ __global__ __launch_bounds__(kTreeThreads, 4) void kda_tree_kernel(TreeArgs a, i
   bool bad;
   const uint64_t above = tree_paths(parent, n, &bad);
   if (!fits || bad || !placed) {
-    for (int64_t i = tid; i < static_cast<int64_t>(t.n) * 128; i += kTreeThreads)
-      a.out[row0 + i / 128 * step + i % 128] = __builtin_nanf("");
+    for (int64_t i = tid; i < static_cast<int64_t>(t.n) * COLS; i += kTreeThreads)
+      a.out[row0 + i / COLS * step + c0 + i % COLS] = __builtin_nanf("");
     return;
   }
   const int depth_of = lane < n ? __popcll(above) - 1 : -1;
@@ -313,15 +312,15 @@ __global__ __launch_bounds__(kTreeThreads, 4) void kda_tree_kernel(TreeArgs a, i
   }
   __syncthreads();
   // -- the decayed vectors as rows of the left operand: 16 nodes' keys, then their
-  // queries
+  // queries (what lies in rows of no node comes out in rows of no node)
   const int tiles = (n + 15) / 16;
 #pragma unroll
   for (int m = 0; m < PER; ++m) {
     const int i = tid / 16 + GROUPS * m;
-    if (4 * wave + GROUPS * m < 16 * tiles) {
+    if (has(m)) {
       const int to = 32 * (i / 16) + i % 16;
-      put_row<HALF>(x_sh + to * kLd, size_sh + to, wk[m], i < n);
-      put_row<HALF>(x_sh + (to + 16) * kLd, size_sh + to + 16, wq[m], i < n);
+      put_row<HALF>(x_sh + to * kLd, size_sh + to, wk[m]);
+      put_row<HALF>(x_sh + (to + 16) * kLd, size_sh + to + 16, wq[m]);
     }
   }
   // (the values are on their way while the products run)
@@ -331,7 +330,7 @@ __global__ __launch_bounds__(kTreeThreads, 4) void kda_tree_kernel(TreeArgs a, i
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int i = 16 * m + 4 * quarter + e;
-      v[m][e] = a.v[row0 + (i < n ? i : 0) * step + col];
+      if (keys) v[m][e] = a.v[row0 + (i < n ? i : 0) * step + c0 + col];
     }
   __syncthreads();
 
@@ -340,8 +339,8 @@ __global__ __launch_bounds__(kTreeThreads, 4) void kda_tree_kernel(TreeArgs a, i
 #pragma unroll
   for (int m = 0; m < TILES; ++m)
     if (m < tiles) {
-      pk[m] = product<HALF>(x_sh + 32 * m * kLd, size_sh + 32 * m, S);
-      pq[m] = product<HALF>(x_sh + (32 * m + 16) * kLd, size_sh + 32 * m + 16, S);
+      if (keys) pk[m] = product<HALF>(x_sh + 32 * m * kLd, size_sh + 32 * m, S);
+      if (queries) pq[m] = product<HALF>(x_sh + (32 * m + 16) * kLd, size_sh + 32 * m + 16, S);
     }
   __syncthreads();
 #pragma unroll
@@ -350,16 +349,17 @@ __global__ __launch_bounds__(kTreeThreads, 4) void kda_tree_kernel(TreeArgs a, i
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int i = 16 * m + 4 * quarter + e;
-        x_sh[i * kLd + col] = v[m][e] - pk[m][e];
-        x_sh[(nb + i) * kLd + col] = pq[m][e];
+        if (keys) x_sh[i * kLd + col] = v[m][e] - pk[m][e];
+        if (queries) x_sh[(nb + i) * kLd + col] = pq[m][e];
       }
 
   // -- the solve and the read-outs, level after level.  A wave takes 64 columns, four a
-  // lane, and each quarter of it a node, so eight waves take 16 nodes of a level at
-  // once; up to four nodes below level 4 have a wave's quarters share each one's sum.
+  // lane, and each quarter of it a node, so eight waves take 16 (32) nodes of a level
+  // at once; up to four nodes below level 4 have a wave's quarters share each one's sum.
   __syncthreads();
-  const int c4 = 64 * (wave % 2) + 4 * (lane % 16);
-  char* const out = reinterpret_cast<char*>(a.out + row0 + c4);
+  const int c4 = 64 * (wave % (COLS / 64)) + 4 * (lane % 16), team = wave / (COLS / 64);
+  constexpr int TURN = 4 * (kTreeThreads / 64) / (COLS / 64);
+  char* const out = reinterpret_cast<char*>(a.out + row0 + c0 + c4);
   const uint32_t out_step = static_cast<uint32_t>(4 * step);  // (64 of them are less than 2^30)
   float* const x_col = x_sh + c4;
   const auto solve = [&](int level, int at, bool some, int part, auto share) __attribute__((always_inline)) {
@@ -408,9 +408,9 @@ __global__ __launch_bounds__(kTreeThreads, 4) void kda_tree_kernel(TreeArgs a, i
     if (level > 0) __syncthreads();
     const int end = place + __popcll(__ballot(depth_of == level));
     if (level > 4 && end - place <= 4) {
-      if (place + wave / 2 < end) solve(level, place + wave / 2, quarter == 0, quarter, std::true_type{});
+      if (place + team < end) solve(level, place + team, quarter == 0, quarter, std::true_type{});
     } else {
-      for (int at = place + 4 * (wave / 2); at < end; at += 16) {
+      for (int at = place + 4 * team; at < end; at += TURN) {
         const bool some = at + quarter < end;
         solve(level, some ? at + quarter : at, some, 0, std::false_type{});
       }
@@ -543,19 +543,23 @@ bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p)
 
 template <int DT>
 hipError_t launch_tree(const TreeArgs& a, hipStream_t st) {
-  const dim3 grid(static_cast<uint32_t>(a.n_req) * a.H);
   const int nb = a.max_nodes < 1 ? 16 : (a.max_nodes + 15) / 16 * 16;
-  const auto launch = [&](auto kernel) {
+  const int64_t units = static_cast<int64_t>(a.n_req) * a.H;
+  const auto launch = [&](auto kernel, int parts) {
     // (more than 64 KiB of LDS has to be asked for)
     hipError_t e = hipSuccess;
     if (tree_lds_bytes(nb) > 65536)
       e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
                               tree_lds_bytes(nb));
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kernel, grid, dim3(kTreeThreads), tree_lds_bytes(nb), st, a, nb);
+    hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(units * parts)), dim3(kTreeThreads), tree_lds_bytes(nb), st, a,
+                       nb);
     return hipGetLastError();
   };
-  return nb <= 32 ? launch(kda_tree_kernel<DT, 1>) : launch(kda_tree_kernel<DT, 2>);
+  // Half heads where whole ones would leave half the chip idle.
+  const bool half = units <= 128;
+  if (nb <= 32) return half ? launch(kda_tree_kernel<DT, 1, 64>, 2) : launch(kda_tree_kernel<DT, 1, 128>, 1);
+  return half ? launch(kda_tree_kernel<DT, 2, 64>, 2) : launch(kda_tree_kernel<DT, 2, 128>, 1);
 }
 
 // threads of a launch stay below 2^32 for the widest workgroup

@@ -384,6 +384,14 @@ def test_decode_tree(dtype, H, n):
     assert torch.equal(s.d["pool"].cpu(), s.pool)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("most", [12, 40])
+def test_decode_tree_of_many_heads(dtype, most):
+    # more than 128 requests x heads: whole heads
+    s = States([some_tree(1 + (7 * r) % most, r) for r in range(23)], H=6, dtype=dtype, seed=most).put()
+    s.check(s.tree())
+
+
 @pytest.mark.parametrize("max_nodes", [5, 16, 17, 32, 33, 64, None])
 def test_decode_tree_variants_agree(max_nodes):
     s = States([some_tree(5, 1), chain(4)], seed=4).put()
