@@ -66,18 +66,18 @@ struct VerifyArgs {
   int32_t* lens;
   int32_t* next;
   VerifyStop* stops;       // workspace: [n_req], then
-  double* sums;            //   [n_req][parts]
+  double* sums;            //   [n_req][runs]
   int64_t target_stride, draft_stride;  // elements between rows
   int64_t n_tokens;
   int32_t n_req, vocab, max_path;
-  int32_t parts, part;     // parts of a row, entries of a part
+  int32_t runs, run;       // runs of a row, entries of a run
 };
 
-// How a row of `vocab` probabilities is dealt to workgroups.
+// How a row of `vocab` probabilities is dealt to waves.
 struct VerifyPlan {
-  int32_t parts, part;
+  int32_t runs, run;
 };
-VerifyPlan verify_plan(int32_t n_req, int32_t vocab);
+VerifyPlan verify_plan(int32_t vocab);
 
 // Checks shared by kda_decode_tree and kda_decode_path, up to the counts.
 int tree_check(const kda_pool* pool, int32_t n_req, int64_t n_tokens, kda_dtype state_dtype);

@@ -24,19 +24,10 @@ int verify_check(int32_t n_req, int64_t n_tokens, int32_t vocab, int32_t max_pat
   return KDA_OK;
 }
 
-VerifyPlan verify_plan(int32_t n_req, int32_t vocab) {
-  VerifyPlan p;
-  const int64_t least = 4096;  // entries of a part: what 256 threads load at once, 16 each
-  int64_t parts = 1024 / (n_req < 1 ? 1 : n_req);
-  const int64_t most = (static_cast<int64_t>(vocab) + least - 1) / least;
-  if (parts > most) parts = most;
-  if (parts > 64) parts = 64;
-  if (parts < 1) parts = 1;
-  int64_t part = (vocab + parts - 1) / parts;
-  part = (part + 255) / 256 * 256;
-  p.part = static_cast<int32_t>(part > INT32_MAX - 255 ? INT32_MAX - 255 : part);
-  p.parts = static_cast<int32_t>((static_cast<int64_t>(vocab) + p.part - 1) / p.part);
-  return p;
+VerifyPlan verify_plan(int32_t vocab) {
+  // at most 64 runs, a lane each where they are searched; of whole loads of a wave
+  const int64_t each = (static_cast<int64_t>(vocab) + 63) / 64, run = (each + 511) / 512 * 512;
+  return {static_cast<int32_t>((vocab + run - 1) / run), static_cast<int32_t>(run)};
 }
 
 }  // namespace kda
@@ -63,8 +54,8 @@ int kda_tree_validate(const int32_t* cu_seqlens_host, const int32_t* parents_hos
 
 size_t kda_verify_workspace(int32_t n_req, int64_t n_tokens, int32_t vocab, int32_t max_path, kda_dtype dtype) {
   if (verify_check(n_req, n_tokens, vocab, max_path, dtype) != KDA_OK || n_req == 0) return 0;
-  const VerifyPlan p = verify_plan(n_req, vocab);
-  return static_cast<size_t>(n_req) * (sizeof(VerifyStop) + p.parts * sizeof(double));
+  const VerifyPlan p = verify_plan(vocab);
+  return static_cast<size_t>(n_req) * (sizeof(VerifyStop) + p.runs * sizeof(double));
 }
 
 }  // extern "C"

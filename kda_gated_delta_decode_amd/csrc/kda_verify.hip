@@ -20,8 +20,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-constexpr int kVec = 8;    // entries a thread loads at once
-constexpr int kRun = 32;   // entries a thread searches
+constexpr int kVec = 8;  // entries a thread loads at once
 
 template <int DT>
 using Entry = std::conditional_t<DT == KDA_F32, float, uint16_t>;
@@ -44,14 +43,14 @@ __device__ __forceinline__ const Entry<DT>* row_of(const void* base, int64_t row
   return static_cast<const Entry<DT>*>(base) + row * stride;
 }
 
-// N entries from x on, of which the row has `left`; 0 behind its end
-template <int DT, int N>
-__device__ __forceinline__ void load_run(const Entry<DT>* p, int left, Entry<DT> (&e)[N]) {
-  if (left >= N) {
-    __builtin_memcpy(e, p, sizeof(e));
+// kVec entries of a row of `vocab`, from `at` on; WHOLE: the row has as many
+template <int DT, bool WHOLE>
+__device__ __forceinline__ void load_run(const Entry<DT>* row, int64_t at, int vocab, Entry<DT> (&e)[kVec]) {
+  if constexpr (WHOLE) {
+    __builtin_memcpy(e, row + at, sizeof(e));
   } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) e[i] = i < left ? p[i] : Entry<DT>{};
+    for (int i = 0; i < kVec; ++i) e[i] = at + i < vocab ? row[at + i] : Entry<DT>{};
   }
 }
 
@@ -62,10 +61,16 @@ __device__ __forceinline__ double lane_double(double x, int lane) {
   return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
 }
 
-// the same sum, in the same order, in every thread
-__device__ __forceinline__ double block_sum(double x, double* sh) {
+// a wave's sum, the same in every lane
+__device__ __forceinline__ double wave_sum(double x) {
 #pragma unroll
   for (int m = 1; m < 64; m *= 2) x += __shfl_xor(x, m);
+  return x;
+}
+
+// the same sum, in the same order, in every thread
+__device__ __forceinline__ double block_sum(double x, double* sh) {
+  x = wave_sum(x);
   if (threadIdx.x % 64 == 0) sh[threadIdx.x / 64] = x;
   __syncthreads();
   double s = 0.0;
@@ -82,60 +87,99 @@ template <int DT, bool DRAFT>
 struct Left {
   const Entry<DT>* p;
   const Entry<DT>* q;
-  int tries;
+  int vocab, tries;
   double mass;
   int token;
   uint64_t refused;
 
-  template <int N>
-  __device__ __forceinline__ void get(int64_t x0, int64_t end, double (&f)[N]) const {
-    const int64_t rest = end - x0;
-    const int left = rest < 0 ? 0 : rest > N ? N : static_cast<int>(rest);
-    Entry<DT> e[N];
-    load_run<DT, N>(p + x0, left, e);
+  // kVec entries as they lie, of which those from x on count: at the end of a run
+  // they begin before x
+  struct Raw {
+    Entry<DT> p[kVec], q[DRAFT ? kVec : 1];
+    int64_t at;
+    int skip;
+  };
+  // (nothing here depends on the row: the loads of a thread do not wait for each other)
+  template <bool WHOLE, bool TRIED>
+  __device__ __forceinline__ void load(int64_t x, int64_t end, Raw& raw) const {
+    const int64_t last = end > kVec ? end - kVec : 0;
+    raw.at = x < last ? x : last;
+    raw.skip = x - raw.at < kVec ? static_cast<int>(x - raw.at) : kVec;
+    load_run<DT, WHOLE>(p, raw.at, vocab, raw.p);
+    if constexpr (TRIED && DRAFT) load_run<DT, WHOLE>(q, raw.at, vocab, raw.q);
+  }
+  // and what is left of them
+  template <bool TRIED>
+  __device__ __forceinline__ void weights(const Raw& raw, double (&f)[kVec]) const {
 #pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = weight<DT>(e[i]);
-    if constexpr (DRAFT) {
-      if (tries > 0) {
-        load_run<DT, N>(q + x0, left, e);
-        for (int j = 0; j < tries; ++j) {
-          const double m = lane_double(mass, j);
+    for (int i = 0; i < kVec; ++i) f[i] = weight<DT>(raw.p[i]);
+    if constexpr (TRIED && DRAFT) {
+      for (int j = 0; j < tries; ++j) {
+        const double m = lane_double(mass, j);
 #pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const double d = f[i] - m * weight<DT>(e[i]);
-            f[i] = d > 0.0 ? d : 0.0;
-          }
+        for (int i = 0; i < kVec; ++i) {
+          const double d = f[i] - m * weight<DT>(raw.q[i]);
+          f[i] = d > 0.0 ? d : 0.0;
         }
       }
-    } else {
+    } else if constexpr (TRIED) {
       for (uint64_t r = refused; r != 0; r &= r - 1) {
-        const int64_t at = __builtin_amdgcn_readlane(token, __builtin_ctzll(r)) - x0;
+        const int64_t at = __builtin_amdgcn_readlane(token, __builtin_ctzll(r)) - raw.at;
 #pragma unroll
-        for (int i = 0; i < N; ++i) f[i] = at == i ? 0.0 : f[i];
+        for (int i = 0; i < kVec; ++i) f[i] = at == i ? 0.0 : f[i];
       }
+    }
+    if (__ballot(raw.skip != 0) != 0) {
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) f[i] = i < raw.skip ? 0.0 : f[i];
     }
   }
 
-  // sum of the entries [x0, x1), by all threads of the block
-  __device__ __forceinline__ double sum(int64_t x0, int64_t x1, double* sh) const {
-    double s = 0.0;
-    for (int64_t x = x0 + threadIdx.x * kVec; x < x1; x += kThreads * kVec) {
-      double f[kVec];
-      get(x, x1, f);
-      s += ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
-    }
-    return block_sum(s, sh);
+  // f(whole, tried) with constants for this row
+  template <typename F>
+  __device__ __forceinline__ auto as(F f) const {
+    if (vocab < kVec) return f(std::false_type{}, std::true_type{});
+    return tries > 0 ? f(std::true_type{}, std::true_type{}) : f(std::true_type{}, std::false_type{});
+  }
+
+  // a thread's share of the sum of entries [x0, x1), `threads` of them on it: four
+  // loads in flight, the rest one by one
+  __device__ __forceinline__ double share(int64_t x0, int64_t x1, int thread, int threads) const {
+    return as([&](auto whole, auto tried) __attribute__((always_inline)) {
+      constexpr bool WHOLE = decltype(whole)::value, TRIED = decltype(tried)::value;
+      const int turn = threads * kVec;
+      int64_t at = x0;
+      double s = 0.0;
+      const auto add = [&](auto ahead) __attribute__((always_inline)) {
+        constexpr int AHEAD = decltype(ahead)::value;
+        Raw raw[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) load<WHOLE, TRIED>(at + thread * kVec + i * turn, x1, raw[i]);
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+          double f[kVec];
+          weights<TRIED>(raw[i], f);
+          s += ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
+        }
+        at += AHEAD * turn;
+      };
+      if constexpr (WHOLE)
+        while (at + 3 * turn < x1) add(std::integral_constant<int, 4>{});
+      while (at < x1) add(std::integral_constant<int, 1>{});
+      return s;
+    });
   }
 };
 
-// A workgroup for each part of each request's last row.  All walk, so that none
-// waits for another: lane i of every wave holds node i, the walk reads lanes.
+// A wave for each run of each request's last row.  All walk, so that none waits
+// for another: lane i of every wave holds node i, the walk reads lanes.
 template <int DT, bool DRAFT>
 __global__ __launch_bounds__(kThreads) void kda_verify_walk_kernel(VerifyArgs a) {
   __shared__ double sh[kWaves];
   const int lane = threadIdx.x % 64;
-  const int r = blockIdx.x / a.parts, part = blockIdx.x % a.parts;
-  const bool writes = part == 0 && threadIdx.x < 64;
+  const int blocks = (a.runs + kWaves - 1) / kWaves;  // of a request
+  const int r = blockIdx.x / blocks, run = blockIdx.x % blocks * kWaves + threadIdx.x / 64;
+  const bool writes = run == 0;
   const Nodes t = nodes_of(a.cu, r, a.n_tokens);
   bool bad = t.n == 0 || t.n > kMaxNodes;
   const int n = bad ? 0 : t.n;
@@ -160,6 +204,7 @@ __global__ __launch_bounds__(kThreads) void kda_verify_walk_kernel(VerifyArgs a)
   }
 
   Left<DT, DRAFT> left;
+  left.vocab = a.vocab;
   left.token = token;
   left.mass = 0.0;
   int last = 0, length = 1;
@@ -200,7 +245,7 @@ __global__ __launch_bounds__(kThreads) void kda_verify_walk_kernel(VerifyArgs a)
         if (kids != 0) {  // the next child's M: a sum of the whole row
           left.p = row_of<DT>(a.target, t.n0 + last, a.target_stride);
           left.q = row_of<DT>(a.draft, t.n0 + last, a.draft_stride);
-          mass = left.sum(0, a.vocab, sh);
+          mass = block_sum(left.share(0, a.vocab, threadIdx.x, kThreads), sh);
         }
       } else {
         ++left.tries;
@@ -221,10 +266,11 @@ __global__ __launch_bounds__(kThreads) void kda_verify_walk_kernel(VerifyArgs a)
       s->tries = left.tries;
     }
   }
-  const int64_t x0 = static_cast<int64_t>(part) * a.part;
-  const int64_t x1 = x0 + a.part < a.vocab ? x0 + a.part : a.vocab;
-  const double s = left.sum(x0, x1, sh);
-  if (threadIdx.x == 0) a.sums[static_cast<int64_t>(r) * a.parts + part] = s;
+  if (run >= a.runs) return;
+  const int64_t x0 = static_cast<int64_t>(run) * a.run;
+  const int64_t x1 = x0 + a.run < a.vocab ? x0 + a.run : a.vocab;
+  const double s = wave_sum(left.share(x0, x1, lane, 64));
+  if (lane == 0) a.sums[static_cast<int64_t>(r) * a.runs + run] = s;
 }
 
 // running sum over the lanes of a wave
@@ -239,58 +285,49 @@ __device__ __forceinline__ double wave_scan(double x) {
 }
 
 // The first entry of [x0, x1) above 0 at which `before` and the running sum
-// exceed `target`; if none does, the last one above 0; -1 if there is none.  By all threads.
+// exceed `target`; if none does, the last one above 0; -1 if there is none.  By all
+// threads, 2048 entries at a time.
 template <typename L>
 __device__ int search(const L& left, int64_t x0, int64_t x1, double before, double target, double* sh, int* found) {
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
   if (threadIdx.x == 0) found[0] = INT32_MAX, found[1] = -1;
-  __syncthreads();
-  // f(entry, its weight) for this thread's run of those from `at` on
-  auto each = [&](int64_t at, auto f) __attribute__((always_inline)) {
-    const int64_t mine = at + threadIdx.x * kRun;
-    for (int i = 0; i < kRun; i += kVec) {
-      double w[kVec];
-      left.get(mine + i < x1 ? mine + i : x1, x1, w);
+  for (int64_t at = x0; at < x1; at += kThreads * kVec) {
+    double w[kVec], s = 0.0;
+    typename L::Raw raw;
+    left.as([&](auto whole, auto tried) __attribute__((always_inline)) {
+      left.template load<decltype(whole)::value, decltype(tried)::value>(at + threadIdx.x * kVec, x1, raw);
+      left.template weights<decltype(tried)::value>(raw, w);
+    });
+    const int mine = static_cast<int>(raw.at);
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) f(static_cast<int>(mine) + i + j, w[j]);
-    }
-  };
-  int64_t weighty = -1;  // the last entries with weight
-  for (int64_t at = x0; at < x1; at += kThreads * kRun) {
-    double s = 0.0;
-    each(at, [&](int, double w) { s += w; });
+    for (int j = 0; j < kVec; ++j) s += w[j];
     const double upto = wave_scan(s);
     if (lane == 63) sh[wave] = upto;
     __syncthreads();
     double base = before, all = 0.0;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      base += w < wave ? sh[w] : 0.0;
-      all += sh[w];
+    for (int v = 0; v < kWaves; ++v) {
+      base += v < wave ? sh[v] : 0.0;
+      all += sh[v];
     }
-    weighty = all > 0.0 ? at : weighty;
-    // Looked through by every thread whose run may hold the border.  (base +
-    // upto is one order of the sum, the running one another: a run is taken on
-    // either's word.)
+    // Looked through by every thread that may hold the border.  (base + upto is
+    // one order of the sum, the running one another: it is taken on either's word.)
     double run = base + (upto - s);
-    if (s > 0.0 && (base + upto > target || run + s > target)) {
+    if (s > 0.0) {
       int hit = INT32_MAX, top = -1;
-      each(at, [&](int x, double w) {
-        run += w;
-        top = w > 0.0 ? x : top;
-        hit = w > 0.0 && run > target && x < hit ? x : hit;
-      });
-      atomicMin(&found[0], hit == INT32_MAX ? top : hit);
+      const bool near = base + upto > target || run + s > target;
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) {
+        run += w[j];
+        top = w[j] > 0.0 ? mine + j : top;
+        hit = w[j] > 0.0 && run > target && hit == INT32_MAX ? mine + j : hit;
+      }
+      if (near) atomicMin(&found[0], hit == INT32_MAX ? top : hit);
+      atomicMax(&found[1], top);
     }
     __syncthreads();
     if (found[0] != INT32_MAX) break;
     before += all;
-    __syncthreads();
-  }
-  if (found[0] == INT32_MAX && weighty >= 0) {
-    int top = -1;
-    each(weighty, [&](int x, double w) { top = w > 0.0 ? x : top; });
-    atomicMax(&found[1], top);
     __syncthreads();
   }
   return found[0] != INT32_MAX ? found[0] : found[1];
@@ -312,29 +349,30 @@ __global__ __launch_bounds__(kThreads) void kda_verify_draw_kernel(VerifyArgs a)
   Left<DT, DRAFT> left;
   left.p = row_of<DT>(a.target, row, a.target_stride);
   left.q = DRAFT ? row_of<DT>(a.draft, row, a.draft_stride) : nullptr;
+  left.vocab = a.vocab;
   left.tries = stop->tries;
   left.refused = stop->refused;
   left.mass = stop->mass[lane];
   left.token = (left.refused >> lane & 1) != 0 ? a.tokens[n0 + lane] : -1;
-  const double part = lane < a.parts ? a.sums[static_cast<int64_t>(r) * a.parts + lane] : 0.0;
+  const double part = lane < a.runs ? a.sums[static_cast<int64_t>(r) * a.runs + lane] : 0.0;
   const double upto = wave_scan(part);
   double total = lane_double(upto, 63);
   const double u = static_cast<double>(a.sample[r]);
   int64_t x0 = 0, x1 = a.vocab;
   double before = 0.0;
   if (total > 0.0) {
-    // the first part that passes the border; the last with weight if none does
+    // the first run that passes the border; the last with weight if none does
     uint64_t over = __ballot(part > 0.0 && upto > u * total);
     if (over == 0) over = 1ull << (63 - __builtin_clzll(__ballot(part > 0.0)));
     const int at = __builtin_ctzll(over);
     before = at == 0 ? 0.0 : lane_double(upto, at - 1);
-    x0 = static_cast<int64_t>(at) * a.part;
-    x1 = x0 + a.part < a.vocab ? x0 + a.part : a.vocab;
+    x0 = static_cast<int64_t>(at) * a.run;
+    x1 = x0 + a.run < a.vocab ? x0 + a.run : a.vocab;
   } else {
     // nothing is left: the target's row itself
     left.tries = 0;
     left.refused = 0;
-    total = left.sum(0, a.vocab, sh);
+    total = block_sum(left.share(0, a.vocab, threadIdx.x, kThreads), sh);
   }
   int x = -1;
   if (total > 0.0 && total < __builtin_huge_val()) x = search(left, x0, x1, before, u * total, sh, found);
@@ -346,7 +384,7 @@ bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p)
 
 template <int DT, bool DRAFT>
 hipError_t launch(const VerifyArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL((kda_verify_walk_kernel<DT, DRAFT>), dim3(static_cast<uint32_t>(a.n_req) * a.parts),
+  hipLaunchKernelGGL((kda_verify_walk_kernel<DT, DRAFT>), dim3(static_cast<uint32_t>(a.n_req) * ((a.runs + kWaves - 1) / kWaves)),
                      dim3(kThreads), 0, st, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -374,8 +412,8 @@ extern "C" int kda_verify_drafts(const void* target, int64_t target_stride, cons
   if (n_tokens > 0 && (target == nullptr || parents == nullptr || tokens == nullptr || accept_rand == nullptr))
     return KDA_ERR_NULL;
   if (target_stride < vocab || (draft != nullptr && draft_stride < vocab)) return KDA_ERR_ARG;
-  const VerifyPlan p = verify_plan(n_req, vocab);
-  if (static_cast<int64_t>(n_req) * p.parts > INT32_MAX / kThreads) return KDA_ERR_ARG;
+  const VerifyPlan p = verify_plan(vocab);
+  if (static_cast<int64_t>(n_req) * ((p.runs + kWaves - 1) / kWaves) > INT32_MAX / kThreads) return KDA_ERR_ARG;
   const unsigned size = dtype == KDA_F32 ? 4 : 2;
   if (!aligned(target, size) || !aligned(draft, size) || !aligned(cu_seqlens, 4) || !aligned(parents, 4) ||
       !aligned(tokens, 4) || !aligned(accept_rand, 4) || !aligned(sample_rand, 4) || !aligned(path, 4) ||
@@ -403,8 +441,8 @@ extern "C" int kda_verify_drafts(const void* target, int64_t target_stride, cons
   a.n_req = n_req;
   a.vocab = vocab;
   a.max_path = max_path;
-  a.parts = p.parts;
-  a.part = p.part;
+  a.runs = p.runs;
+  a.run = p.run;
   hipStream_t st = static_cast<hipStream_t>(stream);
   switch (dtype) {
     case KDA_F32: return status(draft ? launch<KDA_F32, true>(a, st) : launch<KDA_F32, false>(a, st));

@@ -312,20 +312,19 @@ HOST_MAIN = r"""
 #include <vector>
 #include "kda_decode.h"
 #include "kda_tree.h"
-// a row's parts cover every entry once, and none is empty
-static void plan(int32_t n_req, int32_t vocab) {
-  const kda::VerifyPlan p = kda::verify_plan(n_req, vocab);
-  const int64_t covered = (int64_t)p.parts * p.part;
-  if (p.parts < 1 || p.parts > 64 || p.part < 1 || covered < vocab || covered - p.part >= vocab) {
-    std::printf("plan %d %d: %d x %d\n", n_req, vocab, p.parts, p.part);
+// a row's runs cover every entry once, and none is empty
+static void plan(int32_t vocab) {
+  const kda::VerifyPlan p = kda::verify_plan(vocab);
+  const int64_t covered = (int64_t)p.runs * p.run;
+  if (p.runs < 1 || p.runs > 64 || p.run < 1 || covered < vocab || covered - p.run >= vocab) {
+    std::printf("plan %d: %d x %d\n", vocab, p.runs, p.run);
     std::exit(1);
   }
 }
 int main() {
-  for (int32_t n : {1, 2, 3, 7, 16, 33, 64, 100, 1000, 5000, 2147483647})
-    for (int32_t v : {1, 2, 255, 256, 257, 4095, 4096, 4097, 8193, 32768, 50021, 100003, 131072, 999983, 2147483392, 2147483647}) plan(n, v);
+  for (int32_t v : {1, 2, 255, 256, 257, 4095, 4096, 4097, 8193, 32768, 50021, 100003, 131072, 999983, 2147483392, 2147483647}) plan(v);
   std::srand(1);
-  for (int i = 0; i < 20000; ++i) plan(1 + std::rand() % 3000, 1 + std::rand() % 300000);
+  for (int i = 0; i < 20000; ++i) plan(1 + std::rand() % 300000);
   // parents of a table that ends where the nodes end
   for (int n = 0; n <= 64; ++n) {
     std::vector<int32_t> cu = {0, n}, parents(n);

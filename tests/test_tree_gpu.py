@@ -632,8 +632,7 @@ def test_verify_large_vocabularies(V, draft):
         d.check()
 
 
-def test_verify_many_requests_share_parts():
-    # more requests than parts to deal: one part a row
+def test_verify_many_requests():
     trees = [chain(1 + i % 3) for i in range(1100)]
     Drafts(trees, 300, "f16", True, seed=1).check()
 
