@@ -721,9 +721,8 @@ int kda_kv_append_at(const kda_kv_pool* kv, const int32_t* page_table, int32_t m
  * kda_kv_attend_tree -- kda_kv_attend for a tree's nodes: node i of sequence s,
  * cached at position cache_lens[s] + i, sees the cache_lens[s] tokens of the
  * context, the nodes on its path and itself.  Everything else is
- * kda_kv_attend's, workspace and precision included (a chain's results are the
- * same bits); workspace: kda_kv_attend_workspace() bytes for the same
- * arguments.
+ * kda_kv_attend's, precision included; workspace: kda_kv_attend_tree_workspace()
+ * bytes for the same arguments.
  *  parents   device int32 [n_tokens], 4-byte aligned (see above).
  *  max_rows  at most KDA_MAX_NODES (else KDA_ERR_ROWS, checked with the counts).
  * The rows of a sequence of more than KDA_MAX_NODES nodes, or with a parent
@@ -734,6 +733,11 @@ int kda_kv_attend_tree(const kda_kv_pool* kv, const int32_t* page_table, int32_t
                        const void* q, int64_t q_stride, void* out, int32_t n_seq, int64_t n_tokens,
                        int32_t max_rows, int64_t max_kv_len, int32_t q_heads, kda_dtype dtype, float scale,
                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace kda_kv_attend_tree needs for these arguments (0: none, or
+ * arguments it refuses). */
+size_t kda_kv_attend_tree_workspace(const kda_kv_pool* kv, int32_t max_pages, int32_t n_seq, int64_t n_tokens,
+                                    int32_t max_rows, int64_t max_kv_len, int32_t q_heads, kda_dtype dtype);
 
 /*
  * kda_kv_keep -- moves the cache entries of accepted nodes together: node

@@ -142,6 +142,8 @@ SIGNATURES = {
     "kda_kv_attend_tree": (ctypes.c_int, [ctypes.POINTER(kda_kv_pool), _P, _I32, _P, _P, _P, _P, _I64, _P, _I32,
                                           _I64, _I32, _I64, _I32, ctypes.c_int, ctypes.c_float, _P,
                                           ctypes.c_size_t, _P]),
+    "kda_kv_attend_tree_workspace": (ctypes.c_size_t, [ctypes.POINTER(kda_kv_pool), _I32, _I32, _I64, _I32, _I64,
+                                                       _I32, ctypes.c_int]),
     "kda_kv_keep": (ctypes.c_int, [ctypes.POINTER(kda_kv_pool), _P, _I32, _P, _P, _P, _I32, _P, _I32, _I64, _P]),
     "kda_decode_tree": (ctypes.c_int, [ctypes.POINTER(kda_pool), _P, _P, _P, _P, _P, _P, _P, _P, _P, _I32, _I64,
                                        _I32, ctypes.c_int, ctypes.c_float, _P]),
@@ -736,6 +738,15 @@ def kda_kv_attend_workspace(pool, page_table, n_tokens: int, q_heads: int, max_r
                                                  _dtype_arg(dtype)))
 
 
+def kda_kv_attend_tree_workspace(pool, page_table, n_tokens: int, q_heads: int, max_rows: int, max_kv_len: int = 0,
+                                 dtype="f32") -> int:
+    """Bytes of workspace kda_kv_attend_tree needs for a launch of these sizes."""
+    P = make_kv_pool(pool)
+    return int(library().kda_kv_attend_tree_workspace(ctypes.byref(P), page_table.shape[1], page_table.shape[0],
+                                                      int(n_tokens), int(max_rows), int(max_kv_len), int(q_heads),
+                                                      _dtype_arg(dtype)))
+
+
 def _workspace(torch, pool, dev, workspace, bytes_needed, st):
     """(tensor, bytes): the caller's workspace, checked, or one of bytes_needed()
     from torch's allocator, as memory of the launch's stream."""
@@ -767,7 +778,7 @@ def _attend(name, pool, page_table, cu_seqlens, cache_lens, parents, q, out, max
     rows = int(max_rows) if max_rows is not None else T if parents is None else min(T, KDA_MAX_NODES)
     kv, code, st = int(max_kv_len), dtype_code(dtype), _kv_stream(torch, dev, stream)
     pool_ref = ctypes.byref(P)
-    workspace, wn = _workspace(torch, pool, dev, workspace, lambda: (_lib or library()).kda_kv_attend_workspace(
+    workspace, wn = _workspace(torch, pool, dev, workspace, lambda: getattr(_lib or library(), name + "_workspace")(
         pool_ref, tables[1], n_seq, T, rows, kv, heads, code), st)
     if parents is not None:
         tables += (_tree_table(parents, "parents", dev, torch.int32, (T,)),)

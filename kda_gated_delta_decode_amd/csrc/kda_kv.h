@@ -79,13 +79,14 @@ struct KvAttendArgs {
   float* part_ml;  //   [n_splits][n_tokens * q_heads][2] maxima and sums of weights
   int64_t q_stride;
   int32_t q_heads, group;       // group: query heads of one cached head
-  int32_t chunk, n_splits;      // tokens a split covers
+  int32_t chunk, n_splits;      // tokens a split covers (large trees: n_splits places)
   int32_t row_tiles;            // tiles of rows a sequence is given blocks for
   int32_t slots;                // 128-row tiles: places for all sequences' tiles
   float scale;                  // |scale| * log2(e)
   float sign;                   // of scale: queries are multiplied by it
   const int32_t* parents;       // trees: [n_tokens]
   int32_t most_rows;            // trees: KDA_MAX_NODES; else no bound
+  int64_t* starts;              // large trees, workspace: a sequence's first part, and parts of a tile above bit 32
 };
 
 // How kda_kv_attend takes a launch.
@@ -106,6 +107,22 @@ inline int64_t kv_tiles(const KvPlan& p, int32_t n_seq, int32_t H) {
 
 KvPlan kv_plan(int32_t H, int32_t D, int32_t n_seq, int64_t n_tokens, int32_t max_rows,
                int64_t max_kv_len, int32_t q_heads, kda_dtype dtype);
+
+// Large trees (more than 64 rows of a sequence and cached head): tiles are cut in parts
+// of at least kKvTreeSteps 64-token steps, as many as there are places for.
+constexpr int kKvTreeSteps = 8;
+struct KvTreePlan {
+  int32_t places;       // of 128 rows in the workspace; 0: no tile is cut
+  int64_t blocks;
+  int32_t row_tiles;    // tiles of a sequence that the join has blocks for
+  bool many;            // some tiles may have many parts: the join takes them side by side
+  int64_t join_blocks;
+};
+KvTreePlan kv_tree_plan(const kda_kv_pool* kv, int32_t n_seq, int32_t max_rows, int32_t group, int64_t cover,
+                        int64_t max_kv_len, kda_dtype dtype);
+// Workspace: where each sequence's parts begin and how many a tile has, then the
+// places, then their rows' maxima and sums.
+inline int64_t kv_tree_head_bytes(int32_t n_seq) { return (static_cast<int64_t>(n_seq) + 31) / 32 * 32 * 8; }
 
 // Checks shared by the entry points, in the documented order.
 int kv_check(const kda_kv_pool* kv, int32_t max_pages, int32_t n_seq, int64_t n_tokens);

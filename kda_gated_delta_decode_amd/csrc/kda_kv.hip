@@ -1106,9 +1106,21 @@ struct ExpRange {
 // rows of 32 query heads 536 us, 1026 TFLOP/s of the 1211 that a large bf16 matrix
 // product reaches (829 us with two bf16 pieces for a weight, one tile after the
 // other).
-// TREE: as in the rows kernel.
+// TREE: where a part of 128 rows keeps channels 8 k.. of row r: as the lanes hold them,
+// so that a wave writes 1 KiB in a row.  The next four channels are 256 numbers on.
+template <int D>
+__device__ __forceinline__ int tile_piece(int r, int k) {
+  constexpr int VC = D / 16;  // neighbouring channels of a lane, D / VC runs of them in 8 elements of two halves
+  const int run = 8 * k / VC, e = 4 * (run / 8) + run % 4, half = run / 4 % 2;
+  return ((r / 32 * (D / 8) + e * (VC / 4)) * 64 + 32 * half + r % 32) * 4;
+}
+
+// One tile's rows against the tokens [t0, t1).  splits > 1: the rows' sums go to the
+// workspace, as split sp, or TREE, to the 128 rows `place` of it.  TREE otherwise as in
+// the rows kernel.
 template <int DT, int D, bool TREE>
-__device__ __forceinline__ void tiles_body(const KvAttendArgs& a) {
+__device__ __forceinline__ void tile_rows(const KvAttendArgs& a, const Seq& q, int s, int h, int row0, int t0, int t1,
+                                          int splits, int sp, int64_t place) {
   constexpr int KT = 64;            // tokens of a tile
   constexpr int KS = D / 16;        // products over the channels
   constexpr int CB = D / 32;        // 32-channel blocks
@@ -1123,29 +1135,12 @@ __device__ __forceinline__ void tiles_body(const KvAttendArgs& a) {
   __shared__ uint64_t path_sh[TREE ? 4 : 1][TREE ? 64 : 1];
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-  // A sequence's last tiles see the most tokens and go first.  Heads go round
-  // the XCDs: with 8 of them each stays on one, and in its L2.
-  const int h = blockIdx.x % a.t.H, turn = blockIdx.x / a.t.H;
-  const int sp = turn % a.n_splits;
-  const TileAt mine = tile_of_slot(a, a.slots - 1 - turn / a.n_splits);
-  if (mine.tile < 0) return;
-  const int s = mine.s;
-  Seq q = seq_of(a.t, s);
-  if (q.skip) return;
-  if constexpr (TREE) q.bad |= q.rows > a.most_rows;
   const int all_rows = q.rows * a.group;
-  if (mine.tile >= (all_rows + R - 1) / R) return;
-  const int row0 = mine.tile * R;
   const int block_bytes = kv_block_bytes(a.t.P, D);
   const uint8_t* head0 = a.t.base + static_cast<int64_t>(h) * block_bytes;
   const_i32* table = (const_i32*)(a.t.page_table + static_cast<int64_t>(s) * a.t.max_pages);
 
   const int last_row = (row0 + R < all_rows ? row0 + R : all_rows) - 1;
-  const int vis = q.past + last_row / a.group + 1;
-  const int splits = q.bad ? 1 : kv_splits(vis, a);
-  if (sp >= splits) return;
-  const int t0 = q.bad ? 0 : sp * a.chunk;
-  const int t1 = q.bad ? 0 : sp == splits - 1 ? vis : t0 + a.chunk;
   // the last token all of the wave's rows see
   const int w_first = TREE ? q.past - 1 : q.past + (row0 + 32 * wave) / a.group;
   bool broken = false;  // a tree that is none
@@ -1530,18 +1525,29 @@ __device__ __forceinline__ void tiles_body(const KvAttendArgs& a) {
   if (out_row <= last_row) {
     const int ot = out_row / args->group, og = out_row - ot * args->group;
     const int64_t at = (q.n0 + ot) * args->q_heads + static_cast<int64_t>(h) * args->group + og;
-    const int64_t slot = static_cast<int64_t>(sp) * args->t.n_tokens * args->q_heads + at;
+    const int64_t slot =
+        TREE ? place + out_row - row0 : static_cast<int64_t>(sp) * args->t.n_tokens * args->q_heads + at;
     const float inv = splits > 1 ? 1.0f : q.bad || broken ? __builtin_nanf("") : 1.0f / sum;  // sum 0: NaN, as above
+    if (TREE && splits > 1) {
+      float* to = args->part + place * D + ((wave * (D / 8)) * 64 + again % 64) * 4;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int64_t c0 = VC * (8 * (e / 4) + 4 * out_half + e % 4);
-      float x[VC];
+      for (int e = 0; e < 8; ++e)
 #pragma unroll
-      for (int n = 0; n < VC; ++n) x[n] = o[n / 2][8 * (n % 2) + e] * inv;
-      if (splits == 1)
-        store_channels<DT>(args->out, at * D + c0, x);
-      else
-        store_channels<KDA_F32>(args->part, slot * D + c0, x);
+        for (int n = 0; n < VC; n += 4)
+          *reinterpret_cast<f4*>(to + (e * VC + n) * 64) =
+              f4{o[n / 2][e], o[n / 2][8 + e], o[n / 2 + 1][e], o[n / 2 + 1][8 + e]};
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int64_t c0 = VC * (8 * (e / 4) + 4 * out_half + e % 4);
+        float x[VC];
+#pragma unroll
+        for (int n = 0; n < VC; ++n) x[n] = o[n / 2][8 * (n % 2) + e] * inv;
+        if (splits == 1)
+          store_channels<DT>(args->out, at * D + c0, x);
+        else
+          store_channels<KDA_F32>(args->part, slot * D + c0, x);
+      }
     }
     if (splits > 1 && out_half == 0) {
       args->part_ml[2 * slot] = mx - UP;
@@ -1552,11 +1558,25 @@ __device__ __forceinline__ void tiles_body(const KvAttendArgs& a) {
 
 template <int DT, int D>
 __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tiles_kernel(KvAttendArgs a) {
-  tiles_body<DT, D, false>(a);
-}
-template <int DT, int D>
-__global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tree_tiles_kernel(KvAttendArgs a) {
-  tiles_body<DT, D, true>(a);
+  // A sequence's last tiles see the most tokens and go first.  Heads go round
+  // the XCDs: with 8 of them each stays on one, and in its L2.
+  const int h = blockIdx.x % a.t.H, turn = blockIdx.x / a.t.H;
+  const int sp = turn % a.n_splits;
+  const TileAt mine = tile_of_slot(a, a.slots - 1 - turn / a.n_splits);
+  if (mine.tile < 0) return;
+  const int s = mine.s;
+  const Seq q = seq_of(a.t, s);
+  if (q.skip) return;
+  const int all_rows = q.rows * a.group;
+  if (mine.tile >= (all_rows + kTileRows - 1) / kTileRows) return;
+  const int row0 = mine.tile * kTileRows;
+  const int last_row = (row0 + kTileRows < all_rows ? row0 + kTileRows : all_rows) - 1;
+  const int vis = q.past + last_row / a.group + 1;
+  const int splits = q.bad ? 1 : kv_splits(vis, a);
+  if (sp >= splits) return;
+  const int t0 = q.bad ? 0 : sp * a.chunk;
+  const int t1 = q.bad ? 0 : sp == splits - 1 ? vis : t0 + a.chunk;
+  tile_rows<DT, D, false>(a, q, s, h, row0, t0, t1, splits, sp, 0);
 }
 
 // Joins the splits of rows, D / 8 lanes across a row's channels.  Few splits:
@@ -1646,6 +1666,185 @@ __global__ __launch_bounds__(256) void kda_kv_join_kernel(KvAttendArgs a, int ti
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] *= inv;
     if (!MANY || threadIdx.x < PER) store8<DT>(a.out, at * D + c, acc);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Attention: large trees
+// ---------------------------------------------------------------------------
+
+// What a sequence's tiles of 128 rows (times cached heads) take, in steps of 64 tokens.
+struct TreeCost {
+  int units, steps;
+  bool bad;
+};
+// INT: const_i32 for a sequence that is the wave's, int32_t for one that is the lane's
+template <typename INT>
+__device__ __forceinline__ TreeCost tree_cost(const KvAttendArgs& a, int s) {
+  if (s >= a.t.n_seq) return {0, 1, false};
+  const INT *cu = (const INT*)a.t.cu, *lens = (const INT*)a.t.past;
+  const int64_t n0 = cu[s], n1 = cu[s + 1], past = lens[s], rows = n1 - n0;
+  if (n0 < 0 || rows <= 0 || n1 > a.t.n_tokens) return {0, 1, false};
+  if (past < 0 || rows > a.most_rows || past + rows > (static_cast<int64_t>(a.t.max_pages) << a.t.log_p))
+    return {a.t.H, 1, true};
+  return {static_cast<int>(rows * a.group + kTileRows - 1) / kTileRows * a.t.H, static_cast<int>((past + rows + 63) / 64),
+          false};
+}
+__device__ __forceinline__ int ceil_div(int x, int y) { return static_cast<int>((static_cast<uint32_t>(x) + y - 1) / static_cast<uint32_t>(y)); }
+
+// running sum over the lanes of a wave
+__device__ __forceinline__ int wave_scan(int x) {
+  const int lane = threadIdx.x % 64;
+#pragma unroll
+  for (int m = 1; m < 64; m *= 2) {
+    const int y = __shfl_up(x, m);
+    x += lane >= m ? y : 0;
+  }
+  return x;
+}
+
+// Trees' tiles are cut in parts of at most `each` steps, every tile of a sequence
+// alike, such that there are as many parts as places (`a.n_splits`): each = about
+// (all steps) / (places), however lengths and sizes differ.  (16 trees of up to 32
+// nodes on up to 8191 tokens, 32 / 8 heads: 95 us with splits of one length, chosen
+// for the longest sequence.)
+template <int DT, int D>
+__global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tree_tiles_kernel(KvAttendArgs a) {
+  const int lane = threadIdx.x % 64;
+  const bool one = a.t.n_seq <= 64;  // all sequences in the wave's lanes
+  TreeCost c{0, 1, false};
+  float steps = 0.0f, units = 0.0f;
+  for (int s0 = 0; s0 < a.t.n_seq; s0 += 64) {
+    c = tree_cost<int32_t>(a, s0 + lane);
+    steps += wave_sum(static_cast<float>(c.units) * static_cast<float>(c.steps));
+    units += wave_sum(static_cast<float>(c.units));
+  }
+  int each = INT32_MAX;  // no tile is cut
+  const float places = static_cast<float>(a.n_splits);
+  if (units < places) {
+    // one wave's sequences: the first that fits, in steps of an eighth; else what is sure to fit
+    float x = one ? steps / places : 1.001f * steps / (places - units) + 1.0f;
+    x = fmaxf(x, static_cast<float>(kKvTreeSteps));
+    each = x < 0x1p30f ? static_cast<int>(ceilf(x)) : 1 << 30;
+    while (one && each < (1 << 30) && wave_sum(static_cast<float>(c.units) * static_cast<float>(ceil_div(c.steps, each))) > places)
+      each += each / 8;
+  }
+  // the sequence that holds this block's part
+  const int at = tile_of_block(blockIdx.x, gridDim.x);
+  int s = -1, base = 0, parts = 1;
+  for (int s0 = 0; s0 < a.t.n_seq; s0 += 64) {
+    if (!one) c = tree_cost<int32_t>(a, s0 + lane);
+    const int k = ceil_div(c.steps, each), upto = base + wave_scan(c.units * k);
+    const int before = __popcll(__ballot(upto <= at));
+    if (before < 64) {
+      s = s0 + before;
+      parts = __builtin_amdgcn_readlane(k, before);
+      base = before == 0 ? base : __builtin_amdgcn_readlane(upto, before - 1);
+      break;
+    }
+    base = __builtin_amdgcn_readlane(upto, 63);
+  }
+  if (blockIdx.x == 0 && threadIdx.x < 64 && a.starts != nullptr) {  // for the join
+    int from = 0;
+    for (int s0 = 0; s0 < a.t.n_seq; s0 += 64) {
+      if (!one) c = tree_cost<int32_t>(a, s0 + lane);
+      const int k = ceil_div(c.steps, each), upto = from + wave_scan(c.units * k);
+      if (s0 + lane < a.t.n_seq) a.starts[s0 + lane] = static_cast<int64_t>(k) << 32 | (upto - c.units * k);
+      from = __builtin_amdgcn_readlane(upto, 63);
+    }
+  }
+  if (s < 0) return;
+  const int unit = __builtin_amdgcn_readfirstlane((at - base) / parts), part = at - base - unit * parts;
+  const int tile = __builtin_amdgcn_readfirstlane(unit / a.t.H), h = unit - tile * a.t.H, row0 = tile * kTileRows;
+  const Seq q = seq_of(a.t, s);
+  const TreeCost mine = tree_cost<const_i32>(a, s);
+  if (mine.bad) {  // all of its rows, of this head
+    for (int64_t i = threadIdx.x; i < static_cast<int64_t>(q.rows) * a.group * (D / 8); i += 256) {
+      const int64_t row = i / (D / 8);
+      const float none = __builtin_nanf("");
+      const float x[8] = {none, none, none, none, none, none, none, none};
+      store8<DT>(a.out, ((q.n0 + row / a.group) * a.q_heads + static_cast<int64_t>(h) * a.group + row % a.group) * D + 8 * (i % (D / 8)), x);
+    }
+    return;
+  }
+  const int len = __builtin_amdgcn_readfirstlane(ceil_div(mine.steps, parts)), step = part * len, vis = q.past + q.rows;
+  const int t0 = step < mine.steps ? 64 * step : vis;
+  const int t1 = step + len < mine.steps ? 64 * (step + len) : vis;
+  tile_rows<DT, D, true>(a, q, s, h, row0, t0, t1, parts, 0, static_cast<int64_t>(at) * kTileRows);
+}
+
+// Joins the parts of trees' tiles: 16 rows a block, eight channels a thread, PAR threads
+// side by side along a row's parts, which then meet in LDS.  Neighbouring threads have
+// neighbouring rows, as the parts lie.
+template <int D>
+constexpr int tree_join_threads(int par) { return 16 * (D / 8) * par; }
+template <int DT, int D, int PAR>
+__global__ __launch_bounds__(tree_join_threads<D>(PAR)) void kda_kv_tree_join_kernel(KvAttendArgs a) {
+  constexpr int ROWS = 16, PER = D / 8, SLICES = kTileRows / ROWS;
+  __shared__ float part_sh[PAR > 1 ? PAR - 1 : 1][10][PAR > 1 ? ROWS * PER : 1];
+  const int r = threadIdx.x % ROWS, k = threadIdx.x / ROWS % PER, par = threadIdx.x / (ROWS * PER);
+  const int slice = blockIdx.x % SLICES, unit0 = blockIdx.x / SLICES;
+  const int rt0 = unit0 % a.row_tiles, h = unit0 / a.row_tiles % a.t.H, s = unit0 / a.row_tiles / a.t.H;
+  const int64_t start = a.starts[s];
+  const TreeCost cost = tree_cost<const_i32>(a, s);
+  const int parts = static_cast<int>(start >> 32), base = static_cast<int>(start);
+  if (cost.units == 0 || cost.bad || parts == 1) return;
+  const Seq q = seq_of(a.t, s);
+  const int all_rows = q.rows * a.group;
+  for (int tile = rt0; tile < cost.units / a.t.H; tile += a.row_tiles) {
+    const int row0 = tile * kTileRows + ROWS * slice, row = row0 + r;
+    if (row0 >= all_rows) break;
+    const int64_t place0 = (base + static_cast<int64_t>(tile * a.t.H + h) * parts) * kTileRows;
+    const float* from = a.part + place0 * D + tile_piece<D>(ROWS * slice + r, k);
+    const float* ml = a.part_ml + 2 * (place0 + ROWS * slice + r);
+    float acc[8] = {}, total = 0.0f, top = -INFINITY;
+    // as the join above
+    auto join = [&](float m, float l, const float (&x)[8]) __attribute__((always_inline)) {
+      const float to = fmaxf(top, m);
+      const float f = top == to ? 1.0f : exp2_hw(top - to), y = m == to ? 1.0f : exp2_hw(m - to);
+      top = to;
+      total = fmaf(total, f, l * y);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] = fmaf(acc[e], f, x[e] * y);
+    };
+    if (row < all_rows) {
+#pragma unroll 4
+      for (int i = par; i < parts; i += PAR) {
+        const f4* at = reinterpret_cast<const f4*>(from + static_cast<int64_t>(i) * kTileRows * D);
+        const f4 x0 = at[0], x1 = at[64];
+        const float x[8] = {x0[0], x0[1], x0[2], x0[3], x1[0], x1[1], x1[2], x1[3]};
+        const f2 y = *reinterpret_cast<const f2*>(ml + static_cast<int64_t>(i) * 2 * kTileRows);
+        join(y[0], y[1], x);
+      }
+    }
+    if constexpr (PAR > 1) {
+      const int cell = threadIdx.x % (ROWS * PER);
+      if (par > 0) {
+        part_sh[par - 1][8][cell] = top;
+        part_sh[par - 1][9][cell] = total;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) part_sh[par - 1][e][cell] = acc[e];
+      }
+      __syncthreads();
+      if (par == 0) {
+#pragma unroll
+        for (int w = 0; w < PAR - 1; ++w) {
+          float x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = part_sh[w][e][cell];
+          join(part_sh[w][8][cell], part_sh[w][9][cell], x);
+        }
+      }
+      __syncthreads();
+    }
+    if (row < all_rows && par == 0) {
+      const int tok = row / a.group, g = row - tok * a.group;
+      const int64_t at = (q.n0 + tok) * a.q_heads + static_cast<int64_t>(h) * a.group + g;
+      const float inv = 1.0f / total;  // (a sum of zero: NaN, as above)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] *= inv;
+      store8<DT>(a.out, at * D + 8 * k, acc);
+    }
   }
 }
 
@@ -1832,7 +2031,8 @@ int attend(const kda_kv_pool* kv, const int32_t* page_table, int32_t max_pages, 
       !aligned(page_table, 4) || !aligned(cu_seqlens, 4) || !aligned(cache_lens, 4) || !aligned(parents, 4) ||
       q_stride * size % 16 != 0)
     return KDA_ERR_ALIGN;
-  const size_t need = kda_kv_attend_workspace(kv, max_pages, n_seq, n_tokens, max_rows, max_kv_len, q_heads, dtype);
+  const size_t need = (TREE ? kda_kv_attend_tree_workspace : kda_kv_attend_workspace)(
+      kv, max_pages, n_seq, n_tokens, max_rows, max_kv_len, q_heads, dtype);
   if (need > 0 && workspace == nullptr) return KDA_ERR_NULL;
   if (need > workspace_bytes) return KDA_ERR_ARG;
   const int64_t cover = static_cast<int64_t>(max_pages) * kv->page_tokens;
@@ -1856,8 +2056,36 @@ int attend(const kda_kv_pool* kv, const int32_t* page_table, int32_t max_pages, 
   a.sign = scale < 0.0f ? -1.0f : 1.0f;
   a.parents = parents;
   a.most_rows = TREE ? kMaxNodes : INT32_MAX;
+  a.starts = nullptr;
   a.part = static_cast<float*>(workspace);
   a.part_ml = a.part == nullptr ? nullptr : a.part + static_cast<int64_t>(p.n_splits) * n_tokens * q_heads * kv->D;
+  if constexpr (TREE) {
+    if (p.tile_rows == kTileRows) {
+      const KvTreePlan w = kv_tree_plan(kv, n_seq, max_rows, a.group, cover, max_kv_len, dtype);
+      if (w.blocks > kKvMaxBlocks || w.join_blocks > kKvMaxBlocks) return KDA_ERR_ARG;
+      a.starts = static_cast<int64_t*>(workspace);
+      a.n_splits = w.places;
+      if (w.places > 0) {
+        a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + kv_tree_head_bytes(n_seq));
+        a.part_ml = a.part + static_cast<int64_t>(w.places) * kTileRows * kv->D;
+      }
+      a.row_tiles = w.row_tiles;
+      hipStream_t st = static_cast<hipStream_t>(stream);
+      return status(by_type(dtype, kv->D, [&](auto t, auto d) {
+        constexpr int DT = decltype(t)::value, D = decltype(d)::value;
+        hipLaunchKernelGGL((kda_kv_tree_tiles_kernel<DT, D>), dim3(static_cast<uint32_t>(w.blocks)), dim3(256), 0, st, a);
+        hipError_t e = hipGetLastError();
+        if (e != hipSuccess || w.places == 0) return e;
+        const dim3 joins(static_cast<uint32_t>(w.join_blocks));
+        constexpr int PAR = 1024 / tree_join_threads<D>(1);
+        if (w.many)
+          hipLaunchKernelGGL((kda_kv_tree_join_kernel<DT, D, PAR>), joins, dim3(1024), 0, st, a);
+        else
+          hipLaunchKernelGGL((kda_kv_tree_join_kernel<DT, D, 1>), joins, dim3(tree_join_threads<D>(1)), 0, st, a);
+        return hipGetLastError();
+      }));
+    }
+  }
   const int64_t tiles = kv_tiles(p, n_seq, kv->H);
   if (tiles * p.n_splits > kKvMaxBlocks) return KDA_ERR_ARG;  // (many splits: few tiles, so the join's blocks fit too)
   hipStream_t st = static_cast<hipStream_t>(stream);
@@ -1865,9 +2093,7 @@ int attend(const kda_kv_pool* kv, const int32_t* page_table, int32_t max_pages, 
     constexpr int DT = decltype(t)::value, D = decltype(d)::value;
     const dim3 grid(static_cast<uint32_t>(tiles * p.n_splits));
     if constexpr (TREE) {
-      if (p.tile_rows == kTileRows)
-        hipLaunchKernelGGL((kda_kv_tree_tiles_kernel<DT, D>), grid, dim3(256), 0, st, a);
-      else if (p.waves == 8)
+      if (p.waves == 8)
         hipLaunchKernelGGL((kda_kv_tree_rows_kernel<DT, D, 1, 8>), grid, dim3(512), 0, st, a);
       else if (DT == KDA_F32 || p.tile_rows == 16)
         hipLaunchKernelGGL((kda_kv_tree_rows_kernel<DT, D, 1, 4>), grid, dim3(256), 0, st, a);

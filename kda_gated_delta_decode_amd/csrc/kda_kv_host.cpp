@@ -105,6 +105,27 @@ KvPlan kv_plan(int32_t H, int32_t D, int32_t n_seq, int64_t n_tokens, int32_t ma
   return p;
 }
 
+KvTreePlan kv_tree_plan(const kda_kv_pool* kv, int32_t n_seq, int32_t max_rows, int32_t group, int64_t cover,
+                        int64_t max_kv_len, kda_dtype dtype) {
+  KvTreePlan p;
+  const int64_t rows = static_cast<int64_t>(max_rows < 1 ? 1 : max_rows) * group;
+  p.row_tiles = static_cast<int32_t>((rows + 127) / 128);
+  const int64_t units = static_cast<int64_t>(n_seq) * p.row_tiles * kv->H;
+  const int64_t tokens = max_kv_len > 0 && max_kv_len < cover ? max_kv_len : cover;
+  // A place for what is resident at once (two workgroups a compute unit, one of fp32
+  // at 128 channels) and the tiles' rests; none where tiles alone fill the chip four
+  // times, or all are short.
+  const int64_t resident = dtype == KDA_F32 && kv->D == 128 ? 256 : 512;
+  const bool cut = units < 2 * resident && tokens > 64 * kKvTreeSteps;
+  p.places = cut ? static_cast<int32_t>(units + resident / 2 > resident ? units + resident / 2 : resident) : 0;
+  // (a block for every tile of any tree: sizes are hints)
+  const int64_t all = static_cast<int64_t>(n_seq) * ((static_cast<int64_t>(KDA_MAX_NODES) * group + 127) / 128) * kv->H;
+  p.blocks = p.places > all ? p.places : all;
+  p.many = p.places > 8 * static_cast<int64_t>(n_seq) * kv->H;
+  p.join_blocks = cut ? units * (128 / 16) : 0;
+  return p;
+}
+
 }  // namespace kda
 
 using namespace kda;
@@ -126,6 +147,22 @@ size_t kda_kv_attend_workspace(const kda_kv_pool* kv, int32_t max_pages, int32_t
                            max_kv_len > 0 && max_kv_len < cover ? max_kv_len : cover, q_heads, dtype);
   if (p.n_splits == 1 || kv_tiles(p, n_seq, kv->H) * p.n_splits > kKvMaxBlocks) return 0;
   return static_cast<size_t>(p.n_splits) * n_tokens * q_heads * (kv->D + 2) * sizeof(float);
+}
+
+size_t kda_kv_attend_tree_workspace(const kda_kv_pool* kv, int32_t max_pages, int32_t n_seq, int64_t n_tokens,
+                                    int32_t max_rows, int64_t max_kv_len, int32_t q_heads, kda_dtype dtype) {
+  if (kv_check(kv, max_pages, n_seq, n_tokens) != KDA_OK) return 0;
+  if (kv_check_attend(kv, n_tokens, max_rows, max_kv_len, q_heads, dtype) != KDA_OK) return 0;
+  if (max_rows > KDA_MAX_NODES || n_seq == 0 || n_tokens == 0) return 0;
+  const int64_t cover = static_cast<int64_t>(max_pages) * kv->page_tokens;
+  const KvPlan p = kv_plan(kv->H, kv->D, n_seq, n_tokens, max_rows,
+                           max_kv_len > 0 && max_kv_len < cover ? max_kv_len : cover, q_heads, dtype);
+  if (p.tile_rows < 128)
+    return kda_kv_attend_workspace(kv, max_pages, n_seq, n_tokens, max_rows, max_kv_len, q_heads, dtype);
+  const KvTreePlan w = kv_tree_plan(kv, n_seq, max_rows, q_heads / kv->H, cover, max_kv_len, dtype);
+  if (w.places == 0 || w.blocks > kKvMaxBlocks || w.join_blocks > kKvMaxBlocks) return 0;
+  return static_cast<size_t>(kv_tree_head_bytes(n_seq)) +
+         static_cast<size_t>(w.places) * 128 * (kv->D + 2) * sizeof(float);
 }
 
 int kda_kv_validate(const kda_kv_pool* kv, const int32_t* page_table_host, int32_t max_pages,
