@@ -708,7 +708,7 @@ def kda_kv_append(pool, page_table, cu_seqlens, cache_lens, k, v, q=None, q_out=
     if positions is None:
         _kv_call(torch, "kda_kv_append", dev, ctypes.byref(P), *tables, kp, vp, ks, vs, qp, qs, qo, cp, sp, *last)
     else:
-        at = _tree_table(positions, "positions", dev, torch.int32, (T,))
+        at, = _tree_tensors(dev, ((positions, "positions", torch.int32, (T,)),))
         _kv_call(torch, "kda_kv_append_at", dev, ctypes.byref(P), *tables, kp, vp, ks, vs, qp, qs, qo, cp, sp, at, *last)
 
 
@@ -753,11 +753,11 @@ def _workspace(torch, pool, dev, workspace, bytes_needed, st):
     if workspace is None:
         wn = bytes_needed()
         if wn == 0 or st == torch._C._cuda_getCurrentRawStream(dev):
-            return torch.empty(wn, dtype=torch.uint8, device=pool.device), wn
+            return pool.new_empty(wn, dtype=torch.uint8), wn
         # memory of that stream: the allocator hands it on in its order
         on = torch.cuda.ExternalStream(st, device=pool.device) if st else torch.cuda.default_stream(pool.device)
         with torch.cuda.stream(on):
-            return torch.empty(wn, dtype=torch.uint8, device=pool.device), wn
+            return pool.new_empty(wn, dtype=torch.uint8), wn
     if not _kv_is(workspace, dev, torch.uint8):
         _kv_refuse(workspace, "workspace", dev, torch.uint8)
     if not workspace.is_contiguous():
@@ -781,7 +781,7 @@ def _attend(name, pool, page_table, cu_seqlens, cache_lens, parents, q, out, max
     workspace, wn = _workspace(torch, pool, dev, workspace, lambda: getattr(_lib or library(), name + "_workspace")(
         pool_ref, tables[1], n_seq, T, rows, kv, heads, code), st)
     if parents is not None:
-        tables += (_tree_table(parents, "parents", dev, torch.int32, (T,)),)
+        tables += tuple(_tree_tensors(dev, ((parents, "parents", torch.int32, (T,)),)))
     _kv_call(torch, name, dev, pool_ref, *tables, qp, qs, op, n_seq, T, rows, kv, heads, code,
              1.0 / math.sqrt(D) if scale is None else float(scale), workspace.data_ptr(), wn, st)
 
@@ -818,22 +818,32 @@ def kda_kv_attend_tree(pool, page_table, cu_seqlens, cache_lens, parents, q, out
 # trees of drafted tokens
 # ---------------------------------------------------------------------------
 
-def _tree_table(t, name, device, dtype, shape):
-    """Address of a contiguous tensor of this type, shape and GPU."""
-    if not _kv_is(t, device, dtype):
-        _kv_refuse(t, name, device, dtype)
-    if t.shape != shape or not t.is_contiguous():
+def _tree_tensors(device, tensors):
+    """Addresses of tensors given as (tensor, name, dtype, shape): each contiguous,
+    of this type and shape, on this GPU.  (One loop: a step's launches are short.)"""
+    out = []
+    for t, name, dtype, shape in tensors:
+        try:
+            if t.get_device() == device and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+                out.append(t.data_ptr())
+                continue
+        except AttributeError:
+            pass
+        if not _kv_is(t, device, dtype):
+            _kv_refuse(t, name, device, dtype)
         raise ValueError("%s must be contiguous %s, got %s" % (name, list(shape), list(t.shape)))
-    return t.data_ptr()
+    return out
 
 
-def _tree_path(path, dev, i32, n_req):
-    """Address and width of a table of paths."""
-    if not _kv_is(path, dev, i32):
-        _kv_refuse(path, "path", dev, i32)
-    if path.dim() != 2:
-        raise ValueError("path must be [n_req, max_path], got %s" % list(path.shape))
-    return _tree_table(path, "path", dev, i32, (n_req, path.shape[1])), path.shape[1]
+def _tree_sizes(*tensors):
+    """The leading sizes of tensors (-1: none, which no shape matches)."""
+    return [s[0] if len(s) else -1 for s in (getattr(t, "shape", ()) for t in tensors)]
+
+
+def _tree_width(path):
+    """The width of a table of paths."""
+    shape = getattr(path, "shape", ())
+    return shape[1] if len(shape) == 2 else -1
 
 
 def kda_kv_keep(pool, page_table, cu_seqlens, cache_lens, path, path_lens, n_tokens: int | None = None,
@@ -845,27 +855,16 @@ def kda_kv_keep(pool, page_table, cu_seqlens, cache_lens, path, path_lens, n_tok
     import torch
     P, dev, i32 = make_kv_pool(pool), pool.get_device(), torch.int32
     tables, n_seq = _kv_tables(dev, i32, page_table, cu_seqlens, cache_lens)
-    pp, wide = _tree_path(path, dev, i32, n_seq)
-    lp = _tree_table(path_lens, "path_lens", dev, i32, (n_seq,))
+    wide = _tree_width(path)
+    pp, lp = _tree_tensors(dev, ((path, "path", i32, (n_seq, wide)), (path_lens, "path_lens", i32, (n_seq,))))
     T = 2 ** 31 - 1 if n_tokens is None else int(n_tokens)
     _kv_call(torch, "kda_kv_keep", dev, ctypes.byref(P), *tables, pp, wide, lp, n_seq, T, _kv_stream(torch, dev, stream))
 
 
-def _tree_rows(dev, T, H, **rows):
-    """Addresses of the nodes' rows: [T, H, 128] ([T, H] for b), contiguous float32."""
-    import torch
-    return [_tree_table(t, name, dev, torch.float32, (T, H) if name == "b" else (T, H, 128)) for name, t in rows.items()]
-
-
-def _tree_pool(pool, cu_seqlens, init_slot_ids, pool_dtype, state_dtype):
-    """The checked pool, its GPU, the requests and the tables' addresses."""
-    import torch
+def _tree_pool(pool, pool_dtype, state_dtype):
+    """The checked state pool, its GPU and the dtype the caller built for."""
     P = make_pool(pool, pool_dtype)
-    dev = pool.get_device()
-    n_req = init_slot_ids.shape[0] if isinstance(init_slot_ids, torch.Tensor) and init_slot_ids.dim() == 1 else -1
-    ip = _tree_table(init_slot_ids, "init_slot_ids", dev, torch.int32, (n_req,))
-    cp = _tree_table(cu_seqlens, "cu_seqlens", dev, torch.int32, (n_req + 1,))
-    return P, dev, n_req, ip, cp, P.dtype if state_dtype is None else _dtype_arg(state_dtype)
+    return P, pool.get_device(), P.dtype if state_dtype is None else _dtype_arg(state_dtype)
 
 
 def kda_decode_tree(pool, init_slot_ids, cu_seqlens, parents, q, k, v, g, b, out, max_nodes: int | None = None,
@@ -879,12 +878,16 @@ def kda_decode_tree(pool, init_slot_ids, cu_seqlens, parents, q, k, v, g, b, out
     float32 [T, H, 128]; b: [T, H]; max_nodes: the most nodes of a request
     (default: T, at most KDA_MAX_NODES)."""
     import torch
-    P, dev, n_req, ip, cp, sd = _tree_pool(pool, cu_seqlens, init_slot_ids, pool_dtype, state_dtype)
-    T = parents.shape[0] if isinstance(parents, torch.Tensor) and parents.dim() == 1 else -1
-    pp = _tree_table(parents, "parents", dev, torch.int32, (T,))
-    rows = _tree_rows(dev, T, P.H, q=q, k=k, v=v, g=g, b=b, out=out)
+    P, dev, sd = _tree_pool(pool, pool_dtype, state_dtype)
+    i32, f32 = torch.int32, torch.float32
+    n_req, T = _tree_sizes(init_slot_ids, parents)
+    row = (T, P.H, 128)
+    at = _tree_tensors(dev, (
+        (init_slot_ids, "init_slot_ids", i32, (n_req,)), (cu_seqlens, "cu_seqlens", i32, (n_req + 1,)),
+        (parents, "parents", i32, (T,)), (q, "q", f32, row), (k, "k", f32, row), (v, "v", f32, row),
+        (g, "g", f32, row), (b, "b", f32, (T, P.H)), (out, "out", f32, row)))
     most = min(T, KDA_MAX_NODES) if max_nodes is None else int(max_nodes)
-    _kv_call(torch, "kda_decode_tree", dev, ctypes.byref(P), ip, cp, pp, *rows, n_req, T, most, sd,
+    _kv_call(torch, "kda_decode_tree", dev, ctypes.byref(P), *at, n_req, T, most, sd,
              1.0 / math.sqrt(KDA_HEAD_K) if scale is None else float(scale), _kv_stream(torch, dev, stream))
 
 
@@ -895,12 +898,15 @@ def kda_decode_path(pool, init_slot_ids, cu_seqlens, path, path_lens, k, v, g, b
     path_lens: int32 [n_req]; k, v, g: float32 [T, H, 128]; b: [T, H];
     dst_slot_ids: int32 [n_req], or None to store back."""
     import torch
-    P, dev, n_req, ip, cp, sd = _tree_pool(pool, cu_seqlens, init_slot_ids, pool_dtype, state_dtype)
-    dp = 0 if dst_slot_ids is None else _tree_table(dst_slot_ids, "dst_slot_ids", dev, torch.int32, (n_req,))
-    pp, wide = _tree_path(path, dev, torch.int32, n_req)
-    lp = _tree_table(path_lens, "path_lens", dev, torch.int32, (n_req,))
-    T = k.shape[0] if isinstance(k, torch.Tensor) and k.dim() == 3 else -1
-    rows = _tree_rows(dev, T, P.H, k=k, v=v, g=g, b=b)
+    P, dev, sd = _tree_pool(pool, pool_dtype, state_dtype)
+    i32, f32 = torch.int32, torch.float32
+    n_req, T = _tree_sizes(init_slot_ids, k)
+    wide, row, ids = _tree_width(path), (T, P.H, 128), (n_req,)
+    ip, cp, pp, lp, *rows = _tree_tensors(dev, (
+        (init_slot_ids, "init_slot_ids", i32, ids), (cu_seqlens, "cu_seqlens", i32, (n_req + 1,)),
+        (path, "path", i32, (n_req, wide)), (path_lens, "path_lens", i32, ids), (k, "k", f32, row),
+        (v, "v", f32, row), (g, "g", f32, row), (b, "b", f32, (T, P.H))))
+    dp = 0 if dst_slot_ids is None else _tree_tensors(dev, ((dst_slot_ids, "dst_slot_ids", i32, ids),))[0]
     _kv_call(torch, "kda_decode_path", dev, ctypes.byref(P), ip, dp, cp, pp, wide, lp, *rows, n_req, T, sd,
              _kv_stream(torch, dev, stream))
 
@@ -944,19 +950,17 @@ def kda_verify_drafts(target, cu_seqlens, parents, tokens, accept_rand, sample_r
     T, vocab = target.shape
     tp, ts = _verify_rows(target, "target", dev, dtype, T, vocab)
     qp, qs = (0, 0) if draft is None else _verify_rows(draft, "draft", dev, dtype, T, vocab)
-    n_req = sample_rand.shape[0] if isinstance(sample_rand, torch.Tensor) and sample_rand.dim() == 1 else -1
-    sp = _tree_table(sample_rand, "sample_rand", dev, f32, (n_req,))
-    cp = _tree_table(cu_seqlens, "cu_seqlens", dev, i32, (n_req + 1,))
-    pp, xp = _tree_table(parents, "parents", dev, i32, (T,)), _tree_table(tokens, "tokens", dev, i32, (T,))
-    ap = _tree_table(accept_rand, "accept_rand", dev, f32, (T,))
-    op, wide = _tree_path(path, dev, i32, n_req)
-    lp = _tree_table(path_lens, "path_lens", dev, i32, (n_req,))
-    np_ = _tree_table(next_tokens, "next_tokens", dev, i32, (n_req,))
+    n_req, = _tree_sizes(sample_rand)
+    wide, nodes, ids = _tree_width(path), (T,), (n_req,)
+    *at, op, lp, np_ = _tree_tensors(dev, (
+        (cu_seqlens, "cu_seqlens", i32, (n_req + 1,)), (parents, "parents", i32, nodes), (tokens, "tokens", i32, nodes),
+        (accept_rand, "accept_rand", f32, nodes), (sample_rand, "sample_rand", f32, ids),
+        (path, "path", i32, (n_req, wide)), (path_lens, "path_lens", i32, ids), (next_tokens, "next_tokens", i32, ids)))
     code, st = dtype_code(dtype), _kv_stream(torch, dev, stream)
     workspace, wn = _workspace(torch, target, dev, workspace, lambda: (_lib or library()).kda_verify_workspace(
         n_req, T, vocab, wide, code), st)
-    _kv_call(torch, "kda_verify_drafts", dev, tp, ts, qp, qs, cp, pp, xp, ap, sp, op, wide, lp, np_, n_req, T, vocab,
-             code, workspace.data_ptr(), wn, st)
+    _kv_call(torch, "kda_verify_drafts", dev, tp, ts, qp, qs, *at, op, wide, lp, np_, n_req, T, vocab, code,
+              workspace.data_ptr(), wn, st)
 
 
 def kda_tree_validate(cu_seqlens_host, parents_host, n_tokens: int | None = None) -> int:
