@@ -2063,9 +2063,9 @@ int attend(const kda_kv_pool* kv, const int32_t* page_table, int32_t max_pages, 
     if (p.tile_rows == kTileRows) {
       const KvTreePlan w = kv_tree_plan(kv, n_seq, max_rows, a.group, cover, max_kv_len, dtype);
       if (w.blocks > kKvMaxBlocks || w.join_blocks > kKvMaxBlocks) return KDA_ERR_ARG;
-      a.starts = static_cast<int64_t*>(workspace);
       a.n_splits = w.places;
-      if (w.places > 0) {
+      if (w.places > 0) {  // (else the workspace may have any size)
+        a.starts = static_cast<int64_t*>(workspace);
         a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + kv_tree_head_bytes(n_seq));
         a.part_ml = a.part + static_cast<int64_t>(w.places) * kTileRows * kv->D;
       }

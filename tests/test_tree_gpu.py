@@ -140,6 +140,45 @@ def test_sizes_of_the_launch_are_hints():
     c.check(out)
 
 
+def test_a_workspace_that_is_not_needed_is_left_alone():
+    # 40 nodes x 8 query heads, tiles of 128 rows, too few tokens for parts
+    c = TreeCase([some_tree(40, 1), some_tree(9, 2)] * 3, [300, 20] * 3, heads=(8, 1), D=64, P=16).fill()
+    assert B.kda_kv_attend_tree_workspace(c.d_pool, c.d_table, c.T, c.hq, 40, 340) == 0
+    around = torch.full((4096,), 7, dtype=torch.uint8, device="cuda")
+    c.check(c.attend(workspace=around[2048:2064]))
+    assert bool((around == 7).all())
+
+
+@pytest.mark.parametrize("dtype,D", [("f32", 64), ("bf16", 128)])
+def test_large_trees_of_many_sequences(dtype, D):
+    # more sequences than a wave has lanes, of uneven sizes; some without rows
+    rng = np.random.default_rng(8)
+    rows = [int(x) for x in rng.integers(0, 65, 140)]
+    past = [int(x) for x in rng.integers(0, 200, 140)]
+    rows[3], past[3], rows[69], past[69], rows[130], past[130] = 64, 2900, 33, 1500, 17, 777
+    c = TreeCase([some_tree(n, i) for i, n in enumerate(rows)], past, dtype=dtype, heads=(8, 1), D=D, P=64).fill()
+    assert B.kda_kv_attend_tree_workspace(c.d_pool, c.d_table, c.T, c.hq, 64, 2964, dtype) > 0
+    c.check(c.attend())
+
+
+@pytest.mark.parametrize("n", [3, 70])
+@pytest.mark.parametrize("max_rows,max_kv_len", [(20, 600), (64, 100), (17, 0), (64, 1000000)])
+def test_sizes_of_large_trees_are_hints(n, max_rows, max_kv_len):
+    c = TreeCase([some_tree(64, i) if i % 7 == 2 else some_tree(5, i) for i in range(n)],
+                 [1900 if i % 35 == 2 else 13 for i in range(n)], dtype="f16", heads=(8, 1), D=64, P=64).fill()
+    c.check(c.attend(max_rows=max_rows, max_kv_len=max_kv_len))
+
+
+def test_large_trees_many_of_whose_sequences_are_bad():
+    rows = [64, 33, 64, 20, 64]
+    c = TreeCase([some_tree(n, i) for i, n in enumerate(rows)], [2000, 40, 700, 3000, 9], heads=(8, 1), D=64, P=16).fill()
+    c.d_past[1], c.d_past[3] = -1, c.table.shape[1] * 16  # no length; past the table's end
+    out = c.attend()
+    c.check(out, which=[0, 2, 4])
+    for s in (1, 3):
+        assert bool(out[c.cu[s]:c.cu[s + 1]].isnan().all())
+
+
 @pytest.mark.parametrize("heads", [(2, 2), (8, 1)])
 @pytest.mark.parametrize("past", [5, 3000])
 def test_trees_that_are_none_are_nan(heads, past):
@@ -520,6 +559,15 @@ def test_decode_path(dtype, H, elsewhere):
     check_path(s, run_path(s, paths, dst), paths, dst)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+def test_decode_path_of_many_heads(dtype):
+    # more than 128 requests x heads: whole heads; every length around a block's end
+    lens = [0, 1, 2, 3, 4, 5, 7, 8, 9, 15, 16, 17, 18, 31, 32, 33, 48, 49, 63, 64, 1, 6]
+    s = States([chain(64)] * len(lens), H=6, dtype=dtype, seed=9).put()
+    paths = [list(range(n)) for n in lens]
+    check_path(s, run_path(s, paths), paths)
+
+
 def test_decode_path_any_order_and_repeats():
     s = States([star(6), chain(5)], seed=3).put()
     paths = [[3, 1, 1, 5], [4, 0]]
@@ -861,6 +909,31 @@ def test_graph_replays(name):
         assert torch.isfinite(junk)
         for o, w in zip(outs, want):
             assert torch.equal(o, w)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+def test_graphs_of_the_largest_trees(dtype):
+    """The most nodes need the most shared memory; a first call may be a captured one."""
+    s = States([some_tree(64, 1), some_tree(50, 2), chain(64)], H=3, dtype=dtype).put()
+    c = TreeCase([some_tree(64, 1), some_tree(50, 2)], [2100, 30], dtype=dtype, heads=(16, 2), D=64, P=16).fill()
+    read, out = torch.zeros(s.T, 3, 128, device="cuda"), torch.zeros(c.T, 16, 64, dtype=TYPES[dtype], device="cuda")
+    ws = torch.empty(B.kda_kv_attend_tree_workspace(c.d_pool, c.d_table, c.T, 16, 64, 2164, dtype), dtype=torch.uint8,
+                     device="cuda")
+    assert ws.numel() > 0
+    d = s.d
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        B.kda_decode_tree(d["pool"], d["init"], d["cu"], d["up"], d["q"], d["k"], d["v"], d["g"], d["b"], read, scale=0.1,
+                          max_nodes=64)
+        B.kda_kv_attend_tree(c.d_pool, c.d_table, c.d_cu, c.d_past, c.d_up, c.q, out, max_rows=64, max_kv_len=2164,
+                             workspace=ws)
+    for _ in range(3):
+        read.zero_(), out.zero_(), ws.fill_(255)
+        graph.replay()
+        torch.cuda.synchronize()
+        s.check(read)
+        c.check(out)
 
 
 @pytest.mark.parametrize("name", ["attend", "tree", "path", "keep", "verify"])
