@@ -478,13 +478,13 @@ __global__ __launch_bounds__(256) void kda_path_kernel(PathArgs a) {
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) kk = fmaf(x[i / 4][i % 4], x[i / 4][i % 4], kk);
-        const float kn = 1.0f / sqrtf(sum16(kk) + 1e-6f);
+        const float kn = __builtin_amdgcn_rsqf(sum16(kk) + 1e-6f);
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             x[p][i] *= kn;
-            z[p][i] = expf(z[p][i]);
+            z[p][i] = exp_near(z[p][i]);
           }
           *reinterpret_cast<f4*>(&k_sh[tid / 16][4 * l16 + 64 * p]) = x[p];
           *reinterpret_cast<f4*>(&a_sh[tid / 16][4 * l16 + 64 * p]) = z[p];
@@ -640,11 +640,8 @@ extern "C" int kda_decode_path(const kda_pool* pool, const int32_t* init_slot_id
   a.H = pool->H;
   a.n_slots = pool->n_slots;
   a.max_path = max_path;
-  const dim3 grid(static_cast<uint32_t>(n_req) * pool->H);
-  hipStream_t st = static_cast<hipStream_t>(stream);
-  if (state_dtype == KDA_F32)
-    hipLaunchKernelGGL((kda_path_kernel<KDA_F32>), grid, dim3(256), 0, st, a);
-  else
-    hipLaunchKernelGGL((kda_path_kernel<KDA_F16>), grid, dim3(256), 0, st, a);
+  const auto kernel = state_dtype == KDA_F32 ? kda_path_kernel<KDA_F32> : kda_path_kernel<KDA_F16>;
+  hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(n_req) * pool->H), dim3(256), 0,
+                     static_cast<hipStream_t>(stream), a);
   return status(hipGetLastError());
 }
