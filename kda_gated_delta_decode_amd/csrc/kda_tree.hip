@@ -34,8 +34,9 @@ __device__ __forceinline__ float max16(float x) {
 }
 
 // e^x for x below 88, within 2 units of the last place (0 below 2^-126): 2^t, with
-// what rounding x log2(e) to t lost put back.
+// what rounding x log2(e) to t lost put back.  (Of an infinite t nothing is left to put.)
 __device__ __forceinline__ float exp_near(float x) {
+  x = x < -104.0f ? -104.0f : x;
   const float t = x * 1.44269504f;
   const float lost = fmaf(x, 1.44269504f, -t) + x * 1.92596299e-8f;
   const float y = __builtin_amdgcn_exp2f(t);
@@ -65,7 +66,7 @@ __device__ __forceinline__ void put_row(float* row, float* size, const float (&w
     for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(w[e]));
     most = max16(most);
     int ex = __float_as_int(most) >> 23;
-    ex = ex < 1 ? 1 : ex > 253 ? 253 : ex;
+    ex = ex < 12 ? 12 : ex > 253 ? 253 : ex;  // (2^11 over the power of two is finite)
     const float down = __int_as_float((254 - ex) << 23), up = 2048.0f * down;
 #pragma unroll
     for (int p = 0; p < 2; ++p) {

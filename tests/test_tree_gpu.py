@@ -492,6 +492,29 @@ def test_decode_tree_zero_vectors_and_gates():
     s.check(s.tree())
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("decay", [-0.9, -1.5, -3.0, -40.0, -85.0])
+def test_decode_tree_decays_to_nothing(dtype, decay):
+    # products of decays down to 2^-126 and below, in every channel at once, and zero vectors
+    s = States([chain(64), some_tree(30, 3)], seed=13, dtype=dtype)
+    s.g[:] = decay
+    s.q[70], s.k[71] = 0, 0
+    s.put()
+    s.check(s.tree())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+def test_gates_at_infinity(dtype):
+    # a decay of exactly zero, beta of exactly 0 and 1
+    s = States([some_tree(20, 3), chain(6)], seed=12, dtype=dtype)
+    s.g[3, 0], s.g[5, :, 7:90], s.g[21], s.g[8, 1, 4] = -np.inf, -np.inf, -np.inf, -np.finfo(np.float32).max
+    s.b[4], s.b[22] = np.inf, -np.inf
+    s.put()
+    s.check(s.tree())
+    paths = [list(range(20)), list(range(6))]
+    check_path(s, run_path(s, paths), paths)
+
+
 def test_decode_tree_a_bad_number_stays_on_its_paths():
     tree = [-1, 0, 0, 1, 2, -1, 5, 3]
     s = States([tree], seed=11)
