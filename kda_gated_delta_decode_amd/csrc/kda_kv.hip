@@ -1706,8 +1706,11 @@ __device__ __forceinline__ int wave_scan(int x) {
 // Trees' tiles are cut in parts of at most `each` steps, every tile of a sequence
 // alike, such that there are as many parts as places (`a.n_splits`): each = about
 // (all steps) / (places), however lengths and sizes differ.  (16 trees of up to 32
-// nodes on up to 8191 tokens, 32 / 8 heads: 95 us with splits of one length, chosen
-// for the longest sequence.)
+// nodes on up to 8191 tokens, 32 / 8 heads, bf16: 61 us with the join, 95 with splits
+// of one length, chosen for the longest sequence.)  Long caches take 970 TFLOP/s more
+// with every token, nine tenths of what a large matrix product reaches; the 61 us hold
+// 25 that do not grow with them: launches, the plan, tables and first tiles (9 of 51 us
+// of a workgroup), parts out and in again (34 MB each way).
 template <int DT, int D>
 __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tree_tiles_kernel(KvAttendArgs a) {
   const int lane = threadIdx.x % 64;
@@ -1730,7 +1733,7 @@ __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tree_tiles_
       each += each / 8;
   }
   // the sequence that holds this block's part
-  const int at = tile_of_block(blockIdx.x, gridDim.x);
+  const int at = blockIdx.x;  // (parts round the XCDs: where they are fewer than blocks, none is left out)
   int s = -1, base = 0, parts = 1;
   for (int s0 = 0; s0 < a.t.n_seq; s0 += 64) {
     if (!one) c = tree_cost<int32_t>(a, s0 + lane);

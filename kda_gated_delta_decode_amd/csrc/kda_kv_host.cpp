@@ -113,15 +113,19 @@ KvTreePlan kv_tree_plan(const kda_kv_pool* kv, int32_t n_seq, int32_t max_rows, 
   const int64_t units = static_cast<int64_t>(n_seq) * p.row_tiles * kv->H;
   const int64_t tokens = max_kv_len > 0 && max_kv_len < cover ? max_kv_len : cover;
   // A place for what is resident at once (two workgroups a compute unit, one of fp32
-  // at 128 channels) and the tiles' rests; none where tiles alone fill the chip four
-  // times, or all are short.
+  // at 128 channels) and the tiles' rests; none where tiles alone fill the chip twice,
+  // or all are short.  (16 trees of 32 nodes on 8191 tokens: 61 us, 74 with twice as
+  // many places, 77 with half.)
   const int64_t resident = dtype == KDA_F32 && kv->D == 128 ? 256 : 512;
   const bool cut = units < 2 * resident && tokens > 64 * kKvTreeSteps;
   p.places = cut ? static_cast<int32_t>(units + resident / 2 > resident ? units + resident / 2 : resident) : 0;
   // (a block for every tile of any tree: sizes are hints)
   const int64_t all = static_cast<int64_t>(n_seq) * ((static_cast<int64_t>(KDA_MAX_NODES) * group + 127) / 128) * kv->H;
   p.blocks = p.places > all ? p.places : all;
-  p.many = p.places > 8 * static_cast<int64_t>(n_seq) * kv->H;
+  // Threads side by side along parts pay from 16 parts a tile (2 trees of 64 nodes on
+  // 60000 tokens, 16 / 2 heads of 64: 45.5 us, 48.9 one after the other; of 6 and 11
+  // parts 45.2 -> 41.8 and 54.7 -> 52.2 without).
+  p.many = p.places > 16 * units;
   p.join_blocks = cut ? units * (128 / 16) : 0;
   return p;
 }

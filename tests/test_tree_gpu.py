@@ -142,8 +142,8 @@ def test_sizes_of_the_launch_are_hints():
 
 def test_a_workspace_that_is_not_needed_is_left_alone():
     # 40 nodes x 8 query heads, tiles of 128 rows, too few tokens for parts
-    c = TreeCase([some_tree(40, 1), some_tree(9, 2)] * 3, [300, 20] * 3, heads=(8, 1), D=64, P=16).fill()
-    assert B.kda_kv_attend_tree_workspace(c.d_pool, c.d_table, c.T, c.hq, 40, 340) == 0
+    c = TreeCase([some_tree(40, 1), some_tree(9, 2)] * 3, [100, 20] * 3, heads=(8, 1), D=64, P=16).fill()
+    assert B.kda_kv_attend_tree_workspace(c.d_pool, c.d_table, c.T, c.hq, 40, 140) == 0
     around = torch.full((4096,), 7, dtype=torch.uint8, device="cuda")
     c.check(c.attend(workspace=around[2048:2064]))
     assert bool((around == 7).all())
