@@ -960,7 +960,7 @@ def kda_verify_drafts(target, cu_seqlens, parents, tokens, accept_rand, sample_r
     workspace, wn = _workspace(torch, target, dev, workspace, lambda: (_lib or library()).kda_verify_workspace(
         n_req, T, vocab, wide, code), st)
     _kv_call(torch, "kda_verify_drafts", dev, tp, ts, qp, qs, *at, op, wide, lp, np_, n_req, T, vocab, code,
-              workspace.data_ptr(), wn, st)
+             workspace.data_ptr(), wn, st)
 
 
 def kda_tree_validate(cu_seqlens_host, parents_host, n_tokens: int | None = None) -> int:

@@ -961,7 +961,8 @@ __global__ __launch_bounds__(64 * NW, (kv_rows_waves<NT, NW>())) void kda_kv_tre
 // exponents, one with the value exponents.  Four tokens are read, then written; a
 // path ascends, so every source lies at or behind its destination and behind
 // the destinations of all tokens before it.  Bound by latency: path and pages,
-// then the tokens.
+// then the tokens (4 tokens of one sequence, 8 heads: 3.2 us; 128 sequences of up to 8, 12
+// heads: 5.2).
 template <int D>
 __global__ __launch_bounds__(256) void kda_kv_keep_kernel(KvKeepArgs a) {
   using Codes = std::conditional_t<D == 128, u4, u2>;
@@ -1778,7 +1779,8 @@ __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tree_tiles_
 
 // Joins the parts of trees' tiles: 16 rows a block, eight channels a thread, PAR threads
 // side by side along a row's parts, which then meet in LDS.  Neighbouring threads have
-// neighbouring rows, as the parts lie.
+// neighbouring rows, as the parts lie.  (512 parts of 128 rows and channels, 34 MB: 7.6
+// us, as fast as a large copy reads.)
 template <int D>
 constexpr int tree_join_threads(int par) { return 16 * (D / 8) * par; }
 template <int DT, int D, int PAR>

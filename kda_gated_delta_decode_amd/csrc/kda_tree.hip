@@ -139,6 +139,11 @@ constexpr int tree_lds_bytes(int nb) { return tree_rows_bytes(nb) + 9 * first_pa
 // Sixteen lanes a node up to the products, 32 PER nodes in all; there a wave has 16
 // value columns, in the solve 64 and four nodes.  COLS 64: a workgroup has half a
 // head's columns, and half its waves the keys' products, half the queries'.
+// Bound by its phases, each of which waits for the one before it (loads, the pairs up
+// the tree, products, the solve level by level): two workgroups a compute unit run
+// them beside each other.  64 ragged trees of up to 48 nodes, 12 heads, fp16 states:
+// 27.2 us, 72 MB, 2.7 TB/s of the 4.8 a large copy reaches (one node after the other: 87
+// us); 13 nodes, fp32: 7.5.
 template <int DT, int PER, int COLS>
 __global__ __launch_bounds__(kTreeThreads, 4) void kda_tree_kernel(TreeArgs a, int nb) {
   constexpr int GROUPS = kTreeThreads / 16;
@@ -427,7 +432,10 @@ __global__ __launch_bounds__(kTreeThreads, 4) void kda_tree_kernel(TreeArgs a, i
 // A workgroup for a request and head: 32 value columns a wave, 16 bytes of them
 // and R key rows a lane, so that a node's column sums stay inside the wave and the
 // nodes follow each other without a barrier.  The nodes' keys, decays and values
-// are staged sixteen at a time.
+// are staged sixteen at a time.  Bound by HBM for a batch (64 paths of up to 8 nodes, 12
+// heads, fp16: 15.7 us, 3.4 TB/s, reading and writing), by latency for one (5.1).
+// Nodes eight at a time, states updated by matrix products: 41 -> 36 us for up to 20
+// nodes of fp16 states, but fp32 47 -> 59 and 8 nodes no faster; not taken.
 template <int DT>
 __global__ __launch_bounds__(256) void kda_path_kernel(PathArgs a) {
   using T = Stored<DT>;
@@ -557,7 +565,10 @@ hipError_t launch_tree(const TreeArgs& a, hipStream_t st) {
                        nb);
     return hipGetLastError();
   };
-  // Half heads where whole ones would leave half the chip idle.
+  // Half heads where whole ones would leave half the chip idle (13 nodes, fp32, 12 units
+  // of a request and head: 8.3 -> 7.5 us; 24 nodes, 120 units, 11.3 -> 10.4; 144 units
+  // 12.4 -> 13.4, 768 of fp16 27.4 -> 35.8).  Up to 32 nodes a node has one turn's registers
+  // (24 nodes, 480 units, fp16: 14.9 us, 15.3 with the larger form).
   const bool half = units <= 128;
   if (nb <= 32) return half ? launch(kda_tree_kernel<DT, 1, 64>, 2) : launch(kda_tree_kernel<DT, 1, 128>, 1);
   return half ? launch(kda_tree_kernel<DT, 2, 64>, 2) : launch(kda_tree_kernel<DT, 2, 128>, 1);

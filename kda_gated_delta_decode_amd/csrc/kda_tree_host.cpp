@@ -25,7 +25,8 @@ int verify_check(int32_t n_req, int64_t n_tokens, int32_t vocab, int32_t max_pat
 }
 
 VerifyPlan verify_plan(int32_t vocab) {
-  // at most 64 runs, a lane each where they are searched; of whole loads of a wave
+  // At most 64 runs, a lane each where they are searched; of whole loads of a wave.  (One
+  // chain over 32768: 7.0 us, 7.9 with runs of 2048, 11.4 of 8192.)
   const int64_t each = (static_cast<int64_t>(vocab) + 63) / 64, run = (each + 511) / 512 * 512;
   return {static_cast<int32_t>((vocab + run - 1) / run), static_cast<int32_t>(run)};
 }

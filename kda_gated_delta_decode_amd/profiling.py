@@ -36,7 +36,9 @@ DECODE_KERNEL = "kda_decode_tile"
 
 # files a kernel's code and launch shapes also come from
 KERNEL_HEADERS = ("kda_launch.h", "kda_device.h", "kda_internal.h")
-MORE_SOURCES = {"kda_kv.hip": ("kda_kv.h", "kda_kv_host.cpp")}
+TREE_SOURCES = ("kda_tree.h", "kda_tree_device.h", "kda_tree_host.cpp")
+MORE_SOURCES = {"kda_kv.hip": ("kda_kv.h", "kda_kv_host.cpp", "kda_tree_device.h"), "kda_tree.hip": TREE_SOURCES,
+                "kda_verify.hip": TREE_SOURCES}
 
 
 def kernel_sources(src: str) -> tuple:
