@@ -764,7 +764,7 @@ int kda_kv_keep(const kda_kv_pool* kv, const int32_t* page_table, int32_t max_pa
  *  init_slot_ids  device int32 [n_req], may repeat; a request whose slot is
  *                 out of range has NaN rows.
  *  q, k, g, v     device fp32 [n_tokens, H, 128]; b device fp32 [n_tokens, H];
- *  out            device fp32 [n_tokens, H, 128].
+ *  out            device fp32 [n_tokens, H, 128], apart from every input.
  *  max_nodes      the most nodes of a request, in [0, KDA_MAX_NODES]: it chooses
  *                 the kernel.  A request with more nodes has NaN rows, as has one
  *                 with a parent that does not lie before its node.

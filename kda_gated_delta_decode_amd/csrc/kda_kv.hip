@@ -1718,14 +1718,14 @@ __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tree_tiles_
   const bool one = a.t.n_seq <= 64;  // all sequences in the wave's lanes
   TreeCost c{0, 1, false};
   float steps = 0.0f, units = 0.0f;
-  for (int s0 = 0; s0 < a.t.n_seq; s0 += 64) {
+  for (int s0 = 0; s0 < a.t.n_seq && (one || a.n_splits > 0); s0 += 64) {
     c = tree_cost<int32_t>(a, s0 + lane);
     steps += wave_sum(static_cast<float>(c.units) * static_cast<float>(c.steps));
     units += wave_sum(static_cast<float>(c.units));
   }
   int each = INT32_MAX;  // no tile is cut
   const float places = static_cast<float>(a.n_splits);
-  if (units < places) {
+  if (a.n_splits > 0 && units < places) {
     // one wave's sequences: the first that fits, in steps of an eighth; else what is sure to fit
     float x = one ? steps / places : 1.001f * steps / (places - units) + 1.0f;
     x = fmaxf(x, static_cast<float>(kKvTreeSteps));

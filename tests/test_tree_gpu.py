@@ -161,6 +161,16 @@ def test_large_trees_of_many_sequences(dtype, D):
     c.check(c.attend())
 
 
+def test_large_trees_that_fill_the_chip_uncut():
+    # so many tiles that none is cut, more sequences than two waves have lanes
+    rng = np.random.default_rng(9)
+    rows = [int(x) for x in rng.integers(0, 65, 140)]
+    c = TreeCase([some_tree(n, i) for i, n in enumerate(rows)], [int(x) for x in rng.integers(0, 300, 140)], dtype="bf16",
+                 heads=(16, 2), D=64, P=32).fill()
+    assert B.kda_kv_attend_tree_workspace(c.d_pool, c.d_table, c.T, c.hq, 64, 364, "bf16") == 0
+    c.check(c.attend(max_rows=64, max_kv_len=364))
+
+
 @pytest.mark.parametrize("n", [3, 70])
 @pytest.mark.parametrize("max_rows,max_kv_len", [(20, 600), (64, 100), (17, 0), (64, 1000000)])
 def test_sizes_of_large_trees_are_hints(n, max_rows, max_kv_len):
