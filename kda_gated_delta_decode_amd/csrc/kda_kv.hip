@@ -1677,30 +1677,32 @@ __global__ __launch_bounds__(256) void kda_kv_join_kernel(KvAttendArgs a, int ti
 // What a sequence's tiles of 128 rows (times cached heads) take, in steps of 64 tokens.
 struct TreeCost {
   int units, steps;
+  int n0, rows, past;
   bool bad;
 };
 // INT: const_i32 for a sequence that is the wave's, int32_t for one that is the lane's
 template <typename INT>
 __device__ __forceinline__ TreeCost tree_cost(const KvAttendArgs& a, int s) {
-  if (s >= a.t.n_seq) return {0, 1, false};
+  if (s >= a.t.n_seq) return {0, 1, 0, 0, 0, false};
   const INT *cu = (const INT*)a.t.cu, *lens = (const INT*)a.t.past;
   const int64_t n0 = cu[s], n1 = cu[s + 1], past = lens[s], rows = n1 - n0;
-  if (n0 < 0 || rows <= 0 || n1 > a.t.n_tokens) return {0, 1, false};
+  if (n0 < 0 || rows <= 0 || n1 > a.t.n_tokens) return {0, 1, 0, 0, 0, false};
+  const int at = static_cast<int>(n0), all = static_cast<int>(rows), before = static_cast<int>(past);
   if (past < 0 || rows > a.most_rows || past + rows > (static_cast<int64_t>(a.t.max_pages) << a.t.log_p))
-    return {a.t.H, 1, true};
+    return {a.t.H, 1, at, all, before, true};
   return {static_cast<int>(rows * a.group + kTileRows - 1) / kTileRows * a.t.H, static_cast<int>((past + rows + 63) / 64),
-          false};
+          at, all, before, false};
 }
 __device__ __forceinline__ int ceil_div(int x, int y) { return static_cast<int>((static_cast<uint32_t>(x) + y - 1) / static_cast<uint32_t>(y)); }
 
-// running sum over the lanes of a wave
+// running sum over the lanes of a wave: along rows of 16, then over the rows
 __device__ __forceinline__ int wave_scan(int x) {
-  const int lane = threadIdx.x % 64;
-#pragma unroll
-  for (int m = 1; m < 64; m *= 2) {
-    const int y = __shfl_up(x, m);
-    x += lane >= m ? y : 0;
-  }
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);  // row_shr:1
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);  // row_bcast:15, to rows 1 and 3
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);  // row_bcast:31, to rows 2 and 3
   return x;
 }
 
@@ -1735,13 +1737,19 @@ __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tree_tiles_
   }
   // the sequence that holds this block's part
   const int at = blockIdx.x;  // (parts round the XCDs: where they are fewer than blocks, none is left out)
-  int s = -1, base = 0, parts = 1;
+  int s = -1, base = 0, parts = 1, all = 1;
+  Seq q{0, 0, 0, false, false};
   for (int s0 = 0; s0 < a.t.n_seq; s0 += 64) {
     if (!one) c = tree_cost<int32_t>(a, s0 + lane);
     const int k = ceil_div(c.steps, each), upto = base + wave_scan(c.units * k);
     const int before = __popcll(__ballot(upto <= at));
     if (before < 64) {
       s = s0 + before;
+      q.n0 = __builtin_amdgcn_readlane(c.n0, before);
+      q.rows = __builtin_amdgcn_readlane(c.rows, before);
+      q.past = __builtin_amdgcn_readlane(c.past, before);
+      q.bad = __builtin_amdgcn_readlane(c.bad, before) != 0;
+      all = __builtin_amdgcn_readlane(c.steps, before);
       parts = __builtin_amdgcn_readlane(k, before);
       base = before == 0 ? base : __builtin_amdgcn_readlane(upto, before - 1);
       break;
@@ -1760,9 +1768,7 @@ __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tree_tiles_
   if (s < 0) return;
   const int unit = __builtin_amdgcn_readfirstlane((at - base) / parts), part = at - base - unit * parts;
   const int tile = __builtin_amdgcn_readfirstlane(unit / a.t.H), h = unit - tile * a.t.H, row0 = tile * kTileRows;
-  const Seq q = seq_of(a.t, s);
-  const TreeCost mine = tree_cost<const_i32>(a, s);
-  if (mine.bad) {  // all of its rows, of this head
+  if (q.bad) {  // all of its rows, of this head
     for (int64_t i = threadIdx.x; i < static_cast<int64_t>(q.rows) * a.group * (D / 8); i += 256) {
       const int64_t row = i / (D / 8);
       const float none = __builtin_nanf("");
@@ -1771,9 +1777,9 @@ __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tree_tiles_
     }
     return;
   }
-  const int len = __builtin_amdgcn_readfirstlane(ceil_div(mine.steps, parts)), step = part * len, vis = q.past + q.rows;
-  const int t0 = step < mine.steps ? 64 * step : vis;
-  const int t1 = step + len < mine.steps ? 64 * (step + len) : vis;
+  const int len = __builtin_amdgcn_readfirstlane(ceil_div(all, parts)), step = part * len, vis = q.past + q.rows;
+  const int t0 = step < all ? 64 * step : vis;
+  const int t1 = step + len < all ? 64 * (step + len) : vis;
   tile_rows<DT, D, true>(a, q, s, h, row0, t0, t1, parts, 0, static_cast<int64_t>(at) * kTileRows);
 }
 
