@@ -999,6 +999,39 @@ def test_workspaces_of_other_streams():
         assert np.array_equal(a, b)
 
 
+@pytest.mark.parametrize("heads", [(2, 2), (8, 2)])
+def test_caches_beyond_32_bits(heads):
+    c = TreeCase([some_tree(20, 1), some_tree(64, 2)], [700, 300], heads=heads, D=128, P=256, seed=30).fill()
+    want, path, lens = c.attend(), i32([[0, 4, 9], [1, 30, 63]]), i32([3, 3])
+    n = 5 * 2 ** 30 // c.d_pool[0].numel()
+    big = torch.zeros((n, *c.d_pool.shape[1:]), dtype=torch.uint8, device="cuda")
+    big[-c.n_pages:] = c.d_pool
+    small, small_table = c.d_pool, c.d_table
+    c.d_pool, c.d_table = big, torch.where(small_table < 0, small_table, small_table + (n - c.n_pages))
+    assert torch.equal(c.attend(), want)
+    B.kda_kv_keep(small, small_table, c.d_cu, c.d_past, path, lens)
+    B.kda_kv_keep(big, c.d_table, c.d_cu, c.d_past, path, lens)
+    assert torch.equal(big[-c.n_pages:], small) and not bool(big[:-c.n_pages].any())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+def test_pools_beyond_32_bits(dtype):
+    s = States([some_tree(20, 1), some_tree(64, 2), chain(3)], H=3, dtype=dtype, seed=31).put()
+    want, paths = s.tree(), [T.path_to(s.trees[0], 19), T.path_to(s.trees[1], 63), [0, 1]]
+    moved = run_path(s, paths)
+    n = 5 * 2 ** 30 // (s.pool[0].numel() * s.pool.element_size())
+    pool = torch.zeros((n, *s.pool.shape[1:]), dtype=s.pool.dtype, device="cuda")
+    pool[-s.slots:] = s.d["pool"]
+    s.d["pool"], s.d["init"] = pool, s.d["init"] + (n - s.slots)
+    assert torch.equal(s.tree(), want)
+    table = np.zeros((3, 64), np.int32)
+    for r, p in enumerate(paths):
+        table[r, :len(p)] = p
+    d = s.d
+    B.kda_decode_path(pool, d["init"], d["cu"], dev(table), i32([len(p) for p in paths]), d["k"], d["v"], d["g"], d["b"])
+    assert torch.equal(pool[-s.slots:].cpu(), moved) and not bool(pool[:-s.slots].any())
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16"])
 def test_a_whole_step(dtype):
     """A step over trees, then the accepted path's entries and states: the same as
