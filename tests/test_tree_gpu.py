@@ -237,6 +237,48 @@ def test_a_missing_page_is_nan(past, page):
         assert np.isnan(got[a + i]).all() == seen
 
 
+@pytest.mark.parametrize("dtype,D", [("f32", 64), ("f16", 128), ("bf16", 64), ("bf16", 128)])
+@pytest.mark.parametrize("past", [20, 1500])
+def test_a_poisoned_node_of_a_large_tree(dtype, D, past):
+    # tiles of 128 rows, in one part and in many; the node's own page holds others too
+    tree = some_tree(60, 5, roots=2)
+    c = TreeCase([tree], [past], dtype=dtype, heads=(8, 2), D=D, P=64).fill()
+    assert T.path_to(tree, 59)[0] in (0, 1)
+    at = past + 7
+    O.Block(c.pool[c.table[0, at // 64], 1]).ke[at % 64] = 255  # node 7, cached head 1
+    c.d_pool = dev(c.pool)
+    got = host(c.attend())
+    for i in range(60):
+        spoiled = 7 in T.path_to(tree, i)
+        assert np.isnan(got[i, 4:]).all() == spoiled and np.isfinite(got[i, :4]).all()
+        assert spoiled or np.isfinite(got[i]).all()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("past", [20, 1500])
+def test_exponents_outside_fp16_in_a_large_tree(dtype, past):
+    # a small key and a small value late in the context and in a node: the tiles go on in bf16
+    c = TreeCase([some_tree(64, 6)], [past], dtype=dtype, heads=(8, 2), D=64, P=64).fill()
+    for at in (past - 3, past + 9):
+        b = O.Block(c.pool[c.table[0, at // 64], 0])
+        b.ke[at % 64], b.ve[:, at % 64] = 90, 80
+    c.d_pool = dev(c.pool)
+    c.check(c.attend())
+
+
+def test_large_trees_in_place_with_strides_and_bad_sequences():
+    c = TreeCase([some_tree(60, 1), some_tree(40, 2), some_tree(3, 3)], [900, 0, 5], heads=(8, 2), D=64, P=64, dtype="bf16",
+                 seed=3).fill()
+    c.d_past[1] = -1
+    out = c.attend()
+    c.check(out, which=[0, 2])
+    assert np.isnan(host(out)[60:100]).all()
+    q = c.q.contiguous()
+    B.kda_kv_attend_tree(c.d_pool, c.d_table, c.d_cu, c.d_past, c.d_up, q, q, max_rows=60, max_kv_len=960)
+    torch.cuda.synchronize()
+    assert torch.equal(q.view(torch.int16), out.view(torch.int16))
+
+
 def test_attend_tree_in_place_with_strides_and_bad_sequences():
     c = TreeCase([some_tree(7, 1), some_tree(4, 2), some_tree(3, 3)], [20, -1, 5], heads=(2, 2), D=64, P=16, dtype="f16",
                  seed=3)
