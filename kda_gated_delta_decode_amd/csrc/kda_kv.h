@@ -3,6 +3,7 @@
 // gfx950 kernels (kda_kv.hip).  Internal header.
 #pragma once
 
+#include <math.h>
 #include <stddef.h>
 #include <stdint.h>
 
@@ -122,6 +123,27 @@ struct KvTreePlan {
 };
 KvTreePlan kv_tree_plan(const kda_kv_pool* kv, int32_t n_seq, int32_t max_rows, int32_t group, int64_t cover,
                         int64_t max_kv_len, kda_dtype dtype);
+// A tile of `steps` steps in parts of at most `each`.
+KDA_HD inline int kv_tree_parts(int steps, int each) {
+  return static_cast<int>((static_cast<uint32_t>(steps) + each - 1) / static_cast<uint32_t>(each));
+}
+// The most steps of a part, such that all parts find a place (INT32_MAX: no tile is
+// cut).  steps, units: tiles (times cached heads) and their steps, of all sequences;
+// parts(each): how many parts that makes, asked only where `one`.  one: the first
+// length from steps / places on that fits, an eighth longer from one to the next
+// (one step below 8, where an eighth is none); it is found, for parts that hold
+// whole tiles are as many as units.  Else a length that is sure to fit: parts are at
+// most steps / each + units.
+template <typename PARTS>
+KDA_HD inline int kv_tree_each(float steps, float units, int32_t places, bool one, const PARTS& parts) {
+  const float room = static_cast<float>(places);
+  if (places <= 0 || units >= room) return INT32_MAX;
+  float x = one ? steps / room : 1.001f * steps / (room - units) + 1.0f;
+  x = fmaxf(x, static_cast<float>(kKvTreeSteps));
+  int each = x < 0x1p30f ? static_cast<int>(ceilf(x)) : 1 << 30;
+  while (one && each < (1 << 30) && parts(each) > room) each += each < 8 ? 1 : each / 8;
+  return each;
+}
 // Workspace: where each sequence's parts begin and how many a tile has, then the
 // places, then their rows' maxima and sums.
 inline int64_t kv_tree_head_bytes(int32_t n_seq) { return (static_cast<int64_t>(n_seq) + 31) / 32 * 32 * 8; }

@@ -1693,7 +1693,6 @@ __device__ __forceinline__ TreeCost tree_cost(const KvAttendArgs& a, int s) {
   return {static_cast<int>(rows * a.group + kTileRows - 1) / kTileRows * a.t.H, static_cast<int>((past + rows + 63) / 64),
           at, all, before, false};
 }
-__device__ __forceinline__ int ceil_div(int x, int y) { return static_cast<int>((static_cast<uint32_t>(x) + y - 1) / static_cast<uint32_t>(y)); }
 
 // running sum over the lanes of a wave: along rows of 16, then over the rows
 __device__ __forceinline__ int wave_scan(int x) {
@@ -1725,23 +1724,16 @@ __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tree_tiles_
     steps += wave_sum(static_cast<float>(c.units) * static_cast<float>(c.steps));
     units += wave_sum(static_cast<float>(c.units));
   }
-  int each = INT32_MAX;  // no tile is cut
-  const float places = static_cast<float>(a.n_splits);
-  if (a.n_splits > 0 && units < places) {
-    // one wave's sequences: the first that fits, in steps of an eighth; else what is sure to fit
-    float x = one ? steps / places : 1.001f * steps / (places - units) + 1.0f;
-    x = fmaxf(x, static_cast<float>(kKvTreeSteps));
-    each = x < 0x1p30f ? static_cast<int>(ceilf(x)) : 1 << 30;
-    while (one && each < (1 << 30) && wave_sum(static_cast<float>(c.units) * static_cast<float>(ceil_div(c.steps, each))) > places)
-      each += each / 8;
-  }
+  const int each = kv_tree_each(steps, units, a.n_splits, one, [&](int e) __attribute__((always_inline)) {
+    return wave_sum(static_cast<float>(c.units) * static_cast<float>(kv_tree_parts(c.steps, e)));
+  });
   // the sequence that holds this block's part
   const int at = blockIdx.x;  // (parts round the XCDs: where they are fewer than blocks, none is left out)
   int s = -1, base = 0, parts = 1, all = 1;
   Seq q{0, 0, 0, false, false};
   for (int s0 = 0; s0 < a.t.n_seq; s0 += 64) {
     if (!one) c = tree_cost<int32_t>(a, s0 + lane);
-    const int k = ceil_div(c.steps, each), upto = base + wave_scan(c.units * k);
+    const int k = kv_tree_parts(c.steps, each), upto = base + wave_scan(c.units * k);
     const int before = __popcll(__ballot(upto <= at));
     if (before < 64) {
       s = s0 + before;
@@ -1760,7 +1752,7 @@ __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tree_tiles_
     int from = 0;
     for (int s0 = 0; s0 < a.t.n_seq; s0 += 64) {
       if (!one) c = tree_cost<int32_t>(a, s0 + lane);
-      const int k = ceil_div(c.steps, each), upto = from + wave_scan(c.units * k);
+      const int k = kv_tree_parts(c.steps, each), upto = from + wave_scan(c.units * k);
       if (s0 + lane < a.t.n_seq) a.starts[s0 + lane] = static_cast<int64_t>(k) << 32 | (upto - c.units * k);
       from = __builtin_amdgcn_readlane(upto, 63);
     }
@@ -1777,7 +1769,7 @@ __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tree_tiles_
     }
     return;
   }
-  const int len = __builtin_amdgcn_readfirstlane(ceil_div(all, parts)), step = part * len, vis = q.past + q.rows;
+  const int len = __builtin_amdgcn_readfirstlane(kv_tree_parts(all, parts)), step = part * len, vis = q.past + q.rows;
   const int t0 = step < all ? 64 * step : vis;
   const int t1 = step + len < all ? 64 * (step + len) : vis;
   tile_rows<DT, D, true>(a, q, s, h, row0, t0, t1, parts, 0, static_cast<int64_t>(at) * kTileRows);

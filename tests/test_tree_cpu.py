@@ -381,3 +381,116 @@ def test_constants_and_exports():
     for name in ("kda_decode_tree", "kda_decode_path", "kda_kv_attend_tree", "kda_kv_keep", "kda_verify_drafts",
                  "kda_verify_workspace", "kda_tree_validate"):
         assert getattr(pkg, name) is getattr(B, name)
+
+
+PLAN_MAIN = r"""
+#include <algorithm>
+#include <cstdio>
+#include <cstdlib>
+#include <random>
+#include <vector>
+#include "kda_kv.h"
+struct Tree { int rows; int64_t past; };
+static int64_t cut_launches = 0, first_did_not_fit = 0;
+static std::mt19937 rng(1);
+static int pick(int lo, int hi) { return lo + static_cast<int>(rng() % static_cast<uint32_t>(hi - lo + 1)); }
+static int spread(int lo, int hi) {  // over the logarithm
+  return std::min(hi, static_cast<int>(lo * std::pow(static_cast<double>(hi + 1) / lo, rng() % 4096 / 4096.0)));
+}
+// The kernel's choice for these trees under a launch planned with the given sizes:
+// found in few rounds, every part with a place, every tile's steps covered once.
+static void launch(const std::vector<Tree>& trees, int H, int group, int D, kda_dtype dtype, int max_rows, int64_t max_kv_len) {
+  const int n = static_cast<int>(trees.size());
+  kda_kv_pool kv{};
+  kv.H = H;
+  kv.D = D;
+  kv.page_tokens = 64;
+  const int64_t cover = 1ll << 31;
+  const kda::KvTreePlan plan = kda::kv_tree_plan(&kv, n, max_rows, group, cover, max_kv_len, dtype);
+  std::vector<int> units(n), steps(n);
+  float all_steps = 0.0f, all_units = 0.0f;
+  int64_t tiles = 0;
+  for (int i = 0; i < n; ++i) {
+    units[i] = trees[i].rows == 0 ? 0 : (trees[i].rows * group + 127) / 128 * H;
+    steps[i] = static_cast<int>((trees[i].past + trees[i].rows + 63) / 64);
+    all_steps += static_cast<float>(units[i]) * static_cast<float>(steps[i]);
+    all_units += static_cast<float>(units[i]);
+    tiles += units[i];
+  }
+  const auto fail = [&](const char* what, int each) {
+    std::printf("%s: %d trees, %d x %d heads of %d, type %d, rows %d (%d), tokens %lld (%lld), places %d, each %d\n", what, n,
+                H, group, D, static_cast<int>(dtype), trees[0].rows, max_rows, static_cast<long long>(trees[0].past),
+                static_cast<long long>(max_kv_len), plan.places, each);
+    std::exit(1);
+  };
+  int rounds = 0;
+  const int each = kda::kv_tree_each(all_steps, all_units, plan.places, n <= 64, [&](int e) {
+    if (++rounds > 200) fail("does not end", e);
+    float parts = 0.0f;
+    for (int i = 0; i < n; ++i) parts += static_cast<float>(units[i]) * static_cast<float>(kda::kv_tree_parts(steps[i], e));
+    return parts;
+  });
+  first_did_not_fit += rounds > 1;
+  int64_t parts = 0;
+  for (int i = 0; i < n; ++i) {
+    if (units[i] == 0) continue;
+    const int k = kda::kv_tree_parts(steps[i], each), len = kda::kv_tree_parts(steps[i], k);
+    if (k < 1 || static_cast<int64_t>(k) * len < steps[i] || len > each) fail("steps left out", each);
+    parts += static_cast<int64_t>(units[i]) * k;
+  }
+  // uncut: a block for every tile; cut: a place for every part, and a block
+  if (each != INT32_MAX) {
+    ++cut_launches;
+    if (parts > plan.places) fail("parts without a place", each);
+  } else if (parts != tiles) {
+    fail("cut without places", each);
+  }
+  if (parts > plan.blocks) fail("parts without a block", each);
+}
+int main() {
+  const int heads[][2] = {{8, 4}, {2, 8}, {4, 5}, {1, 8}, {8, 2}, {12, 3}, {1, 128}, {64, 2}, {96, 8}};
+  for (const auto& h : heads)
+    for (int n = 1; n <= 64; ++n)
+      for (int nodes : {9, 17, 25, 32, 33, 48, 64})
+        for (int past : {0, 129, 161, 200, 257, 300, 400, 512, 650, 700, 967, 1000, 1100, 1500, 1900, 2500, 4000, 9000, 60000}) {
+          if (nodes * h[1] <= 64) continue;
+          // all alike, then of uneven lengths and sizes below these
+          std::vector<Tree> trees(n, Tree{nodes, past});
+          for (int uneven = 0; uneven < 2; ++uneven) {
+            for (Tree& t : trees)
+              if (uneven) t = {pick(0, nodes), spread(1, past + 1) - 1};
+            launch(trees, h[0], h[1], 128, KDA_BF16, nodes, past + nodes);
+            launch(trees, h[0], h[1], 128, KDA_F32, nodes, past + nodes);
+          }
+        }
+  for (int i = 0; i < 300000; ++i) {  // any number of requests, hints that need not hold
+    const int n = spread(1, 700), H = spread(1, 96), group = spread(1, 64);
+    const int long_one = rng() % 4 == 0 ? 2000000000 : 70000;
+    std::vector<Tree> trees(n);
+    for (Tree& t : trees) t = {pick(0, 64), spread(1, long_one) - 1};
+    if (rng() % 3 == 0) trees.assign(n, trees[0]);
+    launch(trees, H, group, rng() % 2 ? 64 : 128, rng() % 2 ? KDA_F16 : KDA_F32, pick(0, 64), rng() % 3 == 0 ? 0 : spread(1, long_one));
+  }
+  if (cut_launches < 100000 || first_did_not_fit < 10000) {
+    std::printf("%lld, %lld\n", static_cast<long long>(cut_launches), static_cast<long long>(first_did_not_fit));
+    return 1;
+  }
+  std::puts("tree plans ok");
+  return 0;
+}
+"""
+
+
+def test_parts_of_large_trees_are_found_and_have_places(tmp_path):
+    # the choice that every block of the attention makes for itself, over the sizes it meets
+    if not shutil.which("g++"):
+        pytest.skip("no g++")
+    csrc = os.path.join(ROOT, "kda_gated_delta_decode_amd", "csrc")
+    src, exe = tmp_path / "main.cpp", tmp_path / "tree_plan"
+    src.write_text(PLAN_MAIN)
+    b = subprocess.run(["g++", "-std=c++17", "-O1", "-g", "-fsanitize=address,undefined", "-fno-sanitize-recover=all",
+                        "-Wall", "-Wextra", "-Werror", "-I", os.path.join(ROOT, "include"), "-I", csrc, str(src),
+                        os.path.join(csrc, "kda_kv_host.cpp"), "-o", str(exe)], capture_output=True, text=True)
+    assert b.returncode == 0, b.stdout + b.stderr
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "tree plans ok" in r.stdout, r.stdout + r.stderr

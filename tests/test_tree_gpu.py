@@ -189,6 +189,30 @@ def test_large_trees_many_of_whose_sequences_are_bad():
         assert bool(out[c.cu[s]:c.cu[s + 1]].isnan().all())
 
 
+@pytest.mark.parametrize("n,nodes,past,heads,D,dtype", [
+    (25, 32, 400, (32, 8), 128, "bf16"), (15, 32, 1020, (32, 8), 128, "bf16"), (3, 48, 1960, (32, 8), 128, "f16"),
+    (50, 20, 390, (16, 4), 64, "f16"), (43, 20, 390, (8, 2), 128, "f32"), (64, 10, 390, (24, 3), 64, "bf16")])
+@pytest.mark.parametrize("uneven", [False, True])
+def test_large_trees_whose_first_parts_have_no_place(n, nodes, past, heads, D, dtype, uneven):
+    # parts of (all steps) / (places) steps, rounded up, would be more than the places
+    rng = np.random.default_rng(n)
+    rows, lens = [nodes] * n, [past] * n
+    if uneven:
+        rows = [int(x) for x in rng.integers(nodes - 2, nodes + 1, n)]
+        lens = [int(x) for x in rng.integers(past - past // 40, past + 1, n)]
+    c = TreeCase([some_tree(m, i) for i, m in enumerate(rows)], lens, dtype=dtype, heads=heads, D=D, P=64, seed=n).fill()
+    units = np.array([-(-m * (heads[0] // heads[1]) // 128) * heads[1] for m in rows])
+    steps = np.array([-(-(m + t) // 64) for m, t in zip(rows, lens)])
+    most = max(a + b for a, b in zip(rows, lens))
+    work = B.kda_kv_attend_tree_workspace(c.d_pool, c.d_table, c.T, c.hq, max(rows), most, dtype)
+    places = (work - (n + 31) // 32 * 256) // (128 * (D + 2) * 4)
+    first = max(3, -(-int((units * steps).sum()) // places))
+    assert 3 <= first < 8 and (units * -(-steps // first)).sum() > places > units.sum()
+    out = c.attend()
+    assert bool(out.isfinite().all())
+    c.check(out, which=sorted({0, 1, n // 2, n - 2, n - 1}))
+
+
 @pytest.mark.parametrize("heads", [(2, 2), (8, 1)])
 @pytest.mark.parametrize("past", [5, 3000])
 def test_trees_that_are_none_are_nan(heads, past):
