@@ -721,8 +721,10 @@ int kda_kv_append_at(const kda_kv_pool* kv, const int32_t* page_table, int32_t m
  * kda_kv_attend_tree -- kda_kv_attend for a tree's nodes: node i of sequence s,
  * cached at position cache_lens[s] + i, sees the cache_lens[s] tokens of the
  * context, the nodes on its path and itself.  Everything else is
- * kda_kv_attend's, precision included; workspace: kda_kv_attend_tree_workspace()
- * bytes for the same arguments.
+ * kda_kv_attend's; workspace: kda_kv_attend_tree_workspace() bytes for the same
+ * arguments.  So is the precision, more than 64 rows of a sequence and cached head
+ * (max_rows * q_heads / H) counting as a prompt, but for fp16 weights, which then keep
+ * 22 bits, not 11 (down to 2^-32 of the largest).
  *  parents   device int32 [n_tokens], 4-byte aligned (see above).
  *  max_rows  at most KDA_MAX_NODES (else KDA_ERR_ROWS, checked with the counts).
  * The rows of a sequence of more than KDA_MAX_NODES nodes, or with a parent

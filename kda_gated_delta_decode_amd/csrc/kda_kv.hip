@@ -1095,7 +1095,11 @@ struct ExpRange {
 // weights, at most 2^15, keep 11 bits down to 2^-21 of the largest, in both sums
 // alike: fp16 chunks are off by 2.45e-4 of their norm, 2.06e-4 with a second fp16
 // piece of each weight, which takes 207 us instead of 152 (8192 fp16 rows 737
-// instead of 529); bf16 outputs do not show it.  One product for each operand
+// instead of 529); bf16 outputs do not show it.  fp16 trees keep the second piece, as
+// their 64 rows and less do, so that a node's error does not depend on how many others
+// there are: 2.07e-4 of their norm, as in fp32 weights, 2.7e-4 to 2.9e-4 without (16
+// trees of up to 32 nodes on up to 8191 tokens, 32 / 8 heads: 71 us, 57 without; 8 of 48
+// on 1500, 16 / 2 heads of 64: 18.9 and 18.0).  One product for each operand
 // then does what two or three bf16 pieces do.  The exponents are looked at
 // before their tiles are added, two tiles at a time: a block that
 // meets another one goes on from there in bf16 pieces, with the sums that it has
@@ -1164,7 +1168,7 @@ __device__ __forceinline__ void tile_rows(const KvAttendArgs& a, const Seq& q, i
   // fit.  Returns the first token that is left.
   auto attend = [&](auto in_half, int from) __attribute__((always_inline)) {
   constexpr bool HALF = decltype(in_half)::value;
-  constexpr int NQ = HALF ? 1 : q_pieces<DT>(), NP = HALF ? 1 : w_pieces<DT>();
+  constexpr int NQ = HALF ? 1 : q_pieces<DT>(), NP = HALF ? (TREE && DT == KDA_F16 ? 2 : 1) : w_pieces<DT>();
   // 16-bit types in bf16 keep two pieces of weights (fp16: of queries too), and
   // have no registers for a second tile's scores
   constexpr bool PIPED = HALF || DT == KDA_F32;
@@ -1453,11 +1457,18 @@ __device__ __forceinline__ void tile_rows(const KvAttendArgs& a, const Seq& q, i
         const float w0 = exp2_hw(fmaf(sc[b][e], scale, base)), w1 = exp2_hw(fmaf(sc[b][e + 1], scale, base));
         uint32_t x[NP];
         if constexpr (HALF) {
-          // the sum takes the weights as they are multiplied: what their
-          // rounding has in common falls out of the quotient
           const h2 w = {static_cast<_Float16>(w0), static_cast<_Float16>(w1)};
-          sum = __builtin_amdgcn_fdot2(w, h2{1, 1}, sum, false);
           x[0] = __builtin_bit_cast(uint32_t, w);
+          if constexpr (NP == 1) {
+            // the sum takes the weights as they are multiplied: what their
+            // rounding has in common falls out of the quotient
+            sum = __builtin_amdgcn_fdot2(w, h2{1, 1}, sum, false);
+          } else {
+            sum += w0 + w1;
+            const h2 rest = {static_cast<_Float16>(w0 - static_cast<float>(w[0])),
+                             static_cast<_Float16>(w1 - static_cast<float>(w[1]))};
+            x[1] = __builtin_bit_cast(uint32_t, rest);
+          }
         } else {
           sum += w0 + w1;
           split_weights<NP>(w0, w1, x);

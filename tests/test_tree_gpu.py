@@ -290,6 +290,35 @@ def test_exponents_outside_fp16_in_a_large_tree(dtype, past):
     c.check(c.attend())
 
 
+@pytest.mark.parametrize("D,heads", [(64, (8, 1)), (128, (16, 2))])
+@pytest.mark.parametrize("past", [60, 250])
+def test_weights_of_large_fp16_trees_keep_their_bits(D, heads, past):
+    # Two scores, 0 and -x scale, whose values are 1 and -1: an output is (a - n w) / (a + n w)
+    # for w = exp(-x scale), off by up to half of what w is, 2^-12 were it held in 11
+    # bits.  A score is one exact product, rounded twice (scale is a power of two at
+    # D = 64): w is off by less than 2^-20 of itself (x scale < 1), in two fp16 pieces by 2^-22
+    # more, and the sums as everywhere.
+    c = TreeCase([chain(10), some_tree(12, 1)], [past, past // 2], dtype="f16", heads=heads, D=D, P=64, seed=D + past)
+    for s in range(2):
+        n = c.past[s] + c.rows[s]
+        k, v = np.zeros((n, c.h, D)), np.ones((n, c.h, D))
+        less = np.arange(n) % 5 < 3
+        k[less, :, 0], v[less] = -1, -1
+        O.append(c.pool, c.table[s], 0, k, v)
+    c.d_pool = dev(c.pool)
+    c.q = torch.zeros(c.T, c.hq, D, dtype=torch.float16)
+    c.q[:, :, 0] = torch.linspace(0.3, 0.69, c.T * c.hq).view(c.T, c.hq) * D ** 0.5
+    c.hq_np, c.q = host(c.q), c.q.cuda()
+    got = host(c.attend())
+    for s in range(2):
+        a, b, n = c.cu[s], c.cu[s + 1], c.past[s] + c.rows[s]
+        k, v = O.read(c.pool, c.table[s], 0, n)
+        want, _, top = T.attend(k, v, c.hq_np[a:b], c.past[s], c.trees[s], D ** -0.5)
+        assert np.abs(want).max() < 0.25 and (top == 1).all()
+        tol = 2.0 ** -20 + 2.0 ** -22 + 2 * (n + 64) * 2.0 ** -24 + HALF_STEP["f16"] * np.abs(want)
+        assert (np.abs(got[a:b] - want) <= tol).all(), (s, (np.abs(got[a:b] - want) / tol).max())
+
+
 def test_large_trees_in_place_with_strides_and_bad_sequences():
     c = TreeCase([some_tree(60, 1), some_tree(40, 2), some_tree(3, 3)], [900, 0, 5], heads=(8, 2), D=64, P=64, dtype="bf16",
                  seed=3).fill()
