@@ -673,6 +673,9 @@ int kda_kv_validate(const kda_kv_pool* kv, const int32_t* page_table_host, int32
  *   kda_verify_drafts                      once, on the target's probabilities
  *   kda_kv_keep, kda_decode_path           the accepted path enters the caches
  *                                          and the states
+ * A short convolution in front of a KDA layer is the caller's: a node's window
+ * holds its path's inputs, and the accepted path's go into the history.
+ * (kda_decode_step_conv has both for chains.)
  *
  * The tables (device int32):
  *  cu_seqlens  [n_req + 1], non-decreasing: request r owns nodes

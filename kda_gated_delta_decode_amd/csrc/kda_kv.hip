@@ -1070,6 +1070,15 @@ struct ExpRange {
   }
 };
 
+// Trees: where a part of 128 rows keeps channels 8 k.. of row r: as the lanes hold them,
+// so that a wave writes 1 KiB in a row.  The next four channels are 256 numbers on.
+template <int D>
+__device__ __forceinline__ int tile_piece(int r, int k) {
+  constexpr int VC = D / 16;  // neighbouring channels of a lane, D / VC runs of them in 8 elements of two halves
+  const int run = 8 * k / VC, e = 4 * (run / 8) + run % 4, half = run / 4 % 2;
+  return ((r / 32 * (D / 8) + e * (VC / 4)) * 64 + 32 * half + r % 32) * 4;
+}
+
 // Many rows: 128 rows of one sequence and cached head (32 a wave) against one
 // split of its tokens, 64 of them at a time.
 //
@@ -1111,15 +1120,7 @@ struct ExpRange {
 // rows of 32 query heads 536 us, 1026 TFLOP/s of the 1211 that a large bf16 matrix
 // product reaches (829 us with two bf16 pieces for a weight, one tile after the
 // other).
-// TREE: where a part of 128 rows keeps channels 8 k.. of row r: as the lanes hold them,
-// so that a wave writes 1 KiB in a row.  The next four channels are 256 numbers on.
-template <int D>
-__device__ __forceinline__ int tile_piece(int r, int k) {
-  constexpr int VC = D / 16;  // neighbouring channels of a lane, D / VC runs of them in 8 elements of two halves
-  const int run = 8 * k / VC, e = 4 * (run / 8) + run % 4, half = run / 4 % 2;
-  return ((r / 32 * (D / 8) + e * (VC / 4)) * 64 + 32 * half + r % 32) * 4;
-}
-
+//
 // One tile's rows against the tokens [t0, t1).  splits > 1: the rows' sums go to the
 // workspace, as split sp, or TREE, to the 128 rows `place` of it.  TREE otherwise as in
 // the rows kernel.
@@ -1717,18 +1718,20 @@ __device__ __forceinline__ int wave_scan(int x) {
 }
 
 // Trees' tiles are cut in parts of at most `each` steps, every tile of a sequence
-// alike, such that there are as many parts as places (`a.n_splits`): each = about
-// (all steps) / (places), however lengths and sizes differ.  (16 trees of up to 32
+// alike, such that there are as many parts as places (`a.n_splits`) at most: each =
+// about (all steps) / (places), however lengths and sizes differ.  (16 trees of up to 32
 // nodes on up to 8191 tokens, 32 / 8 heads, bf16: 61 us with the join, 95 with splits
-// of one length, chosen for the longest sequence.)  Long caches take 970 TFLOP/s more
-// with every token, nine tenths of what a large matrix product reaches; the 61 us hold
-// 25 that do not grow with them: launches, the plan, tables and first tiles (9 of 51 us
-// of a workgroup), parts out and in again (34 MB each way).
+// of one length, chosen for the longest sequence; 25 of 32 nodes on 400 tokens 30.)  Long
+// caches take 970 TFLOP/s more with every token, nine tenths of what a large matrix
+// product reaches, but a tile multiplies 128 rows however few its sequence has: 1.48
+// times the work that counts, for these 16 trees.  25 of the 61 us do not grow with the
+// tokens: launches, the plan, tables and first tiles (9 of 51 us of a workgroup), parts
+// out and in again (34 MB each way).
 template <int DT, int D>
 __global__ __launch_bounds__(256, DT == KDA_F32 ? 1 : 2) void kda_kv_tree_tiles_kernel(KvAttendArgs a) {
   const int lane = threadIdx.x % 64;
   const bool one = a.t.n_seq <= 64;  // all sequences in the wave's lanes
-  TreeCost c{0, 1, false};
+  TreeCost c{0, 1, 0, 0, 0, false};
   float steps = 0.0f, units = 0.0f;
   for (int s0 = 0; s0 < a.t.n_seq && (one || a.n_splits > 0); s0 += 64) {
     c = tree_cost<int32_t>(a, s0 + lane);

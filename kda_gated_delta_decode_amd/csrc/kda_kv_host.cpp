@@ -122,9 +122,10 @@ KvTreePlan kv_tree_plan(const kda_kv_pool* kv, int32_t n_seq, int32_t max_rows, 
   // (a block for every tile of any tree: sizes are hints)
   const int64_t all = static_cast<int64_t>(n_seq) * ((static_cast<int64_t>(KDA_MAX_NODES) * group + 127) / 128) * kv->H;
   p.blocks = p.places > all ? p.places : all;
-  // Threads side by side along parts pay from 16 parts a tile (2 trees of 64 nodes on
-  // 60000 tokens, 16 / 2 heads of 64: 45.5 us, 48.9 one after the other; of 6 and 11
-  // parts 45.2 -> 41.8 and 54.7 -> 52.2 without).
+  // Threads side by side along parts pay from 16 parts a tile (fp16, 16 / 2 heads of 64: 2
+  // trees of up to 64 nodes on up to 60000 tokens, of 32 parts, 52.5 us, 55.6 one after
+  // the other; 6 of 64 nodes on 20000 and 10 on 12000, of 10 and 6 parts, 77.5 and 79.3,
+  // 75.4 and 75.2 without).
   p.many = p.places > 16 * units;
   p.join_blocks = cut ? units * (128 / 16) : 0;
   return p;

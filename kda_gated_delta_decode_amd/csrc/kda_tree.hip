@@ -141,9 +141,11 @@ constexpr int tree_lds_bytes(int nb) { return tree_rows_bytes(nb) + 9 * first_pa
 // head's columns, and half its waves the keys' products, half the queries'.
 // Bound by its phases, each of which waits for the one before it (loads, the pairs up
 // the tree, products, the solve level by level): two workgroups a compute unit run
-// them beside each other.  64 ragged trees of up to 48 nodes, 12 heads, fp16 states:
-// 27.2 us, 72 MB, 2.7 TB/s of the 4.8 a large copy reaches (one node after the other: 87
-// us); 13 nodes, fp32: 7.5.
+// them beside each other, up to 48 nodes (with more, 89 KB of LDS leave room for one: 64
+// trees of 48 nodes 39 us, of 56 57).  The state comes in 32-byte pieces of fp16, 64 of
+// fp32, in front of the rest.  64 ragged trees of up to 48 nodes, 12 heads, fp16 states: 30.9
+// us, 72 MB, 2.3 TB/s of the 6.5 that a streaming copy reaches (26.8 with all of it in the
+// caches; 87 one node after the other); fp32 states 43.9; one tree of 13 nodes, fp32, 7.8.
 template <int DT, int PER, int COLS>
 __global__ __launch_bounds__(kTreeThreads, 4) void kda_tree_kernel(TreeArgs a, int nb) {
   constexpr int GROUPS = kTreeThreads / 16;
@@ -432,8 +434,10 @@ __global__ __launch_bounds__(kTreeThreads, 4) void kda_tree_kernel(TreeArgs a, i
 // A workgroup for a request and head: 32 value columns a wave, 16 bytes of them
 // and R key rows a lane, so that a node's column sums stay inside the wave and the
 // nodes follow each other without a barrier.  The nodes' keys, decays and values
-// are staged sixteen at a time.  Bound by HBM for a batch (64 paths of up to 8 nodes, 12
-// heads, fp16: 15.7 us, 3.4 TB/s, reading and writing), by latency for one (5.1).
+// are staged sixteen at a time.  A batch is bound by its one round of workgroups, which
+// load, compute and store in step (64 paths of up to 8 nodes, 12 heads, fp16: 15.7 us, 3.4
+// TB/s, reading and writing; kda_decode_step moves these states in 9.4), one path by
+// latency (5.1).
 // Nodes eight at a time, states updated by matrix products: 41 -> 36 us for up to 20
 // nodes of fp16 states, but fp32 47 -> 59 and 8 nodes no faster; not taken.
 template <int DT>
