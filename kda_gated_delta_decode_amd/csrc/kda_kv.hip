@@ -1011,7 +1011,11 @@ __global__ __launch_bounds__(256) void kda_kv_keep_kernel(KvKeepArgs a) {
     } else if (li == 9) {
       exps = static_cast<Exps>(kKvMinExp * 0x01010101u);
     }
-    // (every lane's load above is waited for before the first store below)
+    // One lane's token is another's place: every load above is waited for before the
+    // first store below, and the compiler keeps that order between lanes too.
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     if (dst != nullptr) {
       if (li < 8) *reinterpret_cast<Codes*>(dst + part + rb * (D / 2)) = codes;
       if (li == 8) *reinterpret_cast<Exps*>(dst + kv_key_exps(a.t.P, D) + rb * kExps) = exps;

@@ -461,6 +461,23 @@ def test_keep_with_missing_pages():
     assert np.array_equal(got, same)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_keep_reads_a_token_before_its_place_is_poisoned(D):
+    # four tokens move at once: the fourth has no page, and its place is the first one's token
+    c = K.Case([40], [0], heads=(3, 3), D=D, P=16, seed=D)
+    c.table[0, 1] = -1  # nodes 16..31
+    c.d_table = dev(c.table)
+    got = keep(c, [[3, 4, 5, 20, 33]])
+    page, other = c.table[0, 0], c.table[0, 2]
+    for h in range(c.h):
+        new, old = O.Block(got[page, h]), O.Block(c.pool[page, h])
+        for e, i in enumerate((3, 4, 5)):
+            assert np.array_equal(new.load(e), old.load(i), equal_nan=True)
+        k, v = new.load(3)
+        assert np.isnan(k).all() and (v == 0).all()
+        assert np.array_equal(new.load(4), O.Block(c.pool[other, h]).load(1), equal_nan=True)
+
+
 # --------------------------------------------------------------------------
 # the recurrence
 # --------------------------------------------------------------------------
